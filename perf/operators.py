@@ -233,7 +233,7 @@ def _run_own(s):
         return bw.attn_tree(s["q"], s["k"], s["v"], s["k_new"], s["v_new"], s["nk"], s["cu"], s["mask"], s["nodes"],
                             workspace=s["ws"], out=s["o"], lse=s["lse"])
     if s["op"] == "mask":
-        return bw.tree_mask(s["parents"], s["cu"], s["nodes"], nk=s["nk"])
+        return bw.attn_tree_mask(s["parents"], s["cu"], s["nodes"], nk=s["nk"])
     if s["op"] == "plan":
         got = bw.kv_plan_paged(s["nk"], s["new"], s["table"], s["held"], s["free"], s["count"], s["page"], s["tokens"])
         return (s["table"],) + tuple(got)
