@@ -193,6 +193,12 @@ int varlen_splits(int max_seqlen_k) {
 namespace bw {
 void record_cuda_error(cudaError_t e) { t_last_cuda_error = static_cast<int>(e); }
 void count_launch() { g_launches.fetch_add(1); }
+cudaError_t make_map_bf16(CUtensorMap* m, const void* base, int d, int64_t dim1, int64_t dim2, int64_t stride1_elems,
+                          int64_t stride2_elems, int box1, int box2) {
+  return make_map(m, base, d, dim1, dim2, stride1_elems, stride2_elems, box1, box2);
+}
+cudaError_t status_word(unsigned int** out) { return status_ptr(out); }
+uint64_t wait_timeout_ns() { return g_timeout_ns.load(); }
 
 cudaError_t merge_tickets(int n, unsigned int** out) {
   *out = nullptr;

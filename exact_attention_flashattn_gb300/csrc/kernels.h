@@ -132,6 +132,75 @@ cudaError_t launch_prefill_tc(const TcFwdArgs& a, unsigned int* status, unsigned
 // or tokens high), a.max_pairs = query tiles per (sequence, head).
 cudaError_t launch_prefill_tc256(const TcFwdArgs& a, unsigned int* status, unsigned int* sched, cudaStream_t stream);
 
+// ---- attention of drafted token trees over a cache ----
+struct TreeArgs {
+  const uint16_t* q;      // bf16 bits; node t of the packed batch at q + t * q_stride, heads d apart
+  const uint16_t* k;      // cache: contiguous [B, Hkv, cap, d] or pages [num_pages, page_size, Hkv, d]
+  const uint16_t* v;
+  const uint16_t* k_new;  // drafted rows, node t at k_new + t * k_new_stride, KV heads d apart
+  const uint16_t* v_new;
+  uint16_t* o;            // [total_q, Hq, d]
+  float* lse;             // [total_q, Hq] or null
+  const int32_t* nk;      // [num_seqs] context keys (clamped to kv_cap)
+  const int32_t* cu_q;    // [num_seqs + 1] (clamped to total_q)
+  const uint64_t* mask;   // [total_q, mask_words]: bit j = draft j of the node's own sequence is seen
+  const int32_t* block_table;  // paged cache when non-null: [num_seqs, max_pages]
+  int64_t q_stride, k_new_stride, v_new_stride;
+  int num_seqs, total_q, max_nodes, mask_words;
+  int Hq, Hkv, g, d;
+  int kv_cap;             // keys a sequence's cache can hold
+  int page_size, max_pages, num_pages;
+  float scale_log2;
+};
+constexpr int kTreeMaxNodes = 1024;  // drafted nodes a sequence
+constexpr int kTreeRows = 128;       // rows of a tile: (node, query head) pairs of whole nodes
+// Bytes of workspace of a tree call (a multiple of 256).
+size_t tree_ws_bytes(int num_seqs, int max_nodes, int g, int d);
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
+
+// ---- paged cache bookkeeping ----
+struct TreeMaskArgs {
+  const int32_t* parents;
+  const int32_t* cu_q;
+  const int32_t* nk;  // or null
+  uint64_t* mask;
+  int32_t* positions;  // or null
+  int num_seqs, total_q, max_nodes, words;
+};
+cudaError_t launch_tree_mask(const TreeMaskArgs& a, cudaStream_t stream);
+
+struct PlanArgs {
+  const int32_t* nk;
+  const int32_t* n_new;
+  int32_t* table;
+  const int32_t* held;
+  const int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* nk_out;
+  int32_t* held_out;
+  int32_t* cu;
+  int32_t* slots;
+  int32_t* free_out;
+  int B, page_size, max_pages, free_cap, num_tokens;
+};
+cudaError_t launch_kv_plan(const PlanArgs& a, cudaStream_t stream);
+
+struct AppendArgs {
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  const int32_t* slots;
+  const int32_t* rows;  // or null: slot i takes row i
+  void* k_pages;
+  void* v_pages;
+  const float* k_scale;  // non-null: E4M3 pages
+  const float* v_scale;
+  int64_t k_stride, v_stride;  // elements between rows of k_new / v_new
+  int num_slots, num_rows;     // num_rows: rows of k_new and v_new
+  int64_t pool_rows;           // num_pages * page_size
+  int row_elems;               // Hkv * d
+};
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
+
 // Timeout self-test: one CTA waits on a barrier that is never arrived at.
 cudaError_t launch_wait_timeout_probe(uint64_t timeout_ns, unsigned int* status, cudaStream_t stream);
 
@@ -142,6 +211,13 @@ void count_launch();
 // `n` zeroed merge tickets on the current device for one launch of the split-K kernel (null
 // when the request exceeds the ticket pool: the caller then launches the merge kernel).
 cudaError_t merge_tickets(int n, unsigned int** out);
+// 3-D bf16 tensor map {d, dim1, dim2} with strides in elements, box {64, box1, box2}, 128-byte
+// swizzle, zero fill out of bounds.
+cudaError_t make_map_bf16(CUtensorMap* m, const void* base, int d, int64_t dim1, int64_t dim2, int64_t stride1_elems,
+                          int64_t stride2_elems, int box1, int box2);
+// The device status word of the current device and the bound on a kernel's waits.
+cudaError_t status_word(unsigned int** out);
+uint64_t wait_timeout_ns();
 
 // Float offset of the o[] block of the split-K workspace (after the (m, l) pairs, 256-byte aligned).
 inline size_t splitk_o_offset(int units, int num_splits, int rows_max) {

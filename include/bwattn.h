@@ -19,7 +19,8 @@
  *
  * Conventions shared by every call:
  *   - Every tensor pointer is a DEVICE pointer owned by the caller, contiguous in the layout
- *     given, 16-byte aligned (attn_fwd_host alone takes host pointers). The library never
+ *     given (calls with stride arguments: in those strides), 16-byte aligned (int32 arrays and lse:
+ *     their own size; attn_fwd_host alone takes host pointers). The library never
  *     allocates or frees memory and never synchronises the host.
  *   - Every call is asynchronous on `stream` (a cudaStream_t passed as void*; NULL = the
  *     legacy default stream) and returns a status code. Argument checks happen on the host
@@ -275,6 +276,131 @@ int attn_varlen_window(const void* q, const void* k, const void* v, void* o, flo
                        const int32_t* cu_seqlens_k, int num_seqs, int total_q, int total_k, int max_seqlen_q,
                        int max_seqlen_k, int Hq, int Hkv, int d, int window, float scale, void* workspace,
                        size_t workspace_bytes, void* stream);
+
+/* ---- speculative decoding over a cache: drafted token trees, paged plans and appends ---- */
+
+/*
+ * attn_tree_workspace_size: bytes of workspace attn_tree / attn_tree_paged need, from the
+ * host-side bounds they are given (0 for sizes they refuse).
+ */
+size_t attn_tree_workspace_size(int num_seqs, int max_nodes, int Hq, int Hkv, int d);
+
+/*
+ * attn_tree / attn_tree_paged: verification of drafted token trees. The queries of a sequence are
+ * the nodes of its tree; each sees every context key of the sequence's cache and those drafted
+ * tokens of its own sequence that its mask names (its ancestors and itself, for a tree), whose
+ * keys and values are read from the packed k_new, v_new and need not be in the cache. (The pages'
+ * append class, "Attention Computation in Practice", section 5, kernel class 3, covers drafts that
+ * form one line; the mask takes the place of its causal rule.)
+ *
+ *   q, o         : [total_q, Hq, d] bf16, sequence s owns nodes cu_seqlens_q[s] .. cu_seqlens_q[s+1]-1;
+ *                  consecutive nodes of q lie q_stride elements apart (heads d apart; o is contiguous)
+ *   k_new, v_new : [total_q, Hkv, d] bf16, the nodes' own keys and values, consecutive nodes
+ *                  k_new_stride / v_new_stride elements apart (slices of a fused projection's rows)
+ *   kcache, vcache / k_pages, v_pages, block_table : the cache in the layouts of attn_decode /
+ *                  attn_decode_paged (kcache, vcache may be NULL when nk_cap is 0)
+ *   nk           : [num_seqs] int32 DEVICE array, context keys per sequence, 0 <= nk[s] <= nk_cap (or
+ *                  max_pages_per_seq * page_size); all of them are visible to every node
+ *   cu_seqlens_q : [num_seqs + 1] int32 DEVICE array, non-decreasing, [0] = 0; rows of q behind
+ *                  cu_seqlens_q[num_seqs] belong to no sequence, their o and lse are left as they were
+ *   mask         : [total_q, ceil(max_nodes / 64)] uint64 DEVICE array: bit j % 64 of word j / 64 of a
+ *                  node's row is set iff the node sees draft j of its sequence; bits at or past the
+ *                  sequence's node count are ignored. A node that sees no key gets O = 0, LSE = -inf
+ *   total_q      : host-side row count of the packed tensors
+ *   max_nodes    : host-side upper bound of the nodes of a sequence, at most 1024; a longer
+ *                  sequence's further nodes are neither read nor written
+ *   lse          : [total_q, Hq] fp32, may be NULL
+ *   workspace    : at least attn_tree_workspace_size(...) bytes; contents undefined on exit. Must not
+ *                  be shared by calls that may overlap on the GPU
+ * Keys and values that a node does not see (context rows at or past nk, drafts its mask leaves out)
+ * have no effect on its outputs, whatever they hold (infinities and NaN included). Supported: d in
+ * {64, 128, 256}, Hq / Hkv <= 128, max_nodes <= 1024. Strides are multiples of 8 and at least
+ * Hq * d (q) or Hkv * d (k_new, v_new), else INVALID_ARG; other errors as for attn_decode.
+ */
+int attn_tree(const void* q, const void* kcache, const void* vcache, const void* k_new, const void* v_new, void* o,
+              float* lse, const int32_t* nk, const int32_t* cu_seqlens_q, const uint64_t* mask, int num_seqs,
+              int total_q, int max_nodes, int nk_cap, int Hq, int Hkv, int d, int64_t q_stride, int64_t k_new_stride,
+              int64_t v_new_stride, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+int attn_tree_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* block_table,
+                    const void* k_new, const void* v_new, void* o, float* lse, const int32_t* nk,
+                    const int32_t* cu_seqlens_q, const uint64_t* mask, int num_seqs, int total_q, int max_nodes,
+                    int page_size, int num_pages, int max_pages_per_seq, int Hq, int Hkv, int d, int64_t q_stride,
+                    int64_t k_new_stride, int64_t v_new_stride, float scale, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/*
+ * attn_tree_mask: the masks and positions of drafted trees from their parent links.
+ *
+ *   parents      : [total_q] int32, the parent of node i of a sequence as an index within the sequence;
+ *                  parents come before their children: a value outside [0, i) makes node i a root
+ *   cu_seqlens_q : as for attn_tree
+ *   nk           : [num_seqs] int32 context keys, or NULL (0 for every sequence)
+ *   mask         : [total_q, ceil(max_nodes / 64)] uint64, written: bit j of node i's row is set iff j
+ *                  is i or an ancestor of i
+ *   positions    : [total_q] int32, written unless NULL: nk[s] + depth of the node (0 for a root)
+ * Rows that belong to no sequence, and nodes past a sequence's first max_nodes, are left as they were.
+ */
+int attn_tree_mask(const int32_t* parents, const int32_t* cu_seqlens_q, const int32_t* nk, uint64_t* mask,
+                   int32_t* positions, int num_seqs, int total_q, int max_nodes, void* stream);
+
+/*
+ * kv_plan_paged: room in a paged cache for n_new[b] further tokens of each request b: pages from a
+ * stack of free ones, the block table extended by them, and the slot of every new token. ("Attention
+ * Computation in Practice", "PagedAttention's kernel difference": the block table that the paged
+ * kernels read.) All arrays are int32 DEVICE arrays.
+ *
+ *   nk, n_new   : [B] keys that request b has in the cache, and tokens to make room for (negative: 0)
+ *   held        : [B] pages that request b holds: block_table[b][0 .. held[b]-1]. It may hold more
+ *                 than its keys fill (room left by drafts that were not accepted)
+ *   free_pages,
+ *   free_count  : [free_capacity], [1]: a stack of free pages; the last of the first *free_count is taken first
+ *   block_table : [B, max_pages_per_seq], extended in place: with need_b = max(0, min(ceil((nk + n_new) /
+ *                 page_size), max_pages_per_seq) - held), request b's entries held .. held + need_b - 1
+ *                 become the next need_b pages of the stack, request after request. Other entries stay
+ *   nk_out, held_out : [B] nk + n_new; held + need_b
+ *   cu_seqlens  : [B + 1] exclusive prefix sums of n_new (the total last)
+ *   slots       : [num_tokens] slot of the j-th new token of request b at cu_seqlens[b] + j: page *
+ *                 page_size + row of position nk[b] + j. -1 behind the last token and where there is no
+ *                 page: the stack ran out, or the position is past max_pages_per_seq pages
+ *   free_count_out : [1] *free_count less the pages taken; negative by how many the stack was short,
+ *                 whose table entries are -1: nothing of the plan may then be used, release pages and
+ *                 plan again
+ * The outputs must not overlap the inputs (equal pointers: INVALID_ARG). page_size is a multiple of 16,
+ * 16..1024. The call may be repeated on the same inputs with the same results.
+ */
+int kv_plan_paged(const int32_t* nk, const int32_t* n_new, int32_t* block_table, const int32_t* held,
+                  const int32_t* free_pages, const int32_t* free_count, int32_t* nk_out, int32_t* held_out,
+                  int32_t* cu_seqlens, int32_t* slots, int32_t* free_count_out, int B, int page_size,
+                  int max_pages_per_seq, int free_capacity, int num_tokens, void* stream);
+
+/*
+ * kv_append_paged / kv_append_paged_fp8: new K and V rows written into the pages at given slots.
+ *
+ *   k_new, v_new : [num_rows, Hkv, d] bf16, consecutive rows k_new_stride / v_new_stride elements apart
+ *   slots        : [num_slots] int32 DEVICE array, the pool row (page * page_size + row of the page)
+ *                  that slot i writes; values outside [0, num_pages * page_size) are skipped
+ *   rows         : [num_slots] int32 DEVICE array, the row of k_new and v_new that slot i takes (the
+ *                  accepted nodes of a verified tree); values outside [0, num_rows) are skipped. NULL:
+ *                  slot i takes row i (num_slots <= num_rows)
+ *   k_pages,
+ *   v_pages      : [num_pages, page_size, Hkv, d]: bf16 for kv_append_paged; one E4M3 code per
+ *                  element for kv_append_paged_fp8, the layout of attn_decode_paged_fp8
+ *   k_scale,
+ *   v_scale      : [Hkv, d] fp32 DEVICE arrays, 16-byte aligned, positive and normal: the code of a value x is the
+ *                  E4M3 code nearest to x / scale (ties to the even code; magnitudes past 448, infinities
+ *                  among them, become +-448; NaN stays NaN)
+ * Slots must differ from one another: of two slots with one value, which row stays is not defined (and
+ * may differ within the row). Supported: d in {64, 128, 256}. num_slots = 0 or num_rows = 0 is a no-op.
+ */
+int kv_append_paged(const void* k_new, const void* v_new, const int32_t* slots, const int32_t* rows, void* k_pages,
+                    void* v_pages, int num_slots, int num_rows, int page_size, int num_pages, int Hkv, int d,
+                    int64_t k_new_stride, int64_t v_new_stride, void* stream);
+
+int kv_append_paged_fp8(const void* k_new, const void* v_new, const int32_t* slots, const int32_t* rows,
+                        void* k_pages, void* v_pages, const float* k_scale, const float* v_scale, int num_slots,
+                        int num_rows, int page_size, int num_pages, int Hkv, int d, int64_t k_new_stride,
+                        int64_t v_new_stride, void* stream);
 
 /* ---- status and diagnostics ---- */
 
