@@ -77,9 +77,7 @@ int tree_impl(const void* q, const void* k, const void* v, const void* k_new, co
   a.max_pages = max_pages;
   a.num_pages = num_pages;
   a.scale_log2 = scale * bw::kLog2e;
-  cudaError_t e = bw::launch_tree(a, static_cast<cudaStream_t>(stream));
-  if (e == cudaSuccess) bw::count_launch();
-  return done(e);
+  return done(bw::launch_tree(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 int append_impl(const void* k_new, const void* v_new, const int32_t* slots, const int32_t* rows, void* k_pages,

@@ -133,7 +133,16 @@ cudaError_t launch_prefill_tc(const TcFwdArgs& a, unsigned int* status, unsigned
 cudaError_t launch_prefill_tc256(const TcFwdArgs& a, unsigned int* status, unsigned int* sched, cudaStream_t stream);
 
 // ---- attention of drafted token trees over a cache ----
+// A tile is kTreeRows rows, a row being one (node, query head) pair of the KV head's group; a tile
+// holds kTreeRows / g whole nodes, a unit one or two tiles (tree_row_tiles) of one KV head.
+constexpr int kTreeMaxNodes = 1024;  // drafted nodes a sequence
+constexpr int kTreeRows = 128;
+constexpr int kTreeMaxCtas = 152;    // persistent CTAs, at most one per SM
 struct TreeArgs {
+  CUtensorMap tm_q;        // {d, Hq, total_q}, box {64, g, kTreeRows / g}
+  CUtensorMap tm_k, tm_v;  // contiguous {d, cap, B * Hkv}, box {64, tile keys, 1}; paged {d, Hkv, pool rows},
+                           // box {64, 1, piece}
+  CUtensorMap tm_kn, tm_vn;  // {d, Hkv, total_q}, box {64, 1, new_box}
   const uint16_t* q;      // bf16 bits; node t of the packed batch at q + t * q_stride, heads d apart
   const uint16_t* k;      // cache: contiguous [B, Hkv, cap, d] or pages [num_pages, page_size, Hkv, d]
   const uint16_t* v;
@@ -146,17 +155,29 @@ struct TreeArgs {
   const uint64_t* mask;   // [total_q, mask_words]: bit j = draft j of the node's own sequence is seen
   const int32_t* block_table;  // paged cache when non-null: [num_seqs, max_pages]
   int64_t q_stride, k_new_stride, v_new_stride;
+  int64_t* base;          // workspace: [num_seqs + 1] tiles before each sequence, and in all
+  float* partial;         // workspace: [ctas][2][row tiles][kTreeRows * (d + 2)]
   int num_seqs, total_q, max_nodes, mask_words;
   int Hq, Hkv, g, d;
   int kv_cap;             // keys a sequence's cache can hold
   int page_size, max_pages, num_pages;
+  int piece;              // paged: rows of a copy, a power of two that divides page_size
+  int new_box;            // rows of a copy of drafted rows
+  int ctas;               // CTAs of the attention kernel
   float scale_log2;
+  unsigned int* status;
+  uint64_t timeout_ns;
 };
-constexpr int kTreeMaxNodes = 1024;  // drafted nodes a sequence
-constexpr int kTreeRows = 128;       // rows of a tile: (node, query head) pairs of whole nodes
-// Bytes of workspace of a tree call (a multiple of 256).
-size_t tree_ws_bytes(int num_seqs, int max_nodes, int g, int d);
-cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
+// Row tiles of a unit: two (d <= 128) when a sequence may fill more than one, so that the K and V
+// tiles of a unit serve twice the rows.
+inline int tree_row_tiles(int max_nodes, int g, int d) { return d <= 128 && max_nodes > kTreeRows / g ? 2 : 1; }
+inline size_t tree_base_bytes(int num_seqs) { return (static_cast<size_t>(num_seqs) * 8 + 8 + 255) / 256 * 256; }
+inline size_t tree_ws_bytes(int num_seqs, int max_nodes, int g, int d) {
+  return tree_base_bytes(num_seqs) +
+         static_cast<size_t>(kTreeMaxCtas) * 2 * tree_row_tiles(max_nodes, g, d) * kTreeRows * (d + 2) * sizeof(float);
+}
+// Fills the maps and sizes that follow from the others, launches the attention and the merge.
+cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream);
 
 // ---- paged cache bookkeeping ----
 struct TreeMaskArgs {

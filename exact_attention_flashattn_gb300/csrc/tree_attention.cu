@@ -1,8 +1,40 @@
 // Attention of a tree of drafted tokens over a KV cache: node i of sequence b sees every one of the
 // sequence's nk context keys in the cache and the drafts j whose bit is set in its mask,
 //   O = sum_j e^(s_j - m) v_j / l,  l = sum_j e^(s_j - m),  s_j = scale q.k_j,  LSE = m + ln l,
-// in one pass over the keys with a running maximum m and sum l. A node that sees no key gets O = 0
-// and LSE = -inf.
+// in one pass over the keys with a running maximum m and sum l (the recurrence of the prefill
+// kernels). A node that sees no key gets O = 0 and LSE = -inf.
+//
+// What bounds it: the cache is read once, 4 d bytes per key and KV head, and every key costs 4 d
+// operations per row, a row being one (node, query head) pair of the KV head's group. 128 rows are
+// far on the memory side of this card (128 keys x 128 rows take about 0.35 us of one SM's tensor
+// pipe, their K and V 1.5 us of its share of HBM), 256 rows about level with it. So a tile holds 128
+// rows (whole nodes: kTreeRows / g of them, which the Q copy's box {64, g, nodes} lays out without a
+// gather), and a unit of work is one row tile of one KV head, or two (kTiles == 2) when a sequence
+// may have more than 128 rows, so that a cache byte serves up to 256.
+//
+// Split: lengths are on the device, and one long sequence has to fill the GPU as well as many short
+// ones. The key tiles of all units form one list (unit after unit, context tiles, then drafts), and
+// CTA c of G takes tiles [c T / G, (c + 1) T / G): no CTA has more than one tile above another,
+// whatever the lengths. A unit that lies within one CTA's range is finished there; otherwise each
+// CTA that has a part of it writes its (m, l, o), at most two such parts per CTA, and a second,
+// dependent launch merges them in the order of the keys (no atomics: results do not depend on which
+// CTA ends first).
+//
+// Inside a CTA two streams run, each with its own S and O in tensor memory, its own MMA issuing warp
+// and its own softmax warpgroup (thread = row = TMEM lane):
+//   kTiles == 2   stream w is row tile w; both read the same K and V tiles.
+//   kTiles == 1   both streams have the same rows; the even key tiles go to stream 0, the odd ones to
+//                 stream 1, whose o is added to stream 0's through shared memory at the unit's end.
+//   d == 256      (O alone takes half of tensor memory) one stream of 64-key tiles, two S buffers.
+// A stream's S -> softmax -> P.V is a serial chain per tile; two of them, out of step, cover it. A
+// producer warp streams K and V tiles (TMA, 128-byte swizzle; from a paged cache one copy per run of
+// rows inside a page, a lane each) through a ring of shared-memory slots that runs on across units.
+// The tail tile of the context and the tiles of drafts may hold rows that do not count (keys past
+// the end, other sequences' drafts) and values that some rows must not see; 0 * NaN would still
+// reach O, so the issuing warp zeroes such V rows, and infinities and NaN in V rows of drafts, in
+// shared memory before the P.V of the tile; rows that do see those get them back at the end.
+// Every wait is bounded; a timed-out wait sets the device status word, the CTA stops producing
+// output, waits for its own copies and MMAs and frees its TMEM.
 #include <math.h>
 
 #include "kernels.h"
@@ -12,89 +44,862 @@ namespace bw {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: o is rescaled when the max grew by more than 2^8
+constexpr int kSegSlots = 4;
+constexpr int kBarBytes = 1024;
 
-__device__ __forceinline__ float bf16_f32(uint32_t bits) { return __uint_as_float(bits << 16); }
+template <int D, int kTiles>
+struct Cfg {
+  static constexpr int kStreams = D == 256 ? 1 : 2;
+  static constexpr int kKeys = D == 256 ? 64 : 128;  // keys per tile
+  static constexpr int kHalves = D / 64;             // 128-byte swizzle atoms across the head dim
+  static constexpr uint32_t kQBytes = kTreeRows * D * 2;
+  static constexpr uint32_t kTileBytes = kKeys * D * 2;
+  static constexpr int kStages = D == 64 ? 8 : 4;  // even: V tiles always land in odd slots
+  static constexpr bool kExchange = kTiles == 1 && kStreams == 2;
+  static constexpr uint32_t kRing = kTiles * kQBytes;
+  static constexpr uint32_t kXch = kRing + kStages * kTileBytes;
+  static constexpr uint32_t kXml = kXch + (kExchange ? kTreeRows * D * 4 : 0);
+  static constexpr uint32_t kBar = kXml + (kExchange ? kTreeRows * 8 : 0);
+  static constexpr uint32_t kSmem = kBar + kBarBytes + 1024;  // + alignment slack
+  static constexpr int kTmaWarp = 4 * kStreams;
+  static constexpr int kMmaWarp = kTmaWarp + 1;
+  static constexpr int kThreads = 32 * (5 * kStreams + 1);
+  // tensor memory columns; P (bf16 pairs) takes the place of the S it was made from
+  static constexpr uint32_t kColS = D == 256 ? 256 : 0;  // two buffers of kKeys columns
+  static constexpr uint32_t kColO = D == 256 ? 0 : 256;  // stream w: + w D
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kTiles == 1 || D <= 128, "tiles");
+};
 
-// One CTA per (node, query head): each warp takes every kWarps-th key, its lanes the channels.
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) tree_rows_kernel(const TreeArgs a) {
-  constexpr int kC = D / 32;  // channels per lane: lane + 32 c
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.x, i = blockIdx.y, b = blockIdx.z;
-  const int t0 = min(max(a.cu_q[b], 0), a.total_q);
-  const int n = min(min(max(a.cu_q[b + 1] - t0, 0), a.total_q - t0), a.max_nodes);
-  if (i >= n) return;
-  const int nk = min(max(a.nk[b], 0), a.kv_cap), hkv = h / a.g;
-  float q[kC], o[kC], m = -INFINITY, l = 0.f;
+// A run of key tiles of one unit, published by the producer warp to the other roles.
+struct Seg {
+  int valid;        // 0: the CTA's list is exhausted
+  int tok0, nq, nk; // the sequence's first node, nodes, context keys
+  int hkv, node0;   // KV head; first node (within the sequence) of the unit
+  int k0, nt, ct;   // tiles [k0, k0 + nt) of the unit; its first ct tiles are context
+  int slot;         // -1: the whole unit; else which of the CTA's two partial results
+  int bad;          // set when a draft's V held an infinity or NaN
+};
+
+struct Barriers {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_full[2];
+  uint64_t pv_done[2];  // one stream (d = 256): P.V of S buffer x has completed
+  uint64_t o_full[2], o_empty[2];
+  uint64_t xch_full, xch_empty;
+  uint64_t mma_done[2];
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t v_ready[8];  // two row tiles: stream 0 has looked over the V tile of the slot
+  uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
+  Seg seg[kSegSlots];
+  int64_t scan[12];
+  int64_t first_tiles;  // tiles before the sequence of the CTA's first tile
+  int first_seq;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Barriers) <= kBarBytes, "barrier block");
+
+__device__ __forceinline__ bool vote(bool x) { return __all_sync(0xffffffffu, x); }
+
+// Tiles of one sequence.
+struct SeqTiles {
+  int tok0, nq, nk;
+  int ct, per_unit;  // context tiles, all tiles of a unit
+  int row_units;     // units of a KV head
+  __device__ __forceinline__ int64_t all(int Hkv) const { return static_cast<int64_t>(per_unit) * row_units * Hkv; }
+};
+template <int D, int kTiles>
+__device__ __forceinline__ SeqTiles seq_tiles(const TreeArgs& a, int b) {
+  constexpr int kKeys = Cfg<D, kTiles>::kKeys;
+  SeqTiles s;
+  s.tok0 = min(max(a.cu_q[b], 0), a.total_q);
+  s.nq = min(min(max(a.cu_q[b + 1], s.tok0), a.total_q) - s.tok0, a.max_nodes);
+  s.nk = min(max(a.nk[b], 0), a.kv_cap);
+  s.ct = s.nk / kKeys + (s.nk % kKeys != 0);
+  s.per_unit = s.ct + (s.nq + kKeys - 1) / kKeys;
+  const int unit_nodes = kTiles * (kTreeRows / a.g);
+  s.row_units = (s.nq + unit_nodes - 1) / unit_nodes;  // 0 for a sequence without nodes
+  return s;
+}
+
+// CTAs that share T tiles (none without a tile); the first tile of CTA c of G; the CTA that has tile x.
+__device__ __forceinline__ int ctas_of(int64_t T, int most) { return static_cast<int>(max(min(T, static_cast<int64_t>(most)), static_cast<int64_t>(1))); }
+__device__ __forceinline__ int64_t cta_begin(int64_t c, int64_t T, int G) { return c * T / G; }
+__device__ __forceinline__ int cta_of(int64_t x, int64_t T, int G) { return static_cast<int>(((x + 1) * G + T - 1) / T) - 1; }
+
+// One copy by the calling lane (the wrapper in ptx.cuh elects one lane of a converged warp).
+__device__ __forceinline__ void tma_load_3d_lane(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// One MMA D[tmem] (+)= A[tmem] B[smem], issued by one lane of a converged warp.
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t bhi, uint32_t idesc,
+                                        uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, pe;\n\t.reg .b64 db;\n\telect.sync _|pe, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 db, {%2, %3};\n\t"
+      "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// V tile in shared memory, [atom][kKeys rows][128 bytes]: rows from `valid` on become zero, and with
+// `scan` the infinities and NaN of the others (returns whether there were any). A converged warp.
+template <int kHalves, int kKeys>
+__device__ __forceinline__ bool clean_v(uint8_t* tile, int valid, bool scan, int lane) {
+  bool bad = false;
 #pragma unroll
-  for (int c = 0; c < kC; ++c) {
-    q[c] = bf16_f32(a.q[(t0 + i) * a.q_stride + h * D + lane + 32 * c]) * a.scale_log2;
-    o[c] = 0.f;
-  }
-  const uint64_t* bits = a.mask + static_cast<int64_t>(t0 + i) * a.mask_words;
-  for (int j = warp; j < nk + n; j += kWarps) {
-    const uint16_t *k, *v;
-    if (j >= nk) {
-      const int x = j - nk;
-      if (!(bits[x >> 6] >> (x & 63) & 1)) continue;
-      k = a.k_new + (t0 + x) * a.k_new_stride + hkv * D;
-      v = a.v_new + (t0 + x) * a.v_new_stride + hkv * D;
-    } else {
-      int64_t row;
-      if (a.block_table) {
-        int page = a.block_table[static_cast<int64_t>(b) * a.max_pages + j / a.page_size];
-        page = min(max(page, 0), a.num_pages - 1);
-        row = (static_cast<int64_t>(page) * a.page_size + j % a.page_size) * a.Hkv + hkv;
-      } else {
-        row = (static_cast<int64_t>(b) * a.Hkv + hkv) * a.kv_cap + j;
+  for (int hf = 0; hf < kHalves; ++hf) {
+    uint8_t* atom = tile + hf * (kKeys * 128);
+    if (scan) {
+      for (int off = lane * 16; off < valid * 128; off += 512) {
+        uint4 v = *reinterpret_cast<uint4*>(atom + off);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        bool hit = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if ((w[i] & 0x7f80u) == 0x7f80u) {
+            w[i] &= 0xffff0000u;
+            hit = true;
+          }
+          if ((w[i] & 0x7f800000u) == 0x7f800000u) {
+            w[i] &= 0xffffu;
+            hit = true;
+          }
+        }
+        if (hit) *reinterpret_cast<uint4*>(atom + off) = make_uint4(w[0], w[1], w[2], w[3]);
+        bad |= hit;
       }
-      k = a.k + row * D;
-      v = a.v + row * D;
     }
-    float s = 0.f;
-#pragma unroll
-    for (int c = 0; c < kC; ++c) s = fmaf(q[c], bf16_f32(k[lane + 32 * c]), s);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    const float m_new = fmaxf(m, s), base = m_new == -INFINITY ? 0.f : m_new;
-    const float f = ex2(m - base), p = ex2(s - base);
-    m = m_new;
-    l = l * f + p;
-#pragma unroll
-    for (int c = 0; c < kC; ++c) o[c] = o[c] * f + p * bf16_f32(v[lane + 32 * c]);
+    for (int off = valid * 128 + lane * 16; off < kKeys * 128; off += 512)
+      *reinterpret_cast<uint4*>(atom + off) = make_uint4(0u, 0u, 0u, 0u);
   }
-  __shared__ float sm_m[kWarps], sm_l[kWarps], sm_o[kWarps][D];
-  if (lane == 0) {
-    sm_m[warp] = m;
-    sm_l[warp] = l;
-  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the tensor pipe reads the tile
+  __syncwarp();
+  return __any_sync(0xffffffffu, bad);
+}
+
+template <int D, int kTiles>
+__global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
+  using C = Cfg<D, kTiles>;
+  constexpr int kStreams = C::kStreams, kKeys = C::kKeys, kStages = C::kStages;
+  constexpr int kWarps = C::kThreads / 32;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sRing = smem + C::kRing;
+  Barriers* bar = reinterpret_cast<Barriers*>(smem + C::kBar);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge waits for this grid to complete
+
+  // ---- the list of tiles: every thread sums the tiles of a run of sequences
+  const int run = (a.num_seqs + C::kThreads - 1) / C::kThreads;
+  const int run0 = min(tid * run, a.num_seqs), run1 = min(run0 + run, a.num_seqs);
+  int64_t mine = 0;
+  for (int b = run0; b < run1; ++b) mine += seq_tiles<D, kTiles>(a, b).all(a.Hkv);
+  int64_t incl = mine;
 #pragma unroll
-  for (int c = 0; c < kC; ++c) sm_o[warp][lane + 32 * c] = o[c];
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += x;
+  }
+  if (lane == 31) bar->scan[warp] = incl;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->q_full[i], 1);
+      mbar_init(&bar->q_empty[i], kTiles == 2 ? 1 : kStreams);
+      mbar_init(&bar->s_full[i], 1);
+      mbar_init(&bar->p_full[i], kTreeRows);
+      mbar_init(&bar->pv_done[i], 1);
+      mbar_init(&bar->o_full[i], 1);
+      mbar_init(&bar->o_empty[i], kTreeRows);
+      mbar_init(&bar->mma_done[i], 1);
+    }
+    mbar_init(&bar->xch_full, kTreeRows);
+    mbar_init(&bar->xch_empty, kTreeRows);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bar->kv_full[i], 1);
+      mbar_init(&bar->kv_empty[i], kTiles);  // one commit per stream that reads the slot
+      mbar_init(&bar->v_ready[i], 1);
+    }
+    for (int i = 0; i < kSegSlots; ++i) {
+      mbar_init(&bar->seg_full[i], 1);
+      mbar_init(&bar->seg_empty[i], 5 * kStreams);  // the MMA warps and the softmax warps
+    }
+    bar->first_seq = 0;
+    bar->first_tiles = 0;
+    bar->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(&bar->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   __syncthreads();
-  float M = -INFINITY, L = 0.f;
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w]);
-  const float base = M == -INFINITY ? 0.f : M;
-  for (int w = 0; w < kWarps; ++w) L += sm_l[w] * ex2(sm_m[w] - base);
-  const int64_t orow = static_cast<int64_t>(t0 + i) * a.Hq + h;
-  for (int c = threadIdx.x; c < D; c += kWarps * 32) {
-    float x = 0.f;
-    for (int w = 0; w < kWarps; ++w) x += sm_o[w][c] * ex2(sm_m[w] - base);
-    a.o[orow * D + c] = static_cast<uint16_t>(pack_bf16x2(L == 0.f ? 0.f : x / L, 0.f));
+  tc_fence_after();
+  int64_t T = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) before = T;
+    T += bar->scan[w];
   }
-  if (a.lse && threadIdx.x == 0) a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+  before += incl - mine;  // tiles before this thread's run
+  const int G = ctas_of(T, a.ctas);
+  const int64_t begin = blockIdx.x < G ? cta_begin(blockIdx.x, T, G) : T, end = blockIdx.x < G ? cta_begin(blockIdx.x + 1, T, G) : T;
+  if (blockIdx.x == 0) {  // for the merge
+    int64_t at = before;
+    for (int b = run0; b < run1; ++b) {
+      a.base[b] = at;
+      at += seq_tiles<D, kTiles>(a, b).all(a.Hkv);
+    }
+    if (tid == 0) a.base[a.num_seqs] = T;
+  }
+  if (begin < end && before <= begin && begin < before + mine) {
+    int64_t at = before;
+    int b = run0;
+    for (;; ++b) {
+      const int64_t n = seq_tiles<D, kTiles>(a, b).all(a.Hkv);
+      if (begin < at + n) break;
+      at += n;
+    }
+    bar->first_seq = b;
+    bar->first_tiles = at;
+  }
+  __syncthreads();
+  const uint32_t tbase = bar->tmem_base;
+  volatile int* abort = &bar->abort;
+  const uint64_t tmo = a.timeout_ns;
+  const int tile_nodes = kTreeRows / a.g;
+  const int no_abort = 0;
+
+  // consumer side of the segment queue, called by a converged warp
+  auto wait_seg = [&](int k) -> Seg* {
+    return vote(mbar_wait(&bar->seg_full[k % kSegSlots], (k / kSegSlots) & 1, tmo, abort)) ? &bar->seg[k % kSegSlots] : nullptr;
+  };
+  auto release_seg = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar->seg_empty[k % kSegSlots]);
+  };
+  // rows of the unit's row tile w that exist
+  auto tile_rows = [&](const Seg& s, int w) { return max(0, min(tile_nodes, s.nq - s.node0 - w * tile_nodes)) * a.g; };
+
+  if (warp == C::kTmaWarp) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      prefetch_tmap(&a.tm_q);
+      prefetch_tmap(&a.tm_k);
+      prefetch_tmap(&a.tm_v);
+      prefetch_tmap(&a.tm_kn);
+      prefetch_tmap(&a.tm_vn);
+    }
+    int64_t pos = begin, seq_at = bar->first_tiles;
+    int b = bar->first_seq;
+    int nload = 0, segs = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      Seg s{};
+      int b_seg = 0;
+      if (pos < end) {
+        SeqTiles q = seq_tiles<D, kTiles>(a, b);
+        while (pos >= seq_at + q.all(a.Hkv)) {
+          seq_at += q.all(a.Hkv);
+          q = seq_tiles<D, kTiles>(a, ++b);
+        }
+        const int64_t local = pos - seq_at;
+        const int unit = static_cast<int>(local / q.per_unit);
+        s.valid = 1;
+        s.tok0 = q.tok0;
+        s.nq = q.nq;
+        s.nk = q.nk;
+        s.hkv = unit / q.row_units;
+        s.node0 = unit % q.row_units * (kTiles * tile_nodes);
+        s.k0 = static_cast<int>(local % q.per_unit);
+        s.nt = static_cast<int>(min(static_cast<int64_t>(q.per_unit - s.k0), end - pos));
+        s.ct = q.ct;
+        s.slot = s.nt == q.per_unit ? -1 : (pos == begin ? 0 : 1);
+        b_seg = b;
+        pos += s.nt;
+      }
+      if (k >= kSegSlots && !(ok = vote(mbar_wait(&bar->seg_empty[k % kSegSlots], (k / kSegSlots - 1) & 1, tmo, abort))))
+        break;
+      if (lane == 0) {
+        bar->seg[k % kSegSlots] = s;
+        mbar_arrive(&bar->seg_full[k % kSegSlots]);
+      }
+      __syncwarp();
+      if (!s.valid) break;
+      auto load_q = [&]() -> bool {
+#pragma unroll
+        for (int w = 0; w < kTiles; ++w) {
+          if (segs > 0 && !vote(mbar_wait(&bar->q_empty[w], (segs - 1) & 1, tmo, abort))) return false;
+          mbar_arrive_expect_tx(&bar->q_full[w], static_cast<uint32_t>(tile_nodes * a.g) * 128 * C::kHalves);
+          for (int hf = 0; hf < C::kHalves; ++hf)
+            tma_load_3d(sQ + w * C::kQBytes + hf * (kTreeRows * 128), &a.tm_q, &bar->q_full[w], 64 * hf, s.hkv * a.g,
+                        s.tok0 + s.node0 + w * tile_nodes);
+        }
+        ++segs;
+        return true;
+      };
+      // paged: this lane's copy is atom lane % kHalves of piece lane / kHalves of a tile; the pool row of
+      // the piece in the next tile is looked up one tile ahead
+      const int my_piece = (lane / C::kHalves) * a.piece;
+      auto pool_row = [&](int kt) -> int {
+        const int key = kt * kKeys + my_piece;
+        if (!a.block_table || my_piece >= kKeys || kt >= s.ct || key >= s.nk) return -1;
+        int page = a.block_table[static_cast<int64_t>(b_seg) * a.max_pages + key / a.page_size];
+        page = min(max(page, 0), a.num_pages - 1);  // a bad entry reads a wrong page, never outside the pool
+        return page * a.page_size + key % a.page_size;
+      };
+      int row_next = pool_row(s.k0);
+      const int q_at = min(s.nt, kStages / 4);  // the first loads need ring slots only, not Q's buffer
+      for (int j = 0; j < s.nt && ok; ++j) {
+        if (j == q_at && !(ok = load_q())) break;
+        const int kt = s.k0 + j;
+        const int row = row_next;
+        if (a.block_table) row_next = pool_row(kt + 1);
+        for (int kv = 0; kv < 2; ++kv, ++nload) {
+          const int slot = nload % kStages, round = nload / kStages;
+          if (round > 0 && !(ok = vote(mbar_wait(&bar->kv_empty[slot], (round - 1) & 1, tmo, abort)))) break;
+          uint8_t* dst = sRing + slot * C::kTileBytes;
+          if (kt >= s.ct) {
+            const CUtensorMap* map = kv ? &a.tm_vn : &a.tm_kn;
+            mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(a.new_box) * 128 * C::kHalves);
+            for (int hf = 0; hf < C::kHalves; ++hf)
+              tma_load_3d(dst + hf * (kKeys * 128), map, &bar->kv_full[slot], 64 * hf, s.hkv, s.tok0 + (kt - s.ct) * kKeys);
+          } else if (a.block_table) {
+            // pieces past the last key are not copied: their K scores are masked, their V rows zeroed
+            const int pieces = min(kKeys / a.piece, (s.nk - kt * kKeys + a.piece - 1) / a.piece);
+            const CUtensorMap* map = kv ? &a.tm_v : &a.tm_k;
+            mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(pieces * a.piece) * 128 * C::kHalves);
+            __syncwarp();
+            if (row >= 0) {
+              const int hf = lane % C::kHalves;
+              tma_load_3d_lane(dst + hf * (kKeys * 128) + my_piece * 128, map, &bar->kv_full[slot], 64 * hf, s.hkv, row);
+            }
+            __syncwarp();
+          } else {
+            const CUtensorMap* map = kv ? &a.tm_v : &a.tm_k;
+            mbar_arrive_expect_tx(&bar->kv_full[slot], C::kTileBytes);
+            for (int hf = 0; hf < C::kHalves; ++hf)
+              tma_load_3d(dst + hf * (kKeys * 128), map, &bar->kv_full[slot], 64 * hf, kt * kKeys, b_seg * a.Hkv + s.hkv);
+          }
+        }
+      }
+      if (ok && q_at == s.nt && !(ok = load_q())) break;
+    }
+    if (!ok && lane == 0) raise_timeout(abort, a.status);
+    // every copy this CTA issued must have landed before the CTA may exit
+    if (segs > 0)
+      for (int w = 0; w < kTiles; ++w) mbar_wait(&bar->q_full[w], (segs - 1) & 1, tmo, &no_abort);
+    for (int i = max(0, nload - kStages); i < nload; ++i)
+      mbar_wait(&bar->kv_full[i % kStages], (i / kStages) & 1, tmo, &no_abort);
+  } else if (warp >= C::kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuers, one per stream
+    const int w = warp - C::kMmaWarp;
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(kTreeRows, kKeys, 0, 0);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(kTreeRows, D, 0, 1);
+    const uint32_t hi = sdesc_hi(1024);
+    const uint32_t q_lo = sdesc_lo(smem_u32(sQ) + (kTiles == 2 ? w : 0) * C::kQBytes, 16);
+    const uint32_t k_lo = sdesc_lo(smem_u32(sRing), 16);
+    const uint32_t v_lo = sdesc_lo(smem_u32(sRing), kKeys * 128);
+    constexpr uint32_t slot_step = C::kTileBytes >> 4;
+    const uint32_t tO = tbase + C::kColO + w * D;
+    const int qb = kTiles == 2 ? w : 0;
+    int nload = 0, ns = 0, np = 0, ou = 0;
+    bool ok = true;
+    auto wait_load = [&](int i) -> bool {
+      const bool r = vote(mbar_wait(&bar->kv_full[i % kStages], (i / kStages) & 1, tmo, abort));
+      tc_fence_after();
+      return r;
+    };
+    // S and P buffer of a stream's n-th tile, and how often the buffer was used before
+    auto buf = [&](int n) { return kStreams == 2 ? w : n & 1; };
+    auto use = [&](int n) { return kStreams == 2 ? n : n >> 1; };
+    auto issue_s = [&](int i) {
+      const uint32_t kl = k_lo + (i % kStages) * slot_step;
+      const uint32_t tS = tbase + C::kColS + buf(ns) * kKeys;
+#pragma unroll
+      for (int hf = 0; hf < C::kHalves; ++hf)
+        umma_ss_k64(tS, q_lo + hf * (kTreeRows * 128 / 16), hi, kl + hf * (kKeys * 128 / 16), hi, idesc_qk, hf > 0);
+      umma_commit(&bar->s_full[buf(ns)]);
+      umma_commit(&bar->kv_empty[i % kStages]);
+      ++ns;
+    };
+    auto issue_pv = [&](int i, bool accumulate) {
+      const uint32_t tP = tbase + C::kColS + buf(np) * kKeys;
+      const uint32_t vl = v_lo + (i % kStages) * slot_step;
+      if constexpr (kKeys == 128) {
+        umma_ts_k128(tO, tP, vl, hi, idesc_pv, accumulate ? 1u : 0u);
+      } else {
+#pragma unroll
+        for (int s = 0; s < kKeys / 16; ++s) umma_ts(tO, tP + 8 * s, vl + 128 * s, hi, idesc_pv, (accumulate || s) ? 1u : 0u);
+      }
+      if constexpr (kStreams == 1) umma_commit(&bar->pv_done[buf(np)]);
+      ++np;
+    };
+    for (int k = 0; ok; ++k) {
+      Seg* sp = wait_seg(k);
+      if (!(ok = sp != nullptr)) break;
+      const Seg s = *sp;
+      if (!s.valid) {
+        release_seg(k);
+        break;
+      }
+      if (!(ok = vote(mbar_wait(&bar->q_full[qb], k & 1, tmo, abort)))) break;
+      tc_fence_after();
+      const int base = nload;
+      nload += 2 * s.nt;
+      // this stream's tiles: j0, j0 + step, ... below s.nt
+      const int step = C::kExchange ? 2 : 1;
+      const int j0 = C::kExchange ? w : 0;
+      const bool idle = kTiles == 2 && tile_rows(s, w) == 0;  // no rows: only gives the slots back
+      if (idle || j0 >= s.nt) umma_commit(&bar->q_empty[qb]);
+      if (!idle && j0 < s.nt && kStreams == 1) {
+        if (!(ok = wait_load(base))) break;
+        issue_s(base);
+        if (s.nt == 1) umma_commit(&bar->q_empty[qb]);
+      }
+      for (int j = j0; j < s.nt; j += step) {
+        const int ik = base + 2 * j, iv = ik + 1;
+        if (idle) {
+          if (!(ok = wait_load(ik))) break;
+          umma_commit(&bar->kv_empty[ik % kStages]);
+          if (!(ok = wait_load(iv))) break;
+          umma_commit(&bar->kv_empty[iv % kStages]);
+          continue;
+        }
+        if constexpr (kStreams == 2) {
+          // the stream's previous P.V was issued before, so this S may overwrite its P
+          if (!(ok = wait_load(ik))) break;
+          issue_s(ik);
+          if (j + step >= s.nt) umma_commit(&bar->q_empty[qb]);
+        } else if (j + 1 < s.nt) {
+          // S of the next tile goes ahead of this tile's P.V, into the other buffer
+          if (!(ok = wait_load(ik + 2))) break;
+          issue_s(ik + 2);
+          if (j + 2 == s.nt) umma_commit(&bar->q_empty[qb]);
+        }
+        if (!(ok = wait_load(iv))) break;
+        // V rows that do not count, and drafts' infinities and NaN (two row tiles read one V tile:
+        // stream 0 looks it over for both)
+        const int kt = s.k0 + j;
+        const bool draft = kt >= s.ct;
+        const int valid = min(kKeys, draft ? s.nq - (kt - s.ct) * kKeys : s.nk - kt * kKeys);
+        const bool special = draft || valid < kKeys;
+        uint8_t* vtile = sRing + (iv % kStages) * C::kTileBytes;
+        if (kTiles == 1 || w == 0) {
+          if (special && clean_v<C::kHalves, kKeys>(vtile, valid, draft, lane) && lane == 0) atomicOr(&sp->bad, 1);
+          if (kTiles == 2) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->v_ready[iv % kStages]);
+          }
+        } else if (special) {
+          if (!(ok = vote(mbar_wait(&bar->v_ready[iv % kStages], (iv / kStages) & 1, tmo, abort)))) break;
+        }
+        if (j == j0 && ou > 0 && !(ok = vote(mbar_wait(&bar->o_empty[w], (ou - 1) & 1, tmo, abort)))) break;
+        if (!(ok = vote(mbar_wait(&bar->p_full[buf(np)], use(np) & 1, tmo, abort)))) break;
+        tc_fence_after();
+        issue_pv(iv, j > j0);
+        umma_commit(&bar->kv_empty[iv % kStages]);
+        if (j + step >= s.nt) {
+          umma_commit(&bar->o_full[w]);
+          ++ou;
+        }
+      }
+      if (!ok) break;
+      release_seg(k);
+    }
+    if (!ok && lane == 0) raise_timeout(abort, a.status);
+    // all MMAs issued by this warp complete before TMEM is released
+    umma_commit(&bar->mma_done[w]);
+    mbar_wait(&bar->mma_done[w], 0, tmo, &no_abort);
+  } else {
+    // ------------------------------------------------------------ softmax warpgroups
+    const int w = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;  // = TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tO = tbase + lane_base + C::kColO + w * D;
+    const float sl2 = a.scale_log2;
+    float* xo = reinterpret_cast<float*>(smem + C::kXch);   // [D][kTreeRows]
+    float2* xml = reinterpret_cast<float2*>(smem + C::kXml);  // [kTreeRows]
+    int n = 0, oused = 0, xn = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const Seg* sp = wait_seg(k);
+      if (!(ok = sp != nullptr)) break;
+      const Seg s = *sp;
+      if (!s.valid) {
+        release_seg(k);
+        break;
+      }
+      const int rw = kTiles == 2 ? w : 0;  // row tile of this stream
+      const int rows = tile_rows(s, rw);
+      if (rows == 0) {
+        release_seg(k);
+        continue;
+      }
+      const bool row_ok = row < rows, warp_ok = (warp & 3) * 32 < rows;
+      const int node = s.node0 + rw * tile_nodes + min(row, rows - 1) / a.g;  // within the sequence
+      const int head = s.hkv * a.g + min(row, rows - 1) % a.g;
+      const uint64_t* bits = a.mask + static_cast<int64_t>(s.tok0 + node) * a.mask_words;
+      const int step = C::kExchange ? 2 : 1;
+      const int j0 = C::kExchange ? w : 0;
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = j0; j < s.nt; j += step) {
+        const int x = kStreams == 2 ? w : n & 1, phase = (kStreams == 2 ? n : n >> 1) & 1;
+        const uint32_t tS = tbase + lane_base + C::kColS + x * kKeys;
+        if (!(ok = vote(mbar_wait(&bar->s_full[x], phase, tmo, abort)))) break;
+        tc_fence_after();
+        if (warp_ok) {
+          uint32_t sc[kKeys / 32][32];
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(tS + 32 * c, sc[c]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; ++c) tmem_reg_fence(sc[c]);
+          const int kt = s.k0 + j;
+          const uint32_t ninf = __float_as_uint(-INFINITY);
+          if (kt >= s.ct) {
+            // drafts: 64 mask bits a word; none at or past the sequence's last node
+            const int d0 = (kt - s.ct) * kKeys;
+#pragma unroll
+            for (int h = 0; h < kKeys / 64; ++h) {
+              const int wi = d0 / 64 + h, left = s.nq - 64 * wi;
+              uint64_t m = wi < a.mask_words ? bits[wi] : 0;
+              if (left < 64) m = left > 0 ? m & ((1ull << left) - 1) : 0;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t mm = static_cast<uint32_t>(m >> (32 * c));
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!(mm >> e & 1)) sc[2 * h + c][e] = ninf;
+              }
+            }
+          } else if ((kt + 1) * kKeys > s.nk) {
+            const int left = s.nk - kt * kKeys;  // keys of the context's last tile
+#pragma unroll
+            for (int c = 0; c < kKeys / 32; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (32 * c + e >= left) sc[c][e] = ninf;
+          }
+          float mx[kKeys / 32];
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; ++c) {
+            mx[c] = __uint_as_float(sc[c][0]);
+#pragma unroll
+            for (int e = 1; e < 31; e += 2) mx[c] = max3f(mx[c], __uint_as_float(sc[c][e]), __uint_as_float(sc[c][e + 1]));
+            mx[c] = fmaxf(mx[c], __uint_as_float(sc[c][31]));
+          }
+          float mt = mx[0];
+#pragma unroll
+          for (int c = 1; c < kKeys / 32; ++c) mt = fmaxf(mt, mx[c]);
+          const float m_new = fmaxf(m_ref, mt * sl2);
+          float alpha_o = 1.f;
+          if (m_new > m_ref + kRescaleThreshold) {
+            const float alpha = (m_ref == -INFINITY) ? 0.f : ex2(m_ref - m_new);
+            l *= alpha;
+            if (j > j0) alpha_o = alpha;
+            m_ref = m_new;
+          }
+          const float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
+          // p = 2^(s scale log2e - m) as bf16 pairs into the first half of the S columns; l is the fp32
+          // sum before that rounding
+          float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float x0, x1;
+              ffma2(x0, x1, __uint_as_float(sc[c][2 * e]), __uint_as_float(sc[c][2 * e + 1]), sl2, nm);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              fadd2(ls[(2 * e) & 7], ls[(2 * e + 1) & 7], p0, p1);
+              pk[e] = pack_bf16x2(p0, p1);
+            }
+            tmem_st16(tS + 16 * c, pk);
+          }
+          // O must carry the new reference maximum before this tile's P.V (rare)
+          if (__any_sync(0xffffffffu, alpha_o != 1.f)) {
+            if (kStreams == 1) {
+              // S(j) was issued ahead of P.V(j - 1): that one has to be done
+              ok = vote(mbar_wait(&bar->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, tmo, abort));
+              if (!ok) break;
+              tc_fence_after();
+            }
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t ov[32];
+              tmem_ld32(tO + c * 32, ov);
+              tmem_wait_ld();
+              tmem_reg_fence(ov);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha_o);
+              tmem_st32(tO + c * 32, ov);
+            }
+          }
+          tmem_wait_st();
+          l += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
+        }
+        tc_fence_before();
+        mbar_arrive(&bar->p_full[x]);
+        ++n;
+      }
+      if (!ok) break;
+      // ---- the unit's end in this CTA
+      const bool have_o = j0 < s.nt;
+      if (have_o) {
+        if (!(ok = vote(mbar_wait(&bar->o_full[w], oused & 1, tmo, abort)))) break;
+        ++oused;
+        tc_fence_after();
+      }
+      const bool exchange = C::kExchange && s.nt > 1;
+      if (exchange && w == 1) {
+        // stream 1 hands its state over
+        if (xn > 0 && !(ok = vote(mbar_wait(&bar->xch_empty, (xn - 1) & 1, tmo, abort)))) break;
+        ++xn;
+        if (warp_ok) {
+          xml[row] = make_float2(m_ref, l);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tmem_ld32(tO + c * 32, ov);
+            tmem_wait_ld();
+            tmem_reg_fence(ov);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) xo[(c * 32 + e) * kTreeRows + row] = __uint_as_float(ov[e]);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&bar->o_empty[w]);
+        mbar_arrive(&bar->xch_full);
+        release_seg(k);
+        continue;
+      }
+      if (C::kExchange && w == 1) {  // one tile: stream 0 has it
+        release_seg(k);
+        continue;
+      }
+      float f0 = 1.f, f1 = 0.f;
+      if (exchange) {
+        if (!(ok = vote(mbar_wait(&bar->xch_full, xn & 1, tmo, abort)))) break;
+        ++xn;
+        if (warp_ok) {
+          const float2 o1 = xml[row];
+          const float m = fmaxf(m_ref, o1.x);
+          f0 = m_ref == -INFINITY ? 0.f : ex2(m_ref - m);
+          f1 = o1.x == -INFINITY ? 0.f : ex2(o1.x - m);
+          l = l * f0 + o1.y * f1;
+          m_ref = m;
+        }
+      }
+      if (warp_ok) {
+        const bool bad = *const_cast<const volatile int*>(&sp->bad) != 0;
+        const int64_t orow = static_cast<int64_t>(s.tok0 + node) * a.Hq + head;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        float* part = a.partial + ((static_cast<int64_t>(blockIdx.x) * 2 + max(s.slot, 0)) * kTiles + rw) * (kTreeRows * (D + 2));
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(tO + c * 32, ov);
+          tmem_wait_ld();
+          tmem_reg_fence(ov);
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            o[e] = __uint_as_float(ov[e]);
+            if (exchange) o[e] = o[e] * f0 + xo[(c * 32 + e) * kTreeRows + row] * f1;
+          }
+          if (bad && row_ok) {
+            // the infinities and NaN among the drafts that this row sees
+            const int d0 = max(s.k0 - s.ct, 0) * kKeys, d1 = min((s.k0 + s.nt - s.ct) * kKeys, s.nq);
+            for (int x = d0; x < d1; ++x) {
+              if (!(bits[x >> 6] >> (x & 63) & 1)) continue;
+              const uint16_t* v = a.v_new + (s.tok0 + x) * a.v_new_stride + s.hkv * D + c * 32;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if ((v[e] & 0x7f80) == 0x7f80) o[e] += __uint_as_float(static_cast<uint32_t>(v[e]) << 16);
+            }
+          }
+          if (!row_ok) continue;
+          if (s.slot < 0) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint4 v;
+              v.x = pack_bf16x2(o[8 * q] * inv, o[8 * q + 1] * inv);
+              v.y = pack_bf16x2(o[8 * q + 2] * inv, o[8 * q + 3] * inv);
+              v.z = pack_bf16x2(o[8 * q + 4] * inv, o[8 * q + 5] * inv);
+              v.w = pack_bf16x2(o[8 * q + 6] * inv, o[8 * q + 7] * inv);
+              *reinterpret_cast<uint4*>(a.o + orow * D + c * 32 + 8 * q) = v;
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<float4*>(part + ((c * 8 + q) * kTreeRows + row) * 4) =
+                  make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          }
+        }
+        if (row_ok && s.slot < 0 && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+        if (row_ok && s.slot >= 0) *reinterpret_cast<float2*>(part + kTreeRows * D + 2 * row) = make_float2(m_ref, l);
+      }
+      tc_fence_before();
+      if (have_o) mbar_arrive(&bar->o_empty[w]);
+      if (exchange) mbar_arrive(&bar->xch_empty);
+      release_seg(k);
+    }
+    if (!ok && lane == 0) raise_timeout(abort, a.status);
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == C::kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// The parts of units that several CTAs shared: one CTA per 32 rows of a row tile; lanes are rows,
+// each warp takes every eighth channel quad. m = max m_c, l = sum l_c 2^(m_c - m), o likewise.
+constexpr int kMergeThreads = 256;
+template <int D, int kTiles>
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeArgs a, int row_units) {
+  constexpr int kQ = D / 4 / (kMergeThreads / 32);  // channel quads per thread
+  __shared__ __align__(16) uint16_t out[32][D + 8];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results are complete and visible
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int idx = blockIdx.x;
+  const int quarter = idx % 4;
+  idx /= 4;
+  const int w = idx % kTiles;
+  idx /= kTiles;
+  const int ru = idx % row_units;
+  idx /= row_units;
+  const int hkv = idx % a.Hkv, b = idx / a.Hkv;
+  const SeqTiles q = seq_tiles<D, kTiles>(a, b);
+  const int tile_nodes = kTreeRows / a.g;
+  const int node0 = (ru * kTiles + w) * tile_nodes;
+  const int rows = max(0, min(tile_nodes, q.nq - node0)) * a.g;
+  if (32 * quarter >= rows) return;
+  const int64_t T = a.base[a.num_seqs];
+  const int64_t u0 = a.base[b] + (static_cast<int64_t>(hkv) * q.row_units + ru) * q.per_unit;
+  const int G = ctas_of(T, a.ctas);
+  const int c0 = cta_of(u0, T, G), c1 = cta_of(u0 + q.per_unit - 1, T, G);
+  if (c0 == c1) return;  // written by its CTA
+  const int row = 32 * quarter + lane;
+  const bool row_ok = row < rows;
+  const int slot0 = u0 <= cta_begin(c0, T, G) ? 0 : 1;
+  constexpr int64_t kPart = kTreeRows * (D + 2);
+  auto part = [&](int c) { return a.partial + ((static_cast<int64_t>(c) * 2 + (c == c0 ? slot0 : 0)) * kTiles + w) * kPart; };
+  float m = -INFINITY, l = 0.f;
+  float4 acc[kQ];
+#pragma unroll
+  for (int i = 0; i < kQ; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (row_ok) {
+    for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(part(c) + kTreeRows * D + 2 * row));
+    for (int c = c0; c <= c1; ++c) {
+      const float* p = part(c);
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + kTreeRows * D + 2 * row));
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+      l += ml.y * f;
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(p + ((warp + 8 * i) * kTreeRows + row) * 4));
+        acc[i].x += v.x * f;
+        acc[i].y += v.y * f;
+        acc[i].z += v.z * f;
+        acc[i].w += v.w * f;
+      }
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < kQ; ++i)
+    *reinterpret_cast<uint2*>(&out[lane][4 * (warp + 8 * i)]) =
+        make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
+  auto out_row = [&](int r) { return static_cast<int64_t>(q.tok0 + node0 + r / a.g) * a.Hq + hkv * a.g + r % a.g; };
+  if (warp == 0 && row_ok && a.lse) a.lse[out_row(row)] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  __syncthreads();
+  for (int it = threadIdx.x; it < 32 * (D / 8); it += kMergeThreads) {
+    const int r = it / (D / 8), c = it % (D / 8);
+    if (32 * quarter + r < rows)
+      *reinterpret_cast<uint4*>(a.o + out_row(32 * quarter + r) * D + 8 * c) = *reinterpret_cast<const uint4*>(&out[r][8 * c]);
+  }
+}
+
+template <int D, int kTiles>
+cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
+  using C = Cfg<D, kTiles>;
+  cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
+  if (e != cudaSuccess) return e;
+  tree_kernel<D, kTiles><<<a.ctas, C::kThreads, C::kSmem, stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  count_launch();
+  const int unit_nodes = kTiles * (kTreeRows / a.g);
+  const int row_units = (a.max_nodes + unit_nodes - 1) / unit_nodes;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.num_seqs) * a.Hkv * row_units * kTiles * 4));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, kTiles>, a, row_units)) == cudaSuccess) count_launch();
+  return e;
 }
 
 }  // namespace
 
-size_t tree_ws_bytes(int, int, int, int) { return 256; }
-
-cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
-  const dim3 grid(a.Hq, a.max_nodes, a.num_seqs);
-  if (a.d == 64) tree_rows_kernel<64><<<grid, kWarps * 32, 0, stream>>>(a);
-  if (a.d == 128) tree_rows_kernel<128><<<grid, kWarps * 32, 0, stream>>>(a);
-  if (a.d == 256) tree_rows_kernel<256><<<grid, kWarps * 32, 0, stream>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
+  cudaError_t e = status_word(&a.status);
+  if (e != cudaSuccess) return e;
+  a.timeout_ns = wait_timeout_ns();
+  a.base = static_cast<int64_t*>(workspace);
+  a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + tree_base_bytes(a.num_seqs));
+  const int d = a.d, keys = d == 256 ? 64 : 128;
+  if ((e = make_map_bf16(&a.tm_q, a.q, d, a.Hq, a.total_q, d, a.q_stride, a.g, kTreeRows / a.g)) != cudaSuccess) return e;
+  a.new_box = a.max_nodes < keys ? (a.max_nodes + 7) / 8 * 8 : keys;
+  if ((e = make_map_bf16(&a.tm_kn, a.k_new, d, a.Hkv, a.total_q, d, a.k_new_stride, 1, a.new_box)) != cudaSuccess ||
+      (e = make_map_bf16(&a.tm_vn, a.v_new, d, a.Hkv, a.total_q, d, a.v_new_stride, 1, a.new_box)) != cudaSuccess)
+    return e;
+  if (a.kv_cap == 0) {
+    a.tm_k = a.tm_kn;  // no context tile exists
+    a.tm_v = a.tm_vn;
+  } else if (a.block_table) {
+    a.piece = 16;
+    while (a.piece < keys && a.page_size % (2 * a.piece) == 0) a.piece *= 2;
+    const int64_t rows = static_cast<int64_t>(a.num_pages) * a.page_size, step = static_cast<int64_t>(a.Hkv) * d;
+    if ((e = make_map_bf16(&a.tm_k, a.k, d, a.Hkv, rows, d, step, 1, a.piece)) != cudaSuccess ||
+        (e = make_map_bf16(&a.tm_v, a.v, d, a.Hkv, rows, d, step, 1, a.piece)) != cudaSuccess)
+      return e;
+  } else {
+    const int64_t heads = static_cast<int64_t>(a.num_seqs) * a.Hkv, step = static_cast<int64_t>(a.kv_cap) * d;
+    if ((e = make_map_bf16(&a.tm_k, a.k, d, a.kv_cap, heads, d, step, keys, 1)) != cudaSuccess ||
+        (e = make_map_bf16(&a.tm_v, a.v, d, a.kv_cap, heads, d, step, keys, 1)) != cudaSuccess)
+      return e;
+  }
+  int dev = 0, sms = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  const int tiles = tree_row_tiles(a.max_nodes, a.g, d);
+  // no more CTAs than tiles there can be
+  const int unit_nodes = tiles * (kTreeRows / a.g);
+  const int64_t most = static_cast<int64_t>(a.num_seqs) * a.Hkv * ((a.max_nodes + unit_nodes - 1) / unit_nodes) *
+                       ((a.kv_cap + keys - 1) / keys + (a.max_nodes + keys - 1) / keys);
+  a.ctas = static_cast<int>(most < kTreeMaxCtas ? most : kTreeMaxCtas);
+  if (a.ctas > sms) a.ctas = sms;
+  if (d == 64) return tiles == 2 ? launch<64, 2>(a, stream) : launch<64, 1>(a, stream);
+  if (d == 128) return tiles == 2 ? launch<128, 2>(a, stream) : launch<128, 1>(a, stream);
+  return launch<256, 1>(a, stream);
 }
 
 }  // namespace bw
