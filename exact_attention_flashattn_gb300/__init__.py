@@ -452,56 +452,67 @@ def attn_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q:
 # ---------------------------------------------------------------- speculative decoding
 
 
-class _Call:
-    """Where a call runs: the device of its tensors and ``stream`` (default: that device's current
-    stream). What the call allocates belongs to that stream, so that its memory is not handed to
-    other work while the kernels still run."""
+# These calls run at every step of a server, where the host's time counts: devices are compared by
+# index, the current stream is read as its raw handle (a Stream object costs 2 us), and nothing is
+# entered when the tensors' device is current and no stream is named.
 
-    def __init__(self, device, stream):
-        self.device = device
-        self.here = device.index is None or device.index == torch.cuda.current_device()
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        self.guard = stream is not None or not self.here
-
-    def __enter__(self):
-        if self.guard:
-            self.context = torch.cuda.stream(self.stream) if self.stream.device == self.device else None
-            if self.context is None:
-                raise ValueError(f"the stream is on {self.stream.device}, the tensors on {self.device}")
-            self.context.__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard:
-            self.context.__exit__(*exc)
+_I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
 
 
-def _int32(t, name, device, shape=None):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
-    if shape is not None and tuple(t.shape) != shape:
+def _where(dev: int, stream):
+    """The stream handle of a call on device ``dev`` and the context to run it in: None on the current
+    device's current stream. What a call allocates belongs to its stream, so that the memory is not
+    handed to other work while the kernels still run."""
+    if stream is None:
+        if dev == torch._C._cuda_getDevice():
+            return torch._C._cuda_getCurrentRawStream(dev), None
+        stream = torch.cuda.current_stream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _run(dev, stream, fn, *args):
+    st, context = _where(dev, stream)
+    if context is None:
+        return fn(st, *args)
+    with context:
+        return fn(st, *args)
+
+
+def _first(t, name, ndim):
+    """The device index of a call's leading tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != ndim:
+        raise ValueError(f"{name} must be a {ndim}-D CUDA tensor")
+    return t.get_device()
+
+
+def _like(t, name, dev, dtype, shape=None):
+    """A contiguous tensor of that type on the call's device: its address."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    return t
+    return t.data_ptr()
 
 
-def _out(t, name, device, dtype, shape):
+def _out(t, name, dev, dtype, shape):
     """An output tensor: a new one, or the caller's."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _like(t, name, dev, dtype, shape)
     return t
 
 
-def _rows(t, name, device, heads, d):
+def _rows(t, name, dev, shape):
     """bf16 [rows, heads, d] whose rows may lie apart (a slice of a fused projection): the row stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != device or t.dim() != 3:
-        raise ValueError(f"{name} must be a 3-D bf16 tensor on {device}")
-    n, h, c = t.shape
-    if (h, c) != (heads, d):
-        raise ValueError(f"{name} must be [rows, {heads}, {d}], got {tuple(t.shape)}")
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name} must be a bf16 tensor {shape} on cuda:{dev}")
+    n, h, c = shape
+    if t.is_contiguous():
+        return h * c
     s0, s1, s2 = t.stride()
-    if n and ((s2 != 1 and c > 1) or (s1 != c and h > 1) or (n > 1 and (s0 < h * c or s0 % 8))):
+    if s2 != 1 or (s1 != c and h > 1) or (n > 1 and (s0 < h * c or s0 % 8)):
         raise ValueError(f"{name}: heads must be contiguous, and rows a multiple of 8 elements apart")
     return s0 if n > 1 else h * c
 
@@ -510,64 +521,51 @@ def tree_workspace_size(num_seqs: int, max_nodes: int, Hq: int, Hkv: int, d: int
     return int(lib().attn_tree_workspace_size(num_seqs, max_nodes, Hq, Hkv, d))
 
 
-def _tree(q, k, v, table, k_new, v_new, nk, cu, mask, max_nodes, scale, workspace, out, lse, stream):
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
-        raise ValueError("q must be a CUDA tensor [total_q, Hq, d]")
-    if k.dim() != 4 or tuple(v.shape) != tuple(k.shape) or k_new.dim() != 3:
-        raise ValueError("the caches must be 4-D and alike; k_new and v_new [total_q, Hkv, d]")
-    device = q.device
+def _tree(st, dev, q, k, v, table, k_new, v_new, nk, cu, mask, max_nodes, scale, workspace, out, lse):
     tq, Hq, d = q.shape
-    Hkv = k_new.shape[1]
     if table is None:
-        num_seqs, hk, cap, dk = k.shape
+        num_seqs, Hkv, cap, dk = k.shape
     else:
-        num_pages, page_size, hk, dk = k.shape
-        num_seqs = table.shape[0]
-        _int32(table, "block_table", device)
-        if table.dim() != 2:
-            raise ValueError("block_table must be [num_seqs, max_pages]")
-    if dk != d or hk != Hkv:
-        raise ValueError("q, the caches, k_new and v_new must agree in head dim and KV heads")
-    for t, n in ((k, "k cache"), (v, "v cache")):
-        _cuda(t, n, torch.bfloat16)
-        if t.device != device:
-            raise ValueError(f"the {n} must be on {device}")
-    qs = _rows(q, "q", device, Hq, d)
-    ks = _rows(k_new, "k_new", device, Hkv, d)
-    vs = _rows(v_new, "v_new", device, Hkv, d)
-    if k_new.shape[0] != tq or v_new.shape[0] != tq:
-        raise ValueError("q, k_new and v_new must have the same number of rows")
-    _int32(nk, "nk", device, (num_seqs,))
-    _int32(cu, "cu_seqlens_q", device, (num_seqs + 1,))
-    max_nodes = int(max_nodes)
-    if mask.dtype not in (torch.int64, torch.uint64) or mask.device != device or not mask.is_contiguous() or \
-            tuple(mask.shape) != (tq, (max_nodes + 63) // 64):
-        raise ValueError("mask must be a contiguous int64 tensor [total_q, ceil(max_nodes / 64)]")
-    with _Call(device, stream) as st:
-        out = _out(out, "out", device, torch.bfloat16, (tq, Hq, d))
-        lse_t = None
-        if lse is True:
-            lse_t = torch.empty((tq, Hq), dtype=torch.float32, device=device)
-        elif isinstance(lse, torch.Tensor):
-            lse_t = _out(lse, "lse", device, torch.float32, (tq, Hq))
-        if workspace is None:
-            workspace = torch.empty(max(tree_workspace_size(num_seqs, max_nodes, Hq, Hkv, d), 16), dtype=torch.uint8,
-                                    device=device)
-        _cuda(workspace, "workspace")
-        if workspace.device != device:
-            raise ValueError(f"workspace must be on {device}")
-        ws_bytes = workspace.numel() * workspace.element_size()
-        if table is None:
-            rc = lib().attn_tree(_ptr(q), _ptr(k), _ptr(v), _ptr(k_new), _ptr(v_new), _ptr(out), _ptr(lse_t), _ptr(nk),
-                                 _ptr(cu), _ptr(mask), num_seqs, tq, max_nodes, cap, Hq, Hkv, d, qs, ks, vs,
-                                 _scale(scale, d), _ptr(workspace), ws_bytes, st)
-        else:
-            rc = lib().attn_tree_paged(_ptr(q), _ptr(k), _ptr(v), _ptr(table), _ptr(k_new), _ptr(v_new), _ptr(out),
-                                       _ptr(lse_t), _ptr(nk), _ptr(cu), _ptr(mask), num_seqs, tq, max_nodes, page_size,
-                                       num_pages, table.shape[1], Hq, Hkv, d, qs, ks, vs, _scale(scale, d),
-                                       _ptr(workspace), ws_bytes, st)
+        num_pages, page_size, Hkv, dk = k.shape
+        num_seqs, max_pages = table.shape
+        tp = _like(table, "block_table", dev, _I32)
+    if dk != d:
+        raise ValueError("q and the caches must have the same head dim")
+    kp = _like(k, "the k cache", dev, _BF16)
+    vp = _like(v, "the v cache", dev, _BF16, k.shape)
+    qs = _rows(q, "q", dev, q.shape)
+    ks = _rows(k_new, "k_new", dev, (tq, Hkv, d))
+    vs = _rows(v_new, "v_new", dev, (tq, Hkv, d))
+    nkp = _like(nk, "nk", dev, _I32, (num_seqs,))
+    cup = _like(cu, "cu_seqlens_q", dev, _I32, (num_seqs + 1,))
+    if isinstance(mask, torch.Tensor) and mask.dtype is torch.uint64:
+        mask = mask.view(torch.int64)
+    mp = _like(mask, "mask", dev, torch.int64, (tq, (max_nodes + 63) // 64))
+    out = _out(out, "out", dev, _BF16, q.shape)
+    if lse is True:
+        lse = torch.empty((tq, Hq), dtype=_F32, device=dev)
+    elif not isinstance(lse, torch.Tensor):
+        lse = None
+    else:
+        _like(lse, "lse", dev, _F32, (tq, Hq))
+    if workspace is None:
+        workspace = torch.empty(max(tree_workspace_size(num_seqs, max_nodes, Hq, Hkv, d), 16), dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    scale = _scale(scale, d)
+    lp = None if lse is None else lse.data_ptr()
+    wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    L = _lib or lib()
+    if table is None:
+        rc = L.attn_tree(q.data_ptr(), kp, vp, k_new.data_ptr(), v_new.data_ptr(), out.data_ptr(), lp, nkp, cup, mp,
+                         num_seqs, tq, max_nodes, cap, Hq, Hkv, d, qs, ks, vs, scale, wp, wb, st)
+    else:
+        rc = L.attn_tree_paged(q.data_ptr(), kp, vp, tp, k_new.data_ptr(), v_new.data_ptr(), out.data_ptr(), lp, nkp, cup,
+                               mp, num_seqs, tq, max_nodes, page_size, num_pages, max_pages, Hq, Hkv, d, qs, ks, vs, scale,
+                               wp, wb, st)
+    if rc:
         _check(rc, "attn_tree" if table is None else "attn_tree_paged")
-    return out, lse_t
+    return out, lse
 
 
 def attn_tree(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -577,8 +575,10 @@ def attn_tree(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor, k_new
     """Drafted token trees over a contiguous cache. q [total_q, Hq, d], k_new, v_new [total_q, Hkv, d] bf16
     (rows may lie apart); caches [B, Hkv, cap, d]; nk [B], cu_seqlens_q [B + 1] int32; mask
     [total_q, ceil(max_nodes / 64)] int64 (``attn_tree_mask`` makes it) -> (o, lse or None)."""
-    return _tree(q, kcache, vcache, None, k_new, v_new, nk, cu_seqlens_q, mask, max_nodes, scale, workspace, out, lse,
-                 stream)
+    dev = _first(q, "q", 3)
+    _first(kcache, "kcache", 4)
+    return _run(dev, stream, _tree, dev, q, kcache, vcache, None, k_new, v_new, nk, cu_seqlens_q, mask, int(max_nodes),
+                scale, workspace, out, lse)
 
 
 def attn_tree_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
@@ -587,27 +587,30 @@ def attn_tree_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
                     workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
                     lse: torch.Tensor | bool | None = True, stream=None):
     """``attn_tree`` over a paged cache: pages [num_pages, page_size, Hkv, d], block_table [B, max_pages] int32."""
-    return _tree(q, k_pages, v_pages, block_table, k_new, v_new, nk, cu_seqlens_q, mask, max_nodes, scale, workspace,
-                 out, lse, stream)
+    dev = _first(q, "q", 3)
+    _first(k_pages, "k_pages", 4)
+    _first(block_table, "block_table", 2)
+    return _run(dev, stream, _tree, dev, q, k_pages, v_pages, block_table, k_new, v_new, nk, cu_seqlens_q, mask,
+                int(max_nodes), scale, workspace, out, lse)
 
 
 def attn_tree_mask(parents: torch.Tensor, cu_seqlens_q: torch.Tensor, max_nodes: int, nk: torch.Tensor | None = None,
                    mask: torch.Tensor | None = None, positions: torch.Tensor | None = None, stream=None):
     """Masks and positions of drafted trees. parents [total_q] int32 (index within the sequence, a root
     outside [0, i)) -> (mask [total_q, ceil(max_nodes / 64)] int64, positions [total_q] int32 = nk + depth)."""
-    if not isinstance(parents, torch.Tensor) or not parents.is_cuda or parents.dim() != 1:
-        raise ValueError("parents must be a 1-D CUDA tensor")
-    device, tq, max_nodes = parents.device, parents.shape[0], int(max_nodes)
-    _int32(parents, "parents", device)
-    _int32(cu_seqlens_q, "cu_seqlens_q", device)
-    num_seqs = cu_seqlens_q.numel() - 1
-    if nk is not None:
-        _int32(nk, "nk", device, (num_seqs,))
-    with _Call(device, stream) as st:
-        mask = _out(mask, "mask", device, torch.int64, (tq, max(0, max_nodes + 63) // 64))
-        positions = _out(positions, "positions", device, torch.int32, (tq,))
-        rc = lib().attn_tree_mask(_ptr(parents), _ptr(cu_seqlens_q), _ptr(nk), _ptr(mask), _ptr(positions), num_seqs, tq,
-                                  max_nodes, st)
+    dev = _first(parents, "parents", 1)
+    return _run(dev, stream, _tree_mask, dev, parents, cu_seqlens_q, int(max_nodes), nk, mask, positions)
+
+
+def _tree_mask(st, dev, parents, cu, max_nodes, nk, mask, positions):
+    tq, num_seqs = parents.shape[0], cu.numel() - 1
+    pp = _like(parents, "parents", dev, _I32)
+    cup = _like(cu, "cu_seqlens_q", dev, _I32)
+    nkp = None if nk is None else _like(nk, "nk", dev, _I32, (num_seqs,))
+    mask = _out(mask, "mask", dev, torch.int64, (tq, max(0, max_nodes + 63) // 64))
+    positions = _out(positions, "positions", dev, _I32, (tq,))
+    rc = (_lib or lib()).attn_tree_mask(pp, cup, nkp, mask.data_ptr(), positions.data_ptr(), num_seqs, tq, max_nodes, st)
+    if rc:
         _check(rc, "attn_tree_mask")
     return mask, positions
 
@@ -618,61 +621,50 @@ def kv_plan_paged(nk: torch.Tensor, n_new: torch.Tensor, block_table: torch.Tens
     pages from the top of the stack free_pages[:free_count] and returns (nk + n_new, held + pages taken,
     cu_seqlens [B + 1], slots [num_tokens], free_count - pages taken), all int32. A negative last value:
     the stack was short by so many pages, nothing of the plan may be used."""
-    if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda or block_table.dim() != 2:
-        raise ValueError("block_table must be a CUDA tensor [B, max_pages]")
-    device, (B, max_pages) = block_table.device, block_table.shape
-    _int32(block_table, "block_table", device)
-    for t, n in ((nk, "nk"), (n_new, "n_new"), (held, "held")):
-        _int32(t, n, device, (B,))
-    _int32(free_pages, "free_pages", device)
-    _int32(free_count, "free_count", device)
-    if free_count.numel() != 1 or free_pages.dim() != 1:
-        raise ValueError("free_pages must be 1-D and free_count one value")
-    num_tokens = int(num_tokens)
-    with _Call(device, stream) as st:
-        if num_tokens < 0:
-            raise ValueError("num_tokens must not be negative")
-        nk_out, held_out = torch.empty_like(nk), torch.empty_like(held)
-        cu = torch.empty(B + 1, dtype=torch.int32, device=device)
-        slots = torch.empty(num_tokens, dtype=torch.int32, device=device)
-        free_out = torch.empty_like(free_count)
-        rc = lib().kv_plan_paged(_ptr(nk), _ptr(n_new), _ptr(block_table), _ptr(held), _ptr(free_pages), _ptr(free_count),
-                                 _ptr(nk_out), _ptr(held_out), _ptr(cu), _ptr(slots), _ptr(free_out), B, int(page_size),
-                                 max_pages, free_pages.numel(), num_tokens, st)
+    dev = _first(block_table, "block_table", 2)
+    return _run(dev, stream, _plan, dev, nk, n_new, block_table, held, free_pages, free_count, int(page_size), int(num_tokens))
+
+
+def _plan(st, dev, nk, n_new, table, held, free_pages, free_count, page_size, num_tokens):
+    B, max_pages = table.shape
+    if num_tokens < 0 or free_pages.dim() != 1:
+        raise ValueError("num_tokens must not be negative, free_pages 1-D")
+    args = (_like(nk, "nk", dev, _I32, (B,)), _like(n_new, "n_new", dev, _I32, (B,)), _like(table, "block_table", dev, _I32),
+            _like(held, "held", dev, _I32, (B,)), _like(free_pages, "free_pages", dev, _I32),
+            _like(free_count, "free_count", dev, _I32))
+    if free_count.numel() != 1:
+        raise ValueError("free_count must be one value")
+    nk_out, held_out, free_out = torch.empty_like(nk), torch.empty_like(held), torch.empty_like(free_count)
+    cu = torch.empty(B + 1, dtype=_I32, device=dev)
+    slots = torch.empty(num_tokens, dtype=_I32, device=dev)
+    rc = (_lib or lib()).kv_plan_paged(*args, nk_out.data_ptr(), held_out.data_ptr(), cu.data_ptr(), slots.data_ptr(),
+                                       free_out.data_ptr(), B, page_size, max_pages, free_pages.numel(), num_tokens, st)
+    if rc:
         _check(rc, "kv_plan_paged")
     return nk_out, held_out, cu, slots, free_out
 
 
-def _append(k_new, v_new, slots, k_pages, v_pages, k_scale, v_scale, rows, stream, fp8):
-    if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda or k_pages.dim() != 4:
-        raise ValueError("k_pages and v_pages must be CUDA tensors [num_pages, page_size, Hkv, d]")
-    device = k_pages.device
+def _append(st, dev, k_new, v_new, slots, k_pages, v_pages, k_scale, v_scale, rows, fp8):
     num_pages, page_size, Hkv, d = k_pages.shape
-    if tuple(v_pages.shape) != tuple(k_pages.shape) or v_pages.device != device:
-        raise ValueError("v_pages must be like k_pages")
+    dtype = k_pages.dtype
+    if dtype not in _FP8_CODES if fp8 else dtype is not _BF16:
+        raise ValueError("pages must hold " + ("E4M3 codes (uint8 or float8_e4m3fn)" if fp8 else "bf16") + f", got {dtype}")
+    kp = _like(k_pages, "k_pages", dev, dtype)
+    vp = _like(v_pages, "v_pages", dev, dtype, k_pages.shape)
+    n = k_new.shape[0]
+    ks = _rows(k_new, "k_new", dev, (n, Hkv, d))
+    vs = _rows(v_new, "v_new", dev, (n, Hkv, d))
+    sp = _like(slots, "slots", dev, _I32)
+    rp = None if rows is None else _like(rows, "rows", dev, _I32, slots.shape)
+    L = _lib or lib()
     if fp8:
-        _fp8_cache(k_pages, v_pages, k_scale, v_scale, Hkv, d, ("k_pages", "v_pages"))
-        if k_scale.device != device or v_scale.device != device:
-            raise ValueError(f"k_scale and v_scale must be on {device}")
+        scales = (_like(k_scale, "k_scale", dev, _F32, (Hkv, d)), _like(v_scale, "v_scale", dev, _F32, (Hkv, d)))
+        rc = L.kv_append_paged_fp8(k_new.data_ptr(), v_new.data_ptr(), sp, rp, kp, vp, *scales, slots.numel(), n, page_size,
+                                   num_pages, Hkv, d, ks, vs, st)
     else:
-        _cuda(k_pages, "k_pages", torch.bfloat16)
-        _cuda(v_pages, "v_pages", torch.bfloat16)
-    ks = _rows(k_new, "k_new", device, Hkv, d)
-    vs = _rows(v_new, "v_new", device, Hkv, d)
-    if v_new.shape[0] != k_new.shape[0]:
-        raise ValueError("k_new and v_new must have the same number of rows")
-    _int32(slots, "slots", device)
-    n = slots.numel()
-    if rows is not None:
-        _int32(rows, "rows", device, tuple(slots.shape))
-    with _Call(device, stream) as st:
-        if fp8:
-            rc = lib().kv_append_paged_fp8(_ptr(k_new), _ptr(v_new), _ptr(slots), _ptr(rows), _ptr(k_pages), _ptr(v_pages),
-                                           _ptr(k_scale), _ptr(v_scale), n, k_new.shape[0], page_size, num_pages, Hkv, d,
-                                           ks, vs, st)
-        else:
-            rc = lib().kv_append_paged(_ptr(k_new), _ptr(v_new), _ptr(slots), _ptr(rows), _ptr(k_pages), _ptr(v_pages), n,
-                                       k_new.shape[0], page_size, num_pages, Hkv, d, ks, vs, st)
+        rc = L.kv_append_paged(k_new.data_ptr(), v_new.data_ptr(), sp, rp, kp, vp, slots.numel(), n, page_size, num_pages,
+                               Hkv, d, ks, vs, st)
+    if rc:
         _check(rc, "kv_append_paged_fp8" if fp8 else "kv_append_paged")
     return k_pages, v_pages
 
@@ -681,14 +673,18 @@ def kv_append_paged(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tenso
                     v_pages: torch.Tensor, rows: torch.Tensor | None = None, stream=None):
     """Writes K and V rows [n, Hkv, d] bf16 into the pages: slot slots[i] takes row rows[i] (default i);
     slots and rows out of range are skipped. Returns (k_pages, v_pages), written in place."""
-    return _append(k_new, v_new, slots, k_pages, v_pages, None, None, rows, stream, False)
+    dev = _first(k_pages, "k_pages", 4)
+    _first(k_new, "k_new", 3)
+    return _run(dev, stream, _append, dev, k_new, v_new, slots, k_pages, v_pages, None, None, rows, False)
 
 
 def kv_append_paged_fp8(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor, k_pages: torch.Tensor,
                         v_pages: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
                         rows: torch.Tensor | None = None, stream=None):
     """``kv_append_paged`` into pages of E4M3 codes: code = nearest E4M3 value of x / scale[head, channel]."""
-    return _append(k_new, v_new, slots, k_pages, v_pages, k_scale, v_scale, rows, stream, True)
+    dev = _first(k_pages, "k_pages", 4)
+    _first(k_new, "k_new", 3)
+    return _run(dev, stream, _append, dev, k_new, v_new, slots, k_pages, v_pages, k_scale, v_scale, rows, True)
 
 
 def get_status(stream=None) -> int:

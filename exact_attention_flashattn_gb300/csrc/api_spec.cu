@@ -48,7 +48,7 @@ int tree_impl(const void* q, const void* k, const void* v, const void* k_new, co
   if (!row_stride(q_stride, static_cast<int64_t>(Hq) * d) || !row_stride(k_new_stride, static_cast<int64_t>(Hkv) * d) ||
       !row_stride(v_new_stride, static_cast<int64_t>(Hkv) * d))
     return BWATTN_ERR_INVALID_ARG;
-  if (workspace_bytes < bw::tree_ws_bytes(num_seqs, max_nodes, g, d)) return BWATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < bw::tree_ws_bytes(max_nodes, g, d)) return BWATTN_ERR_INVALID_ARG;
   bw::TreeArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);
@@ -77,6 +77,7 @@ int tree_impl(const void* q, const void* k, const void* v, const void* k_new, co
   a.max_pages = max_pages;
   a.num_pages = num_pages;
   a.scale_log2 = scale * bw::kLog2e;
+  if (bw::tree_most_tiles(a) > 0x7fffffff) return BWATTN_ERR_UNSUPPORTED;
   return done(bw::launch_tree(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
@@ -120,7 +121,7 @@ extern "C" {
 
 size_t attn_tree_workspace_size(int num_seqs, int max_nodes, int Hq, int Hkv, int d) {
   if (num_seqs <= 0 || max_nodes <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || !head_dim(d)) return 0;
-  return bw::tree_ws_bytes(num_seqs, max_nodes, Hq / Hkv, d);
+  return bw::tree_ws_bytes(max_nodes, Hq / Hkv, d);
 }
 
 int attn_tree(const void* q, const void* kcache, const void* vcache, const void* k_new, const void* v_new, void* o,

@@ -138,6 +138,18 @@ cudaError_t launch_prefill_tc256(const TcFwdArgs& a, unsigned int* status, unsig
 constexpr int kTreeMaxNodes = 1024;  // drafted nodes a sequence
 constexpr int kTreeRows = 128;
 constexpr int kTreeMaxCtas = 152;    // persistent CTAs, at most one per SM
+constexpr int kTreeMergeBytes = 8192;
+// What the merge has to do at the boundary between CTA c - 1 and CTA c, written by CTA c: something
+// if that is the first boundary inside a unit.
+struct TreeMergeRec {
+  int rows0, rows1;      // rows of the unit's row tiles (rows0 0: nothing to merge)
+  int node0, node_step;  // packed row of the tiles' first node: node0 + w node_step
+  int hkv;
+  int slot0;             // CTA c - 1 has its part in this slot, the later CTAs in slot 0
+  int last;              // the last CTA with a part
+  int pad;
+};
+static_assert(sizeof(TreeMergeRec) == 32 && kTreeMaxCtas * sizeof(TreeMergeRec) <= kTreeMergeBytes, "merge records");
 struct TreeArgs {
   CUtensorMap tm_q;        // {d, Hq, total_q}, box {64, g, kTreeRows / g}
   CUtensorMap tm_k, tm_v;  // contiguous {d, cap, B * Hkv}, box {64, tile keys, 1}; paged {d, Hkv, pool rows},
@@ -155,7 +167,7 @@ struct TreeArgs {
   const uint64_t* mask;   // [total_q, mask_words]: bit j = draft j of the node's own sequence is seen
   const int32_t* block_table;  // paged cache when non-null: [num_seqs, max_pages]
   int64_t q_stride, k_new_stride, v_new_stride;
-  int64_t* base;          // workspace: [num_seqs + 1] tiles before each sequence, and in all
+  TreeMergeRec* merge;    // workspace: [ctas]
   float* partial;         // workspace: [ctas][2][row tiles][kTreeRows * (d + 2)]
   int num_seqs, total_q, max_nodes, mask_words;
   int Hq, Hkv, g, d;
@@ -171,10 +183,16 @@ struct TreeArgs {
 // Row tiles of a unit: two (d <= 128) when a sequence may fill more than one, so that the K and V
 // tiles of a unit serve twice the rows.
 inline int tree_row_tiles(int max_nodes, int g, int d) { return d <= 128 && max_nodes > kTreeRows / g ? 2 : 1; }
-inline size_t tree_base_bytes(int num_seqs) { return (static_cast<size_t>(num_seqs) * 8 + 8 + 255) / 256 * 256; }
-inline size_t tree_ws_bytes(int num_seqs, int max_nodes, int g, int d) {
-  return tree_base_bytes(num_seqs) +
+inline size_t tree_ws_bytes(int max_nodes, int g, int d) {
+  return kTreeMergeBytes +
          static_cast<size_t>(kTreeMaxCtas) * 2 * tree_row_tiles(max_nodes, g, d) * kTreeRows * (d + 2) * sizeof(float);
+}
+// The most key tiles that the lengths of a call may make (int in the kernel: the host refuses more).
+inline int64_t tree_most_tiles(const TreeArgs& a) {
+  const int keys = a.d == 256 ? 64 : 128, unit_nodes = tree_row_tiles(a.max_nodes, a.g, a.d) * (kTreeRows / a.g);
+  const int64_t seqs = a.num_seqs < a.total_q ? a.num_seqs : a.total_q;
+  return a.Hkv * (seqs + a.total_q / unit_nodes) *
+         ((static_cast<int64_t>(a.kv_cap) + keys - 1) / keys + (a.max_nodes + keys - 1) / keys);
 }
 // Fills the maps and sizes that follow from the others, launches the attention and the merge.
 cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream);
@@ -233,9 +251,9 @@ void count_launch();
 // when the request exceeds the ticket pool: the caller then launches the merge kernel).
 cudaError_t merge_tickets(int n, unsigned int** out);
 // 3-D bf16 tensor map {d, dim1, dim2} with strides in elements, box {64, box1, box2}, 128-byte
-// swizzle, zero fill out of bounds.
+// swizzle, zero fill out of bounds. `narrow`: L2 fetches of 128 bytes instead of 256.
 cudaError_t make_map_bf16(CUtensorMap* m, const void* base, int d, int64_t dim1, int64_t dim2, int64_t stride1_elems,
-                          int64_t stride2_elems, int box1, int box2);
+                          int64_t stride2_elems, int box1, int box2, bool narrow = false);
 // The device status word of the current device and the bound on a kernel's waits.
 cudaError_t status_word(unsigned int** out);
 uint64_t wait_timeout_ns();

@@ -23,8 +23,11 @@
 // Inside a CTA two streams run, each with its own S and O in tensor memory, its own MMA issuing warp
 // and its own softmax warpgroup (thread = row = TMEM lane):
 //   kTiles == 2   stream w is row tile w; both read the same K and V tiles.
-//   kTiles == 1   both streams have the same rows; the even key tiles go to stream 0, the odd ones to
-//                 stream 1, whose o is added to stream 0's through shared memory at the unit's end.
+//   kTiles == 1   both streams have the same rows; of the CTA's key tiles the even ones go to stream 0,
+//                 the odd ones to stream 1 (counted over all its units, so that a ring slot always
+//                 serves the same stream: a stream's waits on a slot's barrier then never skip a
+//                 phase, which their parity could not tell from the one before), and stream 1's o is
+//                 added to stream 0's through shared memory at the unit's end.
 //   d == 256      (O alone takes half of tensor memory) one stream of 64-key tiles, two S buffers.
 // A stream's S -> softmax -> P.V is a serial chain per tile; two of them, out of step, cover it. A
 // producer warp streams K and V tiles (TMA, 128-byte swizzle; from a paged cache one copy per run of
@@ -62,12 +65,20 @@ struct Cfg {
   static constexpr uint32_t kXml = kXch + (kExchange ? kTreeRows * D * 4 : 0);
   static constexpr uint32_t kBar = kXml + (kExchange ? kTreeRows * 8 : 0);
   static constexpr uint32_t kSmem = kBar + kBarBytes + 1024;  // + alignment slack
-  static constexpr int kTmaWarp = 4 * kStreams;
+  static constexpr int kTmaWarp = 4 * kStreams;  // K tiles, Q and the list of segments
   static constexpr int kMmaWarp = kTmaWarp + 1;
-  static constexpr int kThreads = 32 * (5 * kStreams + 1);
-  // tensor memory columns; P (bf16 pairs) takes the place of the S it was made from
+  static constexpr int kTmaVWarp = kMmaWarp + kStreams;
+  static constexpr int kWarps = kTmaVWarp + 1;
+  static constexpr int kThreads = 32 * kWarps;
+  // S of a stream's next tile is issued ahead of the P.V of its current one where tensor memory has
+  // the room: at d = 256 into the other S buffer, at d = 64 into the same one once the softmax has
+  // read it, P having columns of its own
+  static constexpr bool kSplitP = D == 64;
+  static constexpr bool kLook = D != 128;
+  // tensor memory columns; without kSplitP, P (bf16 pairs) takes the place of the S it was made from
   static constexpr uint32_t kColS = D == 256 ? 256 : 0;  // two buffers of kKeys columns
   static constexpr uint32_t kColO = D == 256 ? 0 : 256;  // stream w: + w D
+  static constexpr uint32_t kColP = 384;                 // kSplitP, stream w: + w 64
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(kTiles == 1 || D <= 128, "tiles");
 };
@@ -75,6 +86,7 @@ struct Cfg {
 // A run of key tiles of one unit, published by the producer warp to the other roles.
 struct Seg {
   int valid;        // 0: the CTA's list is exhausted
+  int b;            // the sequence
   int tok0, nq, nk; // the sequence's first node, nodes, context keys
   int hkv, node0;   // KV head; first node (within the sequence) of the unit
   int k0, nt, ct;   // tiles [k0, k0 + nt) of the unit; its first ct tiles are context
@@ -85,7 +97,9 @@ struct Seg {
 struct Barriers {
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2];
-  uint64_t pv_done[2];  // one stream (d = 256): P.V of S buffer x has completed
+  uint64_t s_free[2];   // kSplitP: the softmax has read S
+  uint64_t pv_done[2];  // kLook: the P.V of buffer (stream) x has completed
+  uint64_t turn[2];     // two row tiles at d = 128: P.V turns, 0: stream 0 to 1, 1: back
   uint64_t o_full[2], o_empty[2];
   uint64_t xch_full, xch_empty;
   uint64_t mma_done[2];
@@ -93,9 +107,8 @@ struct Barriers {
   uint64_t v_ready[8];  // two row tiles: stream 0 has looked over the V tile of the slot
   uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
   Seg seg[kSegSlots];
-  int64_t scan[12];
-  int64_t first_tiles;  // tiles before the sequence of the CTA's first tile
-  int first_seq;
+  int scan[12];
+  int list[3];  // tiles of all sequences; the sequence of the CTA's first tile; tiles before it
   uint32_t tmem_base;
   int abort;
 };
@@ -108,7 +121,7 @@ struct SeqTiles {
   int tok0, nq, nk;
   int ct, per_unit;  // context tiles, all tiles of a unit
   int row_units;     // units of a KV head
-  __device__ __forceinline__ int64_t all(int Hkv) const { return static_cast<int64_t>(per_unit) * row_units * Hkv; }
+  __device__ __forceinline__ int all(int Hkv) const { return per_unit * row_units * Hkv; }  // the host bounds the sum
 };
 template <int D, int kTiles>
 __device__ __forceinline__ SeqTiles seq_tiles(const TreeArgs& a, int b) {
@@ -124,10 +137,20 @@ __device__ __forceinline__ SeqTiles seq_tiles(const TreeArgs& a, int b) {
   return s;
 }
 
-// CTAs that share T tiles (none without a tile); the first tile of CTA c of G; the CTA that has tile x.
-__device__ __forceinline__ int ctas_of(int64_t T, int most) { return static_cast<int>(max(min(T, static_cast<int64_t>(most)), static_cast<int64_t>(1))); }
-__device__ __forceinline__ int64_t cta_begin(int64_t c, int64_t T, int G) { return c * T / G; }
-__device__ __forceinline__ int cta_of(int64_t x, int64_t T, int G) { return static_cast<int>(((x + 1) * G + T - 1) / T) - 1; }
+// T tiles over at most `most` CTAs, none without a tile: the first T % G CTAs take one more.
+struct Share {
+  int G, per, rem;
+  __device__ __forceinline__ Share(int T, int most) {
+    G = max(min(T, most), 1);
+    per = T / G;
+    rem = T - per * G;
+  }
+  __device__ __forceinline__ int begin(int c) const { return c * per + min(c, rem); }
+  __device__ __forceinline__ int owner(int x) const {
+    const int t = rem * (per + 1);
+    return x < t ? x / (per + 1) : rem + (x - t) / per;
+  }
+};
 
 // One copy by the calling lane (the wrapper in ptx.cuh elects one lane of a converged warp).
 __device__ __forceinline__ void tma_load_3d_lane(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
@@ -189,7 +212,6 @@ template <int D, int kTiles>
 __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
   using C = Cfg<D, kTiles>;
   constexpr int kStreams = C::kStreams, kKeys = C::kKeys, kStages = C::kStages;
-  constexpr int kWarps = C::kThreads / 32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
@@ -199,25 +221,32 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
 
   asm volatile("griddepcontrol.launch_dependents;");  // the merge waits for this grid to complete
 
-  // ---- the list of tiles: every thread sums the tiles of a run of sequences
-  const int run = (a.num_seqs + C::kThreads - 1) / C::kThreads;
-  const int run0 = min(tid * run, a.num_seqs), run1 = min(run0 + run, a.num_seqs);
-  int64_t mine = 0;
-  for (int b = run0; b < run1; ++b) mine += seq_tiles<D, kTiles>(a, b).all(a.Hkv);
-  int64_t incl = mine;
+  // ---- the list of tiles: a thread sums the tiles of a run of sequences. Up to 128 sequences the
+  // producer warp does it alone (nobody else needs the list), beyond that the whole block
+  const bool wide = a.num_seqs > 128;
+  const int run = wide ? (a.num_seqs + C::kThreads - 1) / C::kThreads : (a.num_seqs + 31) / 32;
+  const int run0 = min((wide ? tid : lane) * run, a.num_seqs), run1 = min(run0 + run, a.num_seqs);
+  int mine = 0, incl = 0;
+  if (wide || warp == C::kTmaWarp) {
+#pragma unroll 4
+    for (int b = run0; b < run1; ++b) mine += seq_tiles<D, kTiles>(a, b).all(a.Hkv);
+    incl = mine;
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += x;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += x;
+    }
+    if (wide && lane == 31) bar->scan[warp] = incl;
   }
-  if (lane == 31) bar->scan[warp] = incl;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->q_full[i], 1);
       mbar_init(&bar->q_empty[i], kTiles == 2 ? 1 : kStreams);
       mbar_init(&bar->s_full[i], 1);
       mbar_init(&bar->p_full[i], kTreeRows);
+      mbar_init(&bar->s_free[i], kTreeRows);
       mbar_init(&bar->pv_done[i], 1);
+      mbar_init(&bar->turn[i], 1);
       mbar_init(&bar->o_full[i], 1);
       mbar_init(&bar->o_empty[i], kTreeRows);
       mbar_init(&bar->mma_done[i], 1);
@@ -231,10 +260,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
     }
     for (int i = 0; i < kSegSlots; ++i) {
       mbar_init(&bar->seg_full[i], 1);
-      mbar_init(&bar->seg_empty[i], 5 * kStreams);  // the MMA warps and the softmax warps
+      mbar_init(&bar->seg_empty[i], 5 * kStreams + 1);  // the softmax and MMA warps, the V producer
     }
-    bar->first_seq = 0;
-    bar->first_tiles = 0;
     bar->abort = 0;
     fence_mbar_init();
   }
@@ -245,35 +272,29 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int64_t T = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) before = T;
-    T += bar->scan[w];
-  }
-  before += incl - mine;  // tiles before this thread's run
-  const int G = ctas_of(T, a.ctas);
-  const int64_t begin = blockIdx.x < G ? cta_begin(blockIdx.x, T, G) : T, end = blockIdx.x < G ? cta_begin(blockIdx.x + 1, T, G) : T;
-  if (blockIdx.x == 0) {  // for the merge
-    int64_t at = before;
-    for (int b = run0; b < run1; ++b) {
-      a.base[b] = at;
-      at += seq_tiles<D, kTiles>(a, b).all(a.Hkv);
+  if (wide || warp == C::kTmaWarp) {
+    int T = __shfl_sync(0xffffffffu, incl, 31), before = incl - mine;
+    if (wide) {
+      T = 0;
+      for (int w = 0; w < C::kWarps; ++w) {
+        if (w == warp) before += T;
+        T += bar->scan[w];
+      }
     }
-    if (tid == 0) a.base[a.num_seqs] = T;
-  }
-  if (begin < end && before <= begin && begin < before + mine) {
-    int64_t at = before;
-    int b = run0;
-    for (;; ++b) {
-      const int64_t n = seq_tiles<D, kTiles>(a, b).all(a.Hkv);
-      if (begin < at + n) break;
-      at += n;
+    const Share share(T, a.ctas);
+    const int begin = share.begin(blockIdx.x);
+    if (static_cast<int>(blockIdx.x) < share.G && before <= begin && begin < before + mine) {
+      int b = run0;
+      for (int n; begin >= before + (n = seq_tiles<D, kTiles>(a, b).all(a.Hkv)); ++b) before += n;
+      bar->list[1] = b;
+      bar->list[2] = before;
     }
-    bar->first_seq = b;
-    bar->first_tiles = at;
+    if (wide ? tid == 0 : lane == 0) bar->list[0] = T;
+    if (wide)
+      __syncthreads();
+    else
+      __syncwarp();
   }
-  __syncthreads();
   const uint32_t tbase = bar->tmem_base;
   volatile int* abort = &bar->abort;
   const uint64_t tmo = a.timeout_ns;
@@ -291,8 +312,61 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
   // rows of the unit's row tile w that exist
   auto tile_rows = [&](const Seg& s, int w) { return max(0, min(tile_nodes, s.nq - s.node0 - w * tile_nodes)) * a.g; };
 
+  // K (kv = 0) or V (1) of a segment's tiles into the even or odd ring slots; `n` counts the tiles over
+  // all segments. Two warps, because a lane's copy of 16 rows takes its warp about 70 ns to issue and a
+  // tile out of 16-row pages is 8 to 16 such copies of K and as many of V (one warp for both held the
+  // paged d = 128 cache at 4400 GB/s where a contiguous one ran at 6270).
+  auto load_tiles = [&](const Seg& s, int kv, int& n, auto before_tile) -> bool {
+    const CUtensorMap* old_map = kv ? &a.tm_v : &a.tm_k;
+    const CUtensorMap* new_map = kv ? &a.tm_vn : &a.tm_kn;
+    // paged: this lane's copy is atom lane % kHalves of piece lane / kHalves of a tile; the pool row of
+    // the piece in the next tile is looked up one tile ahead
+    const int hfl = lane % C::kHalves, my_piece = (lane / C::kHalves) * a.piece;
+    auto pool_row = [&](int kt) -> int {
+      const int key = kt * kKeys + my_piece;
+      if (!a.block_table || my_piece >= kKeys || kt >= s.ct || key >= s.nk) return -1;
+      int page = a.block_table[static_cast<int64_t>(s.b) * a.max_pages + key / a.page_size];
+      page = min(max(page, 0), a.num_pages - 1);  // a bad entry reads a wrong page, never outside the pool
+      return page * a.page_size + key % a.page_size;
+    };
+    int row_next = pool_row(s.k0);
+    for (int j = 0; j < s.nt; ++j, ++n) {
+      if (!before_tile(j)) return false;
+      const int kt = s.k0 + j, row = row_next;
+      if (a.block_table) row_next = pool_row(kt + 1);
+      const int i = 2 * n + kv, slot = i % kStages, round = i / kStages;
+      if (round > 0 && !vote(mbar_wait(&bar->kv_empty[slot], (round - 1) & 1, tmo, abort))) return false;
+      uint8_t* dst = sRing + slot * C::kTileBytes;
+      if (kt >= s.ct) {
+        mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(a.new_box) * 128 * C::kHalves);
+        for (int hf = 0; hf < C::kHalves; ++hf)
+          tma_load_3d(dst + hf * (kKeys * 128), new_map, &bar->kv_full[slot], 64 * hf, s.hkv, s.tok0 + (kt - s.ct) * kKeys);
+      } else if (a.block_table) {
+        // pieces past the last key are not copied: their K scores are masked, their V rows zeroed
+        const int pieces = min(kKeys / a.piece, (s.nk - kt * kKeys + a.piece - 1) / a.piece);
+        mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(pieces * a.piece) * 128 * C::kHalves);
+        __syncwarp();
+        if (row >= 0)
+          tma_load_3d_lane(dst + hfl * (kKeys * 128) + my_piece * 128, old_map, &bar->kv_full[slot], 64 * hfl, s.hkv, row);
+        __syncwarp();
+      } else {
+        mbar_arrive_expect_tx(&bar->kv_full[slot], C::kTileBytes);
+        for (int hf = 0; hf < C::kHalves; ++hf)
+          tma_load_3d(dst + hf * (kKeys * 128), old_map, &bar->kv_full[slot], 64 * hf, kt * kKeys, s.b * a.Hkv + s.hkv);
+      }
+    }
+    return true;
+  };
+  // the copies a producer warp issued last, of n tiles in all, have landed
+  auto drain = [&](int kv, int n) {
+    for (int t = max(0, n - kStages / 2); t < n; ++t) {
+      const int i = 2 * t + kv;
+      mbar_wait(&bar->kv_full[i % kStages], (i / kStages) & 1, tmo, &no_abort);
+    }
+  };
+
   if (warp == C::kTmaWarp) {
-    // ------------------------------------------------------------ TMA producer
+    // ------------------------------------------------------------ segments, Q and K tiles
     if (lane == 0) {
       prefetch_tmap(&a.tm_q);
       prefetch_tmap(&a.tm_k);
@@ -300,33 +374,47 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       prefetch_tmap(&a.tm_kn);
       prefetch_tmap(&a.tm_vn);
     }
-    int64_t pos = begin, seq_at = bar->first_tiles;
-    int b = bar->first_seq;
-    int nload = 0, segs = 0;
+    const Share share(bar->list[0], a.ctas);
+    const int c = blockIdx.x, begin = c < share.G ? share.begin(c) : 0, end = c < share.G && bar->list[0] > 0 ? share.begin(c + 1) : 0;
+    int pos = begin, b = pos < end ? bar->list[1] : 0, seq_at = pos < end ? bar->list[2] : 0;
+    int nload = 0, nq[2] = {0, 0};  // K tiles, and Q tiles into each buffer
     bool ok = true;
+    if (begin == end && lane == 0) a.merge[c] = TreeMergeRec{};  // no part here
     for (int k = 0; ok; ++k) {
       Seg s{};
-      int b_seg = 0;
       if (pos < end) {
         SeqTiles q = seq_tiles<D, kTiles>(a, b);
         while (pos >= seq_at + q.all(a.Hkv)) {
           seq_at += q.all(a.Hkv);
           q = seq_tiles<D, kTiles>(a, ++b);
         }
-        const int64_t local = pos - seq_at;
-        const int unit = static_cast<int>(local / q.per_unit);
+        const int local = pos - seq_at, unit = local / q.per_unit;
         s.valid = 1;
+        s.b = b;
         s.tok0 = q.tok0;
         s.nq = q.nq;
         s.nk = q.nk;
         s.hkv = unit / q.row_units;
-        s.node0 = unit % q.row_units * (kTiles * tile_nodes);
-        s.k0 = static_cast<int>(local % q.per_unit);
-        s.nt = static_cast<int>(min(static_cast<int64_t>(q.per_unit - s.k0), end - pos));
+        s.node0 = (unit - s.hkv * q.row_units) * (kTiles * tile_nodes);
+        s.k0 = local - unit * q.per_unit;
+        s.nt = min(q.per_unit - s.k0, end - pos);
         s.ct = q.ct;
         s.slot = s.nt == q.per_unit ? -1 : (pos == begin ? 0 : 1);
-        b_seg = b;
         pos += s.nt;
+        if (k == 0 && lane == 0) {
+          TreeMergeRec r{};
+          const int u0 = begin - s.k0;
+          if (s.k0 > 0 && share.owner(u0) == c - 1) {
+            r.rows0 = tile_rows(s, 0);
+            r.rows1 = kTiles == 2 ? tile_rows(s, 1) : 0;
+            r.node0 = s.tok0 + s.node0;
+            r.node_step = tile_nodes;
+            r.hkv = s.hkv;
+            r.slot0 = u0 == share.begin(c - 1) ? 0 : 1;
+            r.last = share.owner(u0 + q.per_unit - 1);
+          }
+          a.merge[c] = r;
+        }
       }
       if (k >= kSegSlots && !(ok = vote(mbar_wait(&bar->seg_empty[k % kSegSlots], (k / kSegSlots - 1) & 1, tmo, abort))))
         break;
@@ -339,69 +427,40 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       auto load_q = [&]() -> bool {
 #pragma unroll
         for (int w = 0; w < kTiles; ++w) {
-          if (segs > 0 && !vote(mbar_wait(&bar->q_empty[w], (segs - 1) & 1, tmo, abort))) return false;
+          if (nq[w] > 0 && !vote(mbar_wait(&bar->q_empty[w], (nq[w] - 1) & 1, tmo, abort))) return false;
           mbar_arrive_expect_tx(&bar->q_full[w], static_cast<uint32_t>(tile_nodes * a.g) * 128 * C::kHalves);
           for (int hf = 0; hf < C::kHalves; ++hf)
             tma_load_3d(sQ + w * C::kQBytes + hf * (kTreeRows * 128), &a.tm_q, &bar->q_full[w], 64 * hf, s.hkv * a.g,
                         s.tok0 + s.node0 + w * tile_nodes);
+          ++nq[w];
         }
-        ++segs;
         return true;
       };
-      // paged: this lane's copy is atom lane % kHalves of piece lane / kHalves of a tile; the pool row of
-      // the piece in the next tile is looked up one tile ahead
-      const int my_piece = (lane / C::kHalves) * a.piece;
-      auto pool_row = [&](int kt) -> int {
-        const int key = kt * kKeys + my_piece;
-        if (!a.block_table || my_piece >= kKeys || kt >= s.ct || key >= s.nk) return -1;
-        int page = a.block_table[static_cast<int64_t>(b_seg) * a.max_pages + key / a.page_size];
-        page = min(max(page, 0), a.num_pages - 1);  // a bad entry reads a wrong page, never outside the pool
-        return page * a.page_size + key % a.page_size;
-      };
-      int row_next = pool_row(s.k0);
       const int q_at = min(s.nt, kStages / 4);  // the first loads need ring slots only, not Q's buffer
-      for (int j = 0; j < s.nt && ok; ++j) {
-        if (j == q_at && !(ok = load_q())) break;
-        const int kt = s.k0 + j;
-        const int row = row_next;
-        if (a.block_table) row_next = pool_row(kt + 1);
-        for (int kv = 0; kv < 2; ++kv, ++nload) {
-          const int slot = nload % kStages, round = nload / kStages;
-          if (round > 0 && !(ok = vote(mbar_wait(&bar->kv_empty[slot], (round - 1) & 1, tmo, abort)))) break;
-          uint8_t* dst = sRing + slot * C::kTileBytes;
-          if (kt >= s.ct) {
-            const CUtensorMap* map = kv ? &a.tm_vn : &a.tm_kn;
-            mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(a.new_box) * 128 * C::kHalves);
-            for (int hf = 0; hf < C::kHalves; ++hf)
-              tma_load_3d(dst + hf * (kKeys * 128), map, &bar->kv_full[slot], 64 * hf, s.hkv, s.tok0 + (kt - s.ct) * kKeys);
-          } else if (a.block_table) {
-            // pieces past the last key are not copied: their K scores are masked, their V rows zeroed
-            const int pieces = min(kKeys / a.piece, (s.nk - kt * kKeys + a.piece - 1) / a.piece);
-            const CUtensorMap* map = kv ? &a.tm_v : &a.tm_k;
-            mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(pieces * a.piece) * 128 * C::kHalves);
-            __syncwarp();
-            if (row >= 0) {
-              const int hf = lane % C::kHalves;
-              tma_load_3d_lane(dst + hf * (kKeys * 128) + my_piece * 128, map, &bar->kv_full[slot], 64 * hf, s.hkv, row);
-            }
-            __syncwarp();
-          } else {
-            const CUtensorMap* map = kv ? &a.tm_v : &a.tm_k;
-            mbar_arrive_expect_tx(&bar->kv_full[slot], C::kTileBytes);
-            for (int hf = 0; hf < C::kHalves; ++hf)
-              tma_load_3d(dst + hf * (kKeys * 128), map, &bar->kv_full[slot], 64 * hf, kt * kKeys, b_seg * a.Hkv + s.hkv);
-          }
-        }
-      }
-      if (ok && q_at == s.nt && !(ok = load_q())) break;
+      ok = load_tiles(s, 0, nload, [&](int j) { return j != q_at || load_q(); });
+      if (ok && q_at == s.nt) ok = load_q();
     }
     if (!ok && lane == 0) raise_timeout(abort, a.status);
-    // every copy this CTA issued must have landed before the CTA may exit
-    if (segs > 0)
-      for (int w = 0; w < kTiles; ++w) mbar_wait(&bar->q_full[w], (segs - 1) & 1, tmo, &no_abort);
-    for (int i = max(0, nload - kStages); i < nload; ++i)
-      mbar_wait(&bar->kv_full[i % kStages], (i / kStages) & 1, tmo, &no_abort);
-  } else if (warp >= C::kMmaWarp) {
+    // every copy this warp issued must have landed before the CTA may exit
+#pragma unroll
+    for (int w = 0; w < kTiles; ++w)
+      if (nq[w] > 0) mbar_wait(&bar->q_full[w], (nq[w] - 1) & 1, tmo, &no_abort);
+    drain(0, nload);
+  } else if (warp == C::kTmaVWarp) {
+    // ------------------------------------------------------------ V tiles
+    int nload = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const Seg* sp = wait_seg(k);
+      if (!(ok = sp != nullptr)) break;
+      const Seg s = *sp;
+      release_seg(k);
+      if (!s.valid) break;
+      ok = load_tiles(s, 1, nload, [](int) { return true; });
+    }
+    if (!ok && lane == 0) raise_timeout(abort, a.status);
+    drain(1, nload);
+  } else if (warp >= C::kMmaWarp && warp < C::kTmaVWarp) {
     // ------------------------------------------------------------ MMA issuers, one per stream
     const int w = warp - C::kMmaWarp;
     constexpr uint32_t idesc_qk = idesc_bf16_f32(kTreeRows, kKeys, 0, 0);
@@ -413,14 +472,14 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
     constexpr uint32_t slot_step = C::kTileBytes >> 4;
     const uint32_t tO = tbase + C::kColO + w * D;
     const int qb = kTiles == 2 ? w : 0;
-    int nload = 0, ns = 0, np = 0, ou = 0;
+    int nload = 0, ns = 0, np = 0, ou = 0, nturn = 0;
     bool ok = true;
     auto wait_load = [&](int i) -> bool {
       const bool r = vote(mbar_wait(&bar->kv_full[i % kStages], (i / kStages) & 1, tmo, abort));
       tc_fence_after();
       return r;
     };
-    // S and P buffer of a stream's n-th tile, and how often the buffer was used before
+    // S buffer of a stream's n-th tile, and how often the buffer was used before
     auto buf = [&](int n) { return kStreams == 2 ? w : n & 1; };
     auto use = [&](int n) { return kStreams == 2 ? n : n >> 1; };
     auto issue_s = [&](int i) {
@@ -433,8 +492,18 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       umma_commit(&bar->kv_empty[i % kStages]);
       ++ns;
     };
+    // S of load i, once its K has landed and (kSplitP) the softmax has read the previous S
+    auto start_s = [&](int i) -> bool {
+      if (!wait_load(i)) return false;
+      if (C::kSplitP && ns > 0) {
+        if (!vote(mbar_wait(&bar->s_free[w], (ns - 1) & 1, tmo, abort))) return false;
+        tc_fence_after();
+      }
+      issue_s(i);
+      return true;
+    };
     auto issue_pv = [&](int i, bool accumulate) {
-      const uint32_t tP = tbase + C::kColS + buf(np) * kKeys;
+      const uint32_t tP = tbase + (C::kSplitP ? C::kColP + w * 64 : C::kColS + buf(np) * kKeys);
       const uint32_t vl = v_lo + (i % kStages) * slot_step;
       if constexpr (kKeys == 128) {
         umma_ts_k128(tO, tP, vl, hi, idesc_pv, accumulate ? 1u : 0u);
@@ -442,7 +511,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
 #pragma unroll
         for (int s = 0; s < kKeys / 16; ++s) umma_ts(tO, tP + 8 * s, vl + 128 * s, hi, idesc_pv, (accumulate || s) ? 1u : 0u);
       }
-      if constexpr (kStreams == 1) umma_commit(&bar->pv_done[buf(np)]);
+      if constexpr (C::kLook) umma_commit(&bar->pv_done[buf(np)]);
       ++np;
     };
     for (int k = 0; ok; ++k) {
@@ -459,13 +528,13 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       nload += 2 * s.nt;
       // this stream's tiles: j0, j0 + step, ... below s.nt
       const int step = C::kExchange ? 2 : 1;
-      const int j0 = C::kExchange ? w : 0;
+      const int j0 = C::kExchange ? (base / 2 + w) & 1 : 0;
       const bool idle = kTiles == 2 && tile_rows(s, w) == 0;  // no rows: only gives the slots back
       if (idle || j0 >= s.nt) umma_commit(&bar->q_empty[qb]);
-      if (!idle && j0 < s.nt && kStreams == 1) {
-        if (!(ok = wait_load(base))) break;
-        issue_s(base);
-        if (s.nt == 1) umma_commit(&bar->q_empty[qb]);
+      const bool turns = kTiles == 2 && !C::kLook && tile_rows(s, 1) > 0;
+      if (C::kLook && !idle && j0 < s.nt) {
+        if (!(ok = start_s(base + 2 * j0))) break;
+        if (j0 + step >= s.nt) umma_commit(&bar->q_empty[qb]);
       }
       for (int j = j0; j < s.nt; j += step) {
         const int ik = base + 2 * j, iv = ik + 1;
@@ -476,16 +545,13 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
           umma_commit(&bar->kv_empty[iv % kStages]);
           continue;
         }
-        if constexpr (kStreams == 2) {
+        if constexpr (!C::kLook) {
           // the stream's previous P.V was issued before, so this S may overwrite its P
-          if (!(ok = wait_load(ik))) break;
-          issue_s(ik);
+          if (!(ok = start_s(ik))) break;
           if (j + step >= s.nt) umma_commit(&bar->q_empty[qb]);
-        } else if (j + 1 < s.nt) {
-          // S of the next tile goes ahead of this tile's P.V, into the other buffer
-          if (!(ok = wait_load(ik + 2))) break;
-          issue_s(ik + 2);
-          if (j + 2 == s.nt) umma_commit(&bar->q_empty[qb]);
+        } else if (j + step < s.nt) {
+          if (!(ok = start_s(ik + 2 * step))) break;
+          if (j + 2 * step >= s.nt) umma_commit(&bar->q_empty[qb]);
         }
         if (!(ok = wait_load(iv))) break;
         // V rows that do not count, and drafts' infinities and NaN (two row tiles read one V tile:
@@ -505,9 +571,21 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
           if (!(ok = vote(mbar_wait(&bar->v_ready[iv % kStages], (iv / kStages) & 1, tmo, abort)))) break;
         }
         if (j == j0 && ou > 0 && !(ok = vote(mbar_wait(&bar->o_empty[w], (ou - 1) & 1, tmo, abort)))) break;
+        // two row tiles: P.V in turns (0, 1, 0, ...), which keeps the streams out of step, one's softmax
+        // beside the other's MMAs
+        if (turns) {
+          if (w == 1 ? !(ok = vote(mbar_wait(&bar->turn[0], nturn & 1, tmo, abort)))
+                     : nturn > 0 && !(ok = vote(mbar_wait(&bar->turn[1], (nturn - 1) & 1, tmo, abort))))
+            break;
+        }
         if (!(ok = vote(mbar_wait(&bar->p_full[buf(np)], use(np) & 1, tmo, abort)))) break;
         tc_fence_after();
         issue_pv(iv, j > j0);
+        if (turns) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->turn[w]);
+          ++nturn;
+        }
         umma_commit(&bar->kv_empty[iv % kStages]);
         if (j + step >= s.nt) {
           umma_commit(&bar->o_full[w]);
@@ -530,7 +608,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
     const float sl2 = a.scale_log2;
     float* xo = reinterpret_cast<float*>(smem + C::kXch);   // [D][kTreeRows]
     float2* xml = reinterpret_cast<float2*>(smem + C::kXml);  // [kTreeRows]
-    int n = 0, oused = 0, xn = 0;
+    int n = 0, oused = 0, xn = 0, tiles = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const Seg* sp = wait_seg(k);
@@ -551,11 +629,14 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       const int head = s.hkv * a.g + min(row, rows - 1) % a.g;
       const uint64_t* bits = a.mask + static_cast<int64_t>(s.tok0 + node) * a.mask_words;
       const int step = C::kExchange ? 2 : 1;
-      const int j0 = C::kExchange ? w : 0;
+      const int first = tiles & 1;  // the stream of the segment's first tile
+      const int j0 = C::kExchange ? first ^ w : 0;
+      tiles += s.nt;
       float m_ref = -INFINITY, l = 0.f;
       for (int j = j0; j < s.nt; j += step) {
         const int x = kStreams == 2 ? w : n & 1, phase = (kStreams == 2 ? n : n >> 1) & 1;
         const uint32_t tS = tbase + lane_base + C::kColS + x * kKeys;
+        const uint32_t tP = C::kSplitP ? tbase + lane_base + C::kColP + w * 64 : tS;
         if (!(ok = vote(mbar_wait(&bar->s_full[x], phase, tmo, abort)))) break;
         tc_fence_after();
         if (warp_ok) {
@@ -565,6 +646,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < kKeys / 32; ++c) tmem_reg_fence(sc[c]);
+          if constexpr (C::kSplitP) {
+            tc_fence_before();
+            mbar_arrive(&bar->s_free[x]);  // S is in registers
+          }
           const int kt = s.k0 + j;
           const uint32_t ninf = __float_as_uint(-INFINITY);
           if (kt >= s.ct) {
@@ -611,6 +696,11 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
             m_ref = m_new;
           }
           const float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
+          if (C::kSplitP && n > 0) {
+            // the stream's previous P.V has read the P columns, and O holds it
+            if (!(ok = vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort)))) break;
+            tc_fence_after();
+          }
           // p = 2^(s scale log2e - m) as bf16 pairs into the first half of the S columns; l is the fp32
           // sum before that rounding
           float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -625,7 +715,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
               fadd2(ls[(2 * e) & 7], ls[(2 * e + 1) & 7], p0, p1);
               pk[e] = pack_bf16x2(p0, p1);
             }
-            tmem_st16(tS + 16 * c, pk);
+            tmem_st16(tP + 16 * c, pk);
           }
           // O must carry the new reference maximum before this tile's P.V (rare)
           if (__any_sync(0xffffffffu, alpha_o != 1.f)) {
@@ -648,6 +738,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
           }
           tmem_wait_st();
           l += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
+        } else if (C::kSplitP) {
+          // a warp without rows may not run ahead either: its arrivals for the next P would count for this
+          mbar_arrive(&bar->s_free[x]);
+          if (n > 0 && !(ok = vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort)))) break;
         }
         tc_fence_before();
         mbar_arrive(&bar->p_full[x]);
@@ -661,7 +755,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
         ++oused;
         tc_fence_after();
       }
-      const bool exchange = C::kExchange && s.nt > 1;
+      const bool exchange = C::kExchange && (s.nt > 1 || first == 1);  // stream 1 had a tile
       if (exchange && w == 1) {
         // stream 1 hands its state over
         if (xn > 0 && !(ok = vote(mbar_wait(&bar->xch_empty, (xn - 1) & 1, tmo, abort)))) break;
@@ -684,7 +778,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
         release_seg(k);
         continue;
       }
-      if (C::kExchange && w == 1) {  // one tile: stream 0 has it
+      if (C::kExchange && w == 1) {  // stream 0 had the only tile
         release_seg(k);
         continue;
       }
@@ -708,15 +802,21 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
         float* part = a.partial + ((static_cast<int64_t>(blockIdx.x) * 2 + max(s.slot, 0)) * kTiles + rw) * (kTreeRows * (D + 2));
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-          uint32_t ov[32];
-          tmem_ld32(tO + c * 32, ov);
-          tmem_wait_ld();
-          tmem_reg_fence(ov);
           float o[32];
+          if (have_o) {
+            uint32_t ov[32];
+            tmem_ld32(tO + c * 32, ov);
+            tmem_wait_ld();
+            tmem_reg_fence(ov);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            o[e] = __uint_as_float(ov[e]);
-            if (exchange) o[e] = o[e] * f0 + xo[(c * 32 + e) * kTreeRows + row] * f1;
+            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]) * f0;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          if (exchange) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] += xo[(c * 32 + e) * kTreeRows + row] * f1;
           }
           if (bad && row_ok) {
             // the infinities and NaN among the drafts that this row sees
@@ -766,72 +866,75 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
   }
 }
 
-// The parts of units that several CTAs shared: one CTA per 32 rows of a row tile; lanes are rows,
-// each warp takes every eighth channel quad. m = max m_c, l = sum l_c 2^(m_c - m), o likewise.
-constexpr int kMergeThreads = 256;
-template <int D, int kTiles>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeArgs a, int row_units) {
-  constexpr int kQ = D / 4 / (kMergeThreads / 32);  // channel quads per thread
-  __shared__ __align__(16) uint16_t out[32][D + 8];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results are complete and visible
+// The parts of units that several CTAs shared. At most one unit per boundary between two CTAs has to
+// be merged, so the grid is (boundaries, quarters of a row tile x row tiles, groups of 32 channels),
+// whatever the lengths. Lanes are rows; the warps share out the parts, each with its own running
+// maximum, and are joined in shared memory in their order:
+//   m = max m_c, l = sum l_c 2^(m_c - m), o likewise.
+constexpr int kMergeWarps = 8;
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const float* partial, const TreeMergeRec* merge, uint16_t* out,
+                                                                       float* lse, int D, int tiles, int g, int Hq) {
+  __shared__ float4 sm_o[kMergeWarps][8][33];  // 33: the joining threads' columns fall on different banks
+  __shared__ float2 sm_ml[kMergeWarps][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts and records are complete and visible
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int idx = blockIdx.x;
-  const int quarter = idx % 4;
-  idx /= 4;
-  const int w = idx % kTiles;
-  idx /= kTiles;
-  const int ru = idx % row_units;
-  idx /= row_units;
-  const int hkv = idx % a.Hkv, b = idx / a.Hkv;
-  const SeqTiles q = seq_tiles<D, kTiles>(a, b);
-  const int tile_nodes = kTreeRows / a.g;
-  const int node0 = (ru * kTiles + w) * tile_nodes;
-  const int rows = max(0, min(tile_nodes, q.nq - node0)) * a.g;
+  const int c = blockIdx.x + 1, w = blockIdx.y >> 2, quarter = blockIdx.y & 3, cg = blockIdx.z;
+  const int4 r0 = __ldcg(reinterpret_cast<const int4*>(merge + c)), r1 = __ldcg(reinterpret_cast<const int4*>(merge + c) + 1);
+  const int rows = w ? r0.y : r0.x, hkv = r1.x, slot0 = r1.y, last = r1.z;
   if (32 * quarter >= rows) return;
-  const int64_t T = a.base[a.num_seqs];
-  const int64_t u0 = a.base[b] + (static_cast<int64_t>(hkv) * q.row_units + ru) * q.per_unit;
-  const int G = ctas_of(T, a.ctas);
-  const int c0 = cta_of(u0, T, G), c1 = cta_of(u0 + q.per_unit - 1, T, G);
-  if (c0 == c1) return;  // written by its CTA
   const int row = 32 * quarter + lane;
-  const bool row_ok = row < rows;
-  const int slot0 = u0 <= cta_begin(c0, T, G) ? 0 : 1;
-  constexpr int64_t kPart = kTreeRows * (D + 2);
-  auto part = [&](int c) { return a.partial + ((static_cast<int64_t>(c) * 2 + (c == c0 ? slot0 : 0)) * kTiles + w) * kPart; };
+  const int64_t size = kTreeRows * (D + 2);
   float m = -INFINITY, l = 0.f;
-  float4 acc[kQ];
+  float4 acc[8];
 #pragma unroll
-  for (int i = 0; i < kQ; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (row_ok) {
-    for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(part(c) + kTreeRows * D + 2 * row));
-    for (int c = c0; c <= c1; ++c) {
-      const float* p = part(c);
+  for (int q = 0; q < 8; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (row < rows) {
+    for (int x = c - 1 + warp; x <= last; x += kMergeWarps) {
+      const float* p = partial + ((static_cast<int64_t>(x) * 2 + (x == c - 1 ? slot0 : 0)) * tiles + w) * size;
       const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + kTreeRows * D + 2 * row));
-      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-      l += ml.y * f;
+      float4 v[8];
 #pragma unroll
-      for (int i = 0; i < kQ; ++i) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(p + ((warp + 8 * i) * kTreeRows + row) * 4));
-        acc[i].x += v.x * f;
-        acc[i].y += v.y * f;
-        acc[i].z += v.z * f;
-        acc[i].w += v.w * f;
+      for (int q = 0; q < 8; ++q) v[q] = __ldcg(reinterpret_cast<const float4*>(p + ((cg * 8 + q) * kTreeRows + row) * 4));
+      const float mn = fmaxf(m, ml.x);
+      const float f0 = m == -INFINITY ? 0.f : ex2(m - mn), f1 = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
+      m = mn;
+      l = l * f0 + ml.y * f1;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        acc[q].x = acc[q].x * f0 + v[q].x * f1;
+        acc[q].y = acc[q].y * f0 + v[q].y * f1;
+        acc[q].z = acc[q].z * f0 + v[q].z * f1;
+        acc[q].w = acc[q].w * f0 + v[q].w * f1;
       }
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  sm_ml[warp][lane] = make_float2(m, l);
 #pragma unroll
-  for (int i = 0; i < kQ; ++i)
-    *reinterpret_cast<uint2*>(&out[lane][4 * (warp + 8 * i)]) =
-        make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
-  auto out_row = [&](int r) { return static_cast<int64_t>(q.tok0 + node0 + r / a.g) * a.Hq + hkv * a.g + r % a.g; };
-  if (warp == 0 && row_ok && a.lse) a.lse[out_row(row)] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  for (int q = 0; q < 8; ++q) sm_o[warp][q][lane] = acc[q];
   __syncthreads();
-  for (int it = threadIdx.x; it < 32 * (D / 8); it += kMergeThreads) {
-    const int r = it / (D / 8), c = it % (D / 8);
-    if (32 * quarter + r < rows)
-      *reinterpret_cast<uint4*>(a.o + out_row(32 * quarter + r) * D + 8 * c) = *reinterpret_cast<const uint4*>(&out[r][8 * c]);
+  // thread = (row, channel quad): 8 threads write a row's 64 bytes
+  const int jr = threadIdx.x >> 3, jq = threadIdx.x & 7;
+  if (32 * quarter + jr >= rows) return;
+  const int used = min(kMergeWarps, last - c + 2);
+  float M = -INFINITY, L = 0.f;
+  for (int x = 0; x < used; ++x) M = fmaxf(M, sm_ml[x][jr].x);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int x = 0; x < used; ++x) {
+    const float2 ml = sm_ml[x][jr];
+    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+    const float4 v = sm_o[x][jq][jr];
+    L += ml.y * f;
+    o.x += v.x * f;
+    o.y += v.y * f;
+    o.z += v.z * f;
+    o.w += v.w * f;
   }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int rr = 32 * quarter + jr;
+  const int64_t orow = static_cast<int64_t>(r0.z + w * r0.w + rr / g) * Hq + hkv * g + rr % g;
+  *reinterpret_cast<uint2*>(out + orow * D + cg * 32 + 4 * jq) =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (lse && cg == 0 && jq == 0) lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 template <int D, int kTiles>
@@ -842,18 +945,19 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
   tree_kernel<D, kTiles><<<a.ctas, C::kThreads, C::kSmem, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   count_launch();
-  const int unit_nodes = kTiles * (kTreeRows / a.g);
-  const int row_units = (a.max_nodes + unit_nodes - 1) / unit_nodes;
+  if (a.ctas == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.num_seqs) * a.Hkv * row_units * kTiles * 4));
-  cfg.blockDim = dim3(kMergeThreads);
+  cfg.gridDim = dim3(a.ctas - 1, 4 * kTiles, D / 32);
+  cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, kTiles>, a, row_units)) == cudaSuccess) count_launch();
+  e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, static_cast<const float*>(a.partial), static_cast<const TreeMergeRec*>(a.merge), a.o,
+                         a.lse, D, kTiles, a.g, a.Hq);
+  if (e == cudaSuccess) count_launch();
   return e;
 }
 
@@ -863,8 +967,8 @@ cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
   cudaError_t e = status_word(&a.status);
   if (e != cudaSuccess) return e;
   a.timeout_ns = wait_timeout_ns();
-  a.base = static_cast<int64_t*>(workspace);
-  a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + tree_base_bytes(a.num_seqs));
+  a.merge = static_cast<TreeMergeRec*>(workspace);
+  a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kTreeMergeBytes);
   const int d = a.d, keys = d == 256 ? 64 : 128;
   if ((e = make_map_bf16(&a.tm_q, a.q, d, a.Hq, a.total_q, d, a.q_stride, a.g, kTreeRows / a.g)) != cudaSuccess) return e;
   a.new_box = a.max_nodes < keys ? (a.max_nodes + 7) / 8 * 8 : keys;
@@ -878,8 +982,10 @@ cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
     a.piece = 16;
     while (a.piece < keys && a.page_size % (2 * a.piece) == 0) a.piece *= 2;
     const int64_t rows = static_cast<int64_t>(a.num_pages) * a.page_size, step = static_cast<int64_t>(a.Hkv) * d;
-    if ((e = make_map_bf16(&a.tm_k, a.k, d, a.Hkv, rows, d, step, 1, a.piece)) != cudaSuccess ||
-        (e = make_map_bf16(&a.tm_v, a.v, d, a.Hkv, rows, d, step, 1, a.piece)) != cudaSuccess)
+    // a head's row is 128 bytes at d = 64: wider fetches would bring the next head's along
+    const bool narrow = d == 64;
+    if ((e = make_map_bf16(&a.tm_k, a.k, d, a.Hkv, rows, d, step, 1, a.piece, narrow)) != cudaSuccess ||
+        (e = make_map_bf16(&a.tm_v, a.v, d, a.Hkv, rows, d, step, 1, a.piece, narrow)) != cudaSuccess)
       return e;
   } else {
     const int64_t heads = static_cast<int64_t>(a.num_seqs) * a.Hkv, step = static_cast<int64_t>(a.kv_cap) * d;
@@ -892,9 +998,7 @@ cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   const int tiles = tree_row_tiles(a.max_nodes, a.g, d);
   // no more CTAs than tiles there can be
-  const int unit_nodes = tiles * (kTreeRows / a.g);
-  const int64_t most = static_cast<int64_t>(a.num_seqs) * a.Hkv * ((a.max_nodes + unit_nodes - 1) / unit_nodes) *
-                       ((a.kv_cap + keys - 1) / keys + (a.max_nodes + keys - 1) / keys);
+  const int64_t most = tree_most_tiles(a);  // no more CTAs than tiles there can be
   a.ctas = static_cast<int>(most < kTreeMaxCtas ? most : kTreeMaxCtas);
   if (a.ctas > sms) a.ctas = sms;
   if (d == 64) return tiles == 2 ? launch<64, 2>(a, stream) : launch<64, 1>(a, stream);

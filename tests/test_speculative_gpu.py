@@ -339,6 +339,24 @@ def test_tree_graph_and_streams():
     a.check(outs[0][0], outs[0][1])
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,page,nodes", [(8, 8, 128, 0, 9), (8, 8, 128, 16, 9), (32, 8, 128, 16, 64), (8, 8, 64, 0, 9),
+                                                 (32, 8, 64, 48, 40), (8, 8, 256, 0, 9), (8, 8, 256, 16, 9)])
+def test_tree_runs_of_segments(Hq, Hkv, d, page, nodes):
+    # every CTA walks through parts of several units of odd and even tile counts, over and over: the
+    # hand-over of ring slots, buffers and streams from unit to unit
+    r = np.random.default_rng(d + nodes)
+    nk = [int(x) for x in r.integers(0, 6000, 24)]
+    n = [int(x) for x in r.integers(1, nodes + 1, 24)]
+    c = Case(Hq, Hkv, d, page, nk, n, "tree", seed=73)
+    o, lse = c.run()
+    c.check(o, lse)
+    want = o[:sum(n)].clone()
+    for _ in range(40):
+        o.zero_()
+        c.run(out=o)
+        assert torch.equal(o[:sum(n)], want)
+
+
 def test_tree_many_sequences():
     r = np.random.default_rng(5)
     nk = [int(x) for x in r.integers(0, 60, 700)]
