@@ -482,17 +482,21 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
     // S buffer of a stream's n-th tile, and how often the buffer was used before
     auto buf = [&](int n) { return kStreams == 2 ? w : n & 1; };
     auto use = [&](int n) { return kStreams == 2 ? n : n >> 1; };
+    // S of load i, whose K has landed
     auto issue_s = [&](int i) {
       const uint32_t kl = k_lo + (i % kStages) * slot_step;
       const uint32_t tS = tbase + C::kColS + buf(ns) * kKeys;
+      if constexpr (D == 128) {
+        umma_ss_k128(tS, q_lo, hi, kl, hi, idesc_qk, 0);
+      } else {
 #pragma unroll
-      for (int hf = 0; hf < C::kHalves; ++hf)
-        umma_ss_k64(tS, q_lo + hf * (kTreeRows * 128 / 16), hi, kl + hf * (kKeys * 128 / 16), hi, idesc_qk, hf > 0);
+        for (int hf = 0; hf < C::kHalves; ++hf)
+          umma_ss_k64(tS, q_lo + hf * (kTreeRows * 128 / 16), hi, kl + hf * (kKeys * 128 / 16), hi, idesc_qk, hf > 0);
+      }
       umma_commit(&bar->s_full[buf(ns)]);
-      umma_commit(&bar->kv_empty[i % kStages]);
       ++ns;
     };
-    // S of load i, once its K has landed and (kSplitP) the softmax has read the previous S
+    // the same, once its K has landed and (kSplitP) the softmax has read the previous S
     auto start_s = [&](int i) -> bool {
       if (!wait_load(i)) return false;
       if (C::kSplitP && ns > 0) {
@@ -530,28 +534,28 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       const int step = C::kExchange ? 2 : 1;
       const int j0 = C::kExchange ? (base / 2 + w) & 1 : 0;
       const bool idle = kTiles == 2 && tile_rows(s, w) == 0;  // no rows: only gives the slots back
-      if (idle || j0 >= s.nt) umma_commit(&bar->q_empty[qb]);
       const bool turns = kTiles == 2 && !C::kLook && tile_rows(s, 1) > 0;
-      if (C::kLook && !idle && j0 < s.nt) {
+      if (idle || j0 >= s.nt) {
+        umma_commit(&bar->q_empty[qb]);
+      } else {
         if (!(ok = start_s(base + 2 * j0))) break;
         if (j0 + step >= s.nt) umma_commit(&bar->q_empty[qb]);
       }
       for (int j = j0; j < s.nt; j += step) {
         const int ik = base + 2 * j, iv = ik + 1;
+        if (idle && !(ok = wait_load(ik))) break;
+        umma_commit(&bar->kv_empty[ik % kStages]);  // S of this tile was issued before
         if (idle) {
-          if (!(ok = wait_load(ik))) break;
-          umma_commit(&bar->kv_empty[ik % kStages]);
           if (!(ok = wait_load(iv))) break;
           umma_commit(&bar->kv_empty[iv % kStages]);
           continue;
         }
-        if constexpr (!C::kLook) {
-          // the stream's previous P.V was issued before, so this S may overwrite its P
-          if (!(ok = start_s(ik))) break;
-          if (j + step >= s.nt) umma_commit(&bar->q_empty[qb]);
-        } else if (j + step < s.nt) {
-          if (!(ok = start_s(ik + 2 * step))) break;
-          if (j + 2 * step >= s.nt) umma_commit(&bar->q_empty[qb]);
+        const int inext = ik + 2 * step;
+        const bool more = j + step < s.nt, last_s = j + 2 * step >= s.nt;
+        if (C::kLook && more) {
+          // S of the next tile goes ahead of this tile's P.V
+          if (!(ok = start_s(inext))) break;
+          if (last_s) umma_commit(&bar->q_empty[qb]);
         }
         if (!(ok = wait_load(iv))) break;
         // V rows that do not count, and drafts' infinities and NaN (two row tiles read one V tile:
@@ -570,7 +574,6 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
         } else if (special) {
           if (!(ok = vote(mbar_wait(&bar->v_ready[iv % kStages], (iv / kStages) & 1, tmo, abort)))) break;
         }
-        if (j == j0 && ou > 0 && !(ok = vote(mbar_wait(&bar->o_empty[w], (ou - 1) & 1, tmo, abort)))) break;
         // two row tiles: P.V in turns (0, 1, 0, ...), which keeps the streams out of step, one's softmax
         // beside the other's MMAs
         if (turns) {
@@ -578,6 +581,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
                      : nturn > 0 && !(ok = vote(mbar_wait(&bar->turn[1], (nturn - 1) & 1, tmo, abort))))
             break;
         }
+        if (j == j0 && ou > 0 && !(ok = vote(mbar_wait(&bar->o_empty[w], (ou - 1) & 1, tmo, abort)))) break;
         if (!(ok = vote(mbar_wait(&bar->p_full[buf(np)], use(np) & 1, tmo, abort)))) break;
         tc_fence_after();
         issue_pv(iv, j > j0);
@@ -586,11 +590,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
           if (lane == 0) mbar_arrive(&bar->turn[w]);
           ++nturn;
         }
-        umma_commit(&bar->kv_empty[iv % kStages]);
-        if (j + step >= s.nt) {
+        if (!more) {
           umma_commit(&bar->o_full[w]);
           ++ou;
+        } else if (!C::kLook) {
+          // S of the next tile overwrites P: it follows this P.V in the warp's stream
+          if (!(ok = start_s(inext))) break;
+          if (last_s) umma_commit(&bar->q_empty[qb]);
         }
+        umma_commit(&bar->kv_empty[iv % kStages]);
       }
       if (!ok) break;
       release_seg(k);
