@@ -151,7 +151,7 @@ struct TreeMergeRec {
 };
 static_assert(sizeof(TreeMergeRec) == 32 && kTreeMaxCtas * sizeof(TreeMergeRec) <= kTreeMergeBytes, "merge records");
 struct TreeArgs {
-  CUtensorMap tm_q;        // {d, Hq, total_q}, box {64, g, kTreeRows / g}
+  CUtensorMap tm_q;        // {d, Hq, total_q}, box {64, g, tile_rows / g}
   CUtensorMap tm_k, tm_v;  // contiguous {d, cap, B * Hkv}, box {64, tile keys, 1}; paged {d, Hkv, pool rows},
                            // box {64, 1, piece}
   CUtensorMap tm_kn, tm_vn;  // {d, Hkv, total_q}, box {64, 1, new_box}
@@ -173,6 +173,7 @@ struct TreeArgs {
   int Hq, Hkv, g, d;
   int kv_cap;             // keys a sequence's cache can hold
   int page_size, max_pages, num_pages;
+  int tile_rows;          // tree_tile_rows(max_nodes, g, d)
   int piece;              // paged: rows of a copy, a power of two that divides page_size
   int new_box;            // rows of a copy of drafted rows
   int ctas;               // CTAs of the attention kernel
@@ -183,13 +184,17 @@ struct TreeArgs {
 // Row tiles of a unit: two (d <= 128) when a sequence may fill more than one, so that the K and V
 // tiles of a unit serve twice the rows.
 inline int tree_row_tiles(int max_nodes, int g, int d) { return d <= 128 && max_nodes > kTreeRows / g ? 2 : 1; }
+// Rows of a tile that hold nodes: 64 where no sequence has more (d <= 128).
+inline int tree_tile_rows(int max_nodes, int g, int d) {
+  return d <= 128 && static_cast<int64_t>(max_nodes) * g <= 64 ? 64 : kTreeRows;
+}
 inline size_t tree_ws_bytes(int max_nodes, int g, int d) {
   return kTreeMergeBytes +
          static_cast<size_t>(kTreeMaxCtas) * 2 * tree_row_tiles(max_nodes, g, d) * kTreeRows * (d + 2) * sizeof(float);
 }
 // The most key tiles that the lengths of a call may make (int in the kernel: the host refuses more).
 inline int64_t tree_most_tiles(const TreeArgs& a) {
-  const int keys = a.d == 256 ? 64 : 128, unit_nodes = tree_row_tiles(a.max_nodes, a.g, a.d) * (kTreeRows / a.g);
+  const int keys = a.d == 256 ? 64 : 128, unit_nodes = tree_row_tiles(a.max_nodes, a.g, a.d) * (tree_tile_rows(a.max_nodes, a.g, a.d) / a.g);
   const int64_t seqs = a.num_seqs < a.total_q ? a.num_seqs : a.total_q;
   return a.Hkv * (seqs + a.total_q / unit_nodes) *
          ((static_cast<int64_t>(a.kv_cap) + keys - 1) / keys + (a.max_nodes + keys - 1) / keys);

@@ -28,6 +28,9 @@
 //                 serves the same stream: a stream's waits on a slot's barrier then never skip a
 //                 phase, which their parity could not tell from the one before), and stream 1's o is
 //                 added to stream 0's through shared memory at the unit's end.
+//                 A tile of at most 64 rows is laid out twice, for stream 1 on lanes 64 to 127: a warp's
+//                 softmax costs the same for one row as for 32, so the streams share the SM's four
+//                 sub-partitions instead of two of them.
 //   d == 256      (O alone takes half of tensor memory) one stream of 64-key tiles, two S buffers.
 // A stream's S -> softmax -> P.V is a serial chain per tile; two of them, out of step, cover it. A
 // producer warp streams K and V tiles (TMA, 128-byte swizzle; from a paged cache one copy per run of
@@ -68,7 +71,10 @@ struct Cfg {
   static constexpr int kTmaWarp = 4 * kStreams;  // K tiles, Q and the list of segments
   static constexpr int kMmaWarp = kTmaWarp + 1;
   static constexpr int kTmaVWarp = kMmaWarp + kStreams;
-  static constexpr int kWarps = kTmaVWarp + 1;
+  // more warps that issue copies of K, and as many of V (with two row tiles the MMAs set the pace)
+  static constexpr int kHelpers = kTiles == 1 ? 2 : 0;
+  static constexpr int kHelpWarp = kTmaVWarp + 1;
+  static constexpr int kWarps = kHelpWarp + 2 * kHelpers;
   static constexpr int kThreads = 32 * kWarps;
   // S of a stream's next tile is issued ahead of the P.V of its current one where tensor memory has
   // the room: at d = 256 into the other S buffer, at d = 64 into the same one once the softmax has
@@ -104,10 +110,10 @@ struct Barriers {
   uint64_t xch_full, xch_empty;
   uint64_t mma_done[2];
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t v_ready[8];  // two row tiles: stream 0 has looked over the V tile of the slot
+  uint64_t v_ready[8];  // two row tiles: stream 0 has looked over the V tile, in turn for those that need it
   uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
   Seg seg[kSegSlots];
-  int scan[12];
+  int scan[16];
   int list[3];  // tiles of all sequences; the sequence of the CTA's first tile; tiles before it
   uint32_t tmem_base;
   int abort;
@@ -132,7 +138,7 @@ __device__ __forceinline__ SeqTiles seq_tiles(const TreeArgs& a, int b) {
   s.nk = min(max(a.nk[b], 0), a.kv_cap);
   s.ct = s.nk / kKeys + (s.nk % kKeys != 0);
   s.per_unit = s.ct + (s.nq + kKeys - 1) / kKeys;
-  const int unit_nodes = kTiles * (kTreeRows / a.g);
+  const int unit_nodes = kTiles * (a.tile_rows / a.g);
   s.row_units = (s.nq + unit_nodes - 1) / unit_nodes;  // 0 for a sequence without nodes
   return s;
 }
@@ -177,7 +183,7 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32
 template <int kHalves, int kKeys>
 __device__ __forceinline__ bool clean_v(uint8_t* tile, int valid, bool scan, int lane) {
   bool bad = false;
-#pragma unroll
+#pragma unroll 1
   for (int hf = 0; hf < kHalves; ++hf) {
     uint8_t* atom = tile + hf * (kKeys * 128);
     if (scan) {
@@ -208,6 +214,19 @@ __device__ __forceinline__ bool clean_v(uint8_t* tile, int valid, bool scan, int
   return __any_sync(0xffffffffu, bad);
 }
 
+// Registers: a softmax thread holds a row's 128 scores, the other eight warps of a block with helpers
+// little. Such a block of two streams has 512 x 128 of them; 256 x 184 + 256 x 72 is the same number.
+constexpr int kSoftRegs = 184, kOtherRegs = 72;
+static_assert(256 * kSoftRegs + 256 * kOtherRegs <= 512 * 128, "register split");
+template <bool kSplit>
+__device__ __forceinline__ void give_registers() {
+  if constexpr (kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+}
+template <bool kSplit>
+__device__ __forceinline__ void take_registers() {
+  if constexpr (kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+}
+
 template <int D, int kTiles>
 __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
   using C = Cfg<D, kTiles>;
@@ -217,7 +236,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
   uint8_t* sQ = smem;
   uint8_t* sRing = smem + C::kRing;
   Barriers* bar = reinterpret_cast<Barriers*>(smem + C::kBar);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   asm volatile("griddepcontrol.launch_dependents;");  // the merge waits for this grid to complete
 
@@ -260,7 +279,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
     }
     for (int i = 0; i < kSegSlots; ++i) {
       mbar_init(&bar->seg_full[i], 1);
-      mbar_init(&bar->seg_empty[i], 5 * kStreams + 1);  // the softmax and MMA warps, the V producer
+      mbar_init(&bar->seg_empty[i], 5 * kStreams + 1 + 2 * C::kHelpers);  // all but the K producer
     }
     bar->abort = 0;
     fence_mbar_init();
@@ -295,10 +314,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
     else
       __syncwarp();
   }
-  const uint32_t tbase = bar->tmem_base;
+  const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_base, 0);
   volatile int* abort = &bar->abort;
   const uint64_t tmo = a.timeout_ns;
-  const int tile_nodes = kTreeRows / a.g;
+  const int tile_nodes = a.tile_rows / a.g;
   const int no_abort = 0;
 
   // consumer side of the segment queue, called by a converged warp
@@ -313,15 +332,18 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
   auto tile_rows = [&](const Seg& s, int w) { return max(0, min(tile_nodes, s.nq - s.node0 - w * tile_nodes)) * a.g; };
 
   // K (kv = 0) or V (1) of a segment's tiles into the even or odd ring slots; `n` counts the tiles over
-  // all segments. Two warps, because a lane's copy of 16 rows takes its warp about 70 ns to issue and a
-  // tile out of 16-row pages is 8 to 16 such copies of K and as many of V (one warp for both held the
-  // paged d = 128 cache at 4400 GB/s where a contiguous one ran at 6270).
-  auto load_tiles = [&](const Seg& s, int kv, int& n, auto before_tile) -> bool {
+  // all segments. A lane's copy of 16 rows takes its warp about 70 ns to issue, and a tile out of 16-row
+  // pages is 8 to 16 such copies of K and as many of V, so kHelpers warps beside the K and the V producer
+  // take a share of them (a tile's one warp for both held the paged d = 128 cache at 4400 GB/s where a
+  // contiguous one ran at 6270). `member` 0 is the producer itself, which alone announces the bytes; a
+  // helper's copies may land before that, but the phase waits for the announcement.
+  auto load_tiles = [&](const Seg& s, int kv, int member, int& n, auto before_tile) -> bool {
     const CUtensorMap* old_map = kv ? &a.tm_v : &a.tm_k;
     const CUtensorMap* new_map = kv ? &a.tm_vn : &a.tm_kn;
-    // paged: this lane's copy is atom lane % kHalves of piece lane / kHalves of a tile; the pool row of
-    // the piece in the next tile is looked up one tile ahead
-    const int hfl = lane % C::kHalves, my_piece = (lane / C::kHalves) * a.piece;
+    // paged: this lane's copy (number lane (1 + kHelpers) + member) is atom `hfl` of a piece of a tile; the
+    // pool row of the piece in the next tile is looked up one tile ahead
+    const int copy = lane * (1 + C::kHelpers) + member;
+    const int hfl = copy % C::kHalves, my_piece = (copy / C::kHalves) * a.piece;
     auto pool_row = [&](int kt) -> int {
       const int key = kt * kKeys + my_piece;
       if (!a.block_table || my_piece >= kKeys || kt >= s.ct || key >= s.nk) return -1;
@@ -337,7 +359,11 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       const int i = 2 * n + kv, slot = i % kStages, round = i / kStages;
       if (round > 0 && !vote(mbar_wait(&bar->kv_empty[slot], (round - 1) & 1, tmo, abort))) return false;
       uint8_t* dst = sRing + slot * C::kTileBytes;
-      if (kt >= s.ct) {
+      if (member > 0) {
+        if (row >= 0)
+          tma_load_3d_lane(dst + hfl * (kKeys * 128) + my_piece * 128, old_map, &bar->kv_full[slot], 64 * hfl, s.hkv, row);
+        __syncwarp();
+      } else if (kt >= s.ct) {
         mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(a.new_box) * 128 * C::kHalves);
         for (int hf = 0; hf < C::kHalves; ++hf)
           tma_load_3d(dst + hf * (kKeys * 128), new_map, &bar->kv_full[slot], 64 * hf, s.hkv, s.tok0 + (kt - s.ct) * kKeys);
@@ -367,6 +393,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
 
   if (warp == C::kTmaWarp) {
     // ------------------------------------------------------------ segments, Q and K tiles
+    give_registers<C::kThreads == 512>();
     if (lane == 0) {
       prefetch_tmap(&a.tm_q);
       prefetch_tmap(&a.tm_k);
@@ -428,16 +455,18 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
 #pragma unroll
         for (int w = 0; w < kTiles; ++w) {
           if (nq[w] > 0 && !vote(mbar_wait(&bar->q_empty[w], (nq[w] - 1) & 1, tmo, abort))) return false;
-          mbar_arrive_expect_tx(&bar->q_full[w], static_cast<uint32_t>(tile_nodes * a.g) * 128 * C::kHalves);
-          for (int hf = 0; hf < C::kHalves; ++hf)
-            tma_load_3d(sQ + w * C::kQBytes + hf * (kTreeRows * 128), &a.tm_q, &bar->q_full[w], 64 * hf, s.hkv * a.g,
-                        s.tok0 + s.node0 + w * tile_nodes);
+          const int copies = kTreeRows / a.tile_rows;
+          mbar_arrive_expect_tx(&bar->q_full[w], static_cast<uint32_t>(copies * tile_nodes * a.g) * 128 * C::kHalves);
+          for (int i = 0; i < copies; ++i)
+            for (int hf = 0; hf < C::kHalves; ++hf)
+              tma_load_3d(sQ + w * C::kQBytes + hf * (kTreeRows * 128) + i * a.tile_rows * 128, &a.tm_q, &bar->q_full[w],
+                          64 * hf, s.hkv * a.g, s.tok0 + s.node0 + w * tile_nodes);
           ++nq[w];
         }
         return true;
       };
       const int q_at = min(s.nt, kStages / 4);  // the first loads need ring slots only, not Q's buffer
-      ok = load_tiles(s, 0, nload, [&](int j) { return j != q_at || load_q(); });
+      ok = load_tiles(s, 0, 0, nload, [&](int j) { return j != q_at || load_q(); });
       if (ok && q_at == s.nt) ok = load_q();
     }
     if (!ok && lane == 0) raise_timeout(abort, a.status);
@@ -446,8 +475,12 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
     for (int w = 0; w < kTiles; ++w)
       if (nq[w] > 0) mbar_wait(&bar->q_full[w], (nq[w] - 1) & 1, tmo, &no_abort);
     drain(0, nload);
-  } else if (warp == C::kTmaVWarp) {
-    // ------------------------------------------------------------ V tiles
+  } else if (warp >= C::kTmaVWarp) {
+    // ------------------------------------------------------------ V tiles, and the helpers (K's, then V's)
+    give_registers<C::kThreads == 512>();
+    const int help = warp - C::kHelpWarp;
+    const int kv = warp == C::kTmaVWarp || help >= C::kHelpers ? 1 : 0;
+    const int member = warp == C::kTmaVWarp ? 0 : 1 + (help & 1);
     int nload = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -456,12 +489,14 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       const Seg s = *sp;
       release_seg(k);
       if (!s.valid) break;
-      ok = load_tiles(s, 1, nload, [](int) { return true; });
+      if (member > 0 && !a.block_table) continue;  // a contiguous cache's tile is kHalves copies
+      ok = load_tiles(s, kv, member, nload, [](int) { return true; });
     }
     if (!ok && lane == 0) raise_timeout(abort, a.status);
-    drain(1, nload);
-  } else if (warp >= C::kMmaWarp && warp < C::kTmaVWarp) {
+    drain(kv, nload);
+  } else if (warp >= C::kMmaWarp) {
     // ------------------------------------------------------------ MMA issuers, one per stream
+    give_registers<C::kThreads == 512>();
     const int w = warp - C::kMmaWarp;
     constexpr uint32_t idesc_qk = idesc_bf16_f32(kTreeRows, kKeys, 0, 0);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(kTreeRows, D, 0, 1);
@@ -472,7 +507,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
     constexpr uint32_t slot_step = C::kTileBytes >> 4;
     const uint32_t tO = tbase + C::kColO + w * D;
     const int qb = kTiles == 2 ? w : 0;
-    int nload = 0, ns = 0, np = 0, ou = 0, nturn = 0;
+    int nload = 0, ns = 0, np = 0, ou = 0, nturn = 0, nspecial = 0;
     bool ok = true;
     auto wait_load = [&](int i) -> bool {
       const bool r = vote(mbar_wait(&bar->kv_full[i % kStages], (i / kStages) & 1, tmo, abort));
@@ -534,6 +569,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       const int step = C::kExchange ? 2 : 1;
       const int j0 = C::kExchange ? (base / 2 + w) & 1 : 0;
       const bool idle = kTiles == 2 && tile_rows(s, w) == 0;  // no rows: only gives the slots back
+      const int special_from = s.nk % kKeys ? s.ct - 1 : s.ct;
       const bool turns = kTiles == 2 && !C::kLook && tile_rows(s, 1) > 0;
       if (idle || j0 >= s.nt) {
         umma_commit(&bar->q_empty[qb]);
@@ -548,6 +584,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
         if (idle) {
           if (!(ok = wait_load(iv))) break;
           umma_commit(&bar->kv_empty[iv % kStages]);
+          nspecial += s.k0 + j >= special_from;
           continue;
         }
         const int inext = ik + 2 * step;
@@ -558,21 +595,22 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
           if (last_s) umma_commit(&bar->q_empty[qb]);
         }
         if (!(ok = wait_load(iv))) break;
-        // V rows that do not count, and drafts' infinities and NaN (two row tiles read one V tile:
-        // stream 0 looks it over for both)
-        const int kt = s.k0 + j;
-        const bool draft = kt >= s.ct;
-        const int valid = min(kKeys, draft ? s.nq - (kt - s.ct) * kKeys : s.nk - kt * kKeys);
-        const bool special = draft || valid < kKeys;
-        uint8_t* vtile = sRing + (iv % kStages) * C::kTileBytes;
-        if (kTiles == 1 || w == 0) {
-          if (special && clean_v<C::kHalves, kKeys>(vtile, valid, draft, lane) && lane == 0) atomicOr(&sp->bad, 1);
-          if (kTiles == 2) {
+        if (s.k0 + j >= special_from) {
+          // V rows that do not count, and drafts' infinities and NaN (two row tiles read one V tile:
+          // stream 0 looks it over for both)
+          const int kt = s.k0 + j;
+          const bool draft = kt >= s.ct;
+          uint64_t* ready = &bar->v_ready[nspecial % (kStages / 2)];
+          if (kTiles == 1 || w == 0) {
+            const int valid = min(kKeys, draft ? s.nq - (kt - s.ct) * kKeys : s.nk - kt * kKeys);
+            if (clean_v<C::kHalves, kKeys>(sRing + (iv % kStages) * C::kTileBytes, valid, draft, lane) && lane == 0)
+              atomicOr(&sp->bad, 1);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar->v_ready[iv % kStages]);
+            if (kTiles == 2 && lane == 0) mbar_arrive(ready);
+          } else if (!(ok = vote(mbar_wait(ready, (nspecial / (kStages / 2)) & 1, tmo, abort)))) {
+            break;
           }
-        } else if (special) {
-          if (!(ok = vote(mbar_wait(&bar->v_ready[iv % kStages], (iv / kStages) & 1, tmo, abort)))) break;
+          ++nspecial;
         }
         // two row tiles: P.V in turns (0, 1, 0, ...), which keeps the streams out of step, one's softmax
         // beside the other's MMAs
@@ -609,8 +647,11 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
     mbar_wait(&bar->mma_done[w], 0, tmo, &no_abort);
   } else {
     // ------------------------------------------------------------ softmax warpgroups
+    take_registers<C::kThreads == 512>();
     const int w = warp >> 2;
-    const int row = (warp & 3) * 32 + lane;  // = TMEM lane
+    // row of the tile: the TMEM lane, less 64 in stream 1 where a tile has 64 rows (it works on the second
+    // copy of them, on the other two of the SM's four sub-partitions)
+    const int row = (warp & 3) * 32 + lane - w * (kTreeRows - a.tile_rows);
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tO = tbase + lane_base + C::kColO + w * D;
     const float sl2 = a.scale_log2;
@@ -632,14 +673,16 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
         release_seg(k);
         continue;
       }
-      const bool row_ok = row < rows, warp_ok = (warp & 3) * 32 < rows;
-      const int node = s.node0 + rw * tile_nodes + min(row, rows - 1) / a.g;  // within the sequence
-      const int head = s.hkv * a.g + min(row, rows - 1) % a.g;
+      const bool row_ok = row >= 0 && row < rows, warp_ok = row - lane >= 0 && row - lane < rows;
+      const int some_row = min(max(row, 0), rows - 1);
+      const int node = s.node0 + rw * tile_nodes + some_row / a.g;  // within the sequence
+      const int head = s.hkv * a.g + some_row % a.g;
       const uint64_t* bits = a.mask + static_cast<int64_t>(s.tok0 + node) * a.mask_words;
       const int step = C::kExchange ? 2 : 1;
       const int first = tiles & 1;  // the stream of the segment's first tile
       const int j0 = C::kExchange ? first ^ w : 0;
       tiles += s.nt;
+      const int masked_from = s.nk % kKeys ? s.ct - 1 : s.ct;  // first tile with keys that some row does not see
       float m_ref = -INFINITY, l = 0.f;
       for (int j = j0; j < s.nt; j += step) {
         const int x = kStreams == 2 ? w : n & 1, phase = (kStreams == 2 ? n : n >> 1) & 1;
@@ -648,6 +691,32 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
         if (!(ok = vote(mbar_wait(&bar->s_full[x], phase, tmo, abort)))) break;
         tc_fence_after();
         if (warp_ok) {
+          const int kt = s.k0 + j;
+          if (kt >= masked_from) {
+            // keys that the row does not see become -inf in tensor memory, 32 at a time (rolled, and apart
+            // from the common path: code that is jumped over still costs the loop its instruction fetches):
+            // the context's last tile ends at nk, drafts go by the mask's bits, none past the last node
+            const bool draft = kt >= s.ct;
+            const int left = draft ? s.nq - (kt - s.ct) * kKeys : s.nk - kt * kKeys;
+#pragma unroll 1
+            for (int c = 0; c < kKeys / 32; ++c) {
+              const int rest = left - 32 * c;
+              uint32_t keep = rest >= 32 ? 0xffffffffu : rest > 0 ? (1u << rest) - 1u : 0u;
+              if (draft) {
+                const int bit = (kt - s.ct) * kKeys + 32 * c;  // of the row's mask
+                keep &= bit < 64 * a.mask_words ? static_cast<uint32_t>(bits[bit >> 6] >> (bit & 32)) : 0u;
+              }
+              uint32_t x[32];
+              tmem_ld32(tS + 32 * c, x);
+              tmem_wait_ld();
+              tmem_reg_fence(x);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(keep >> e & 1)) x[e] = __float_as_uint(-INFINITY);
+              tmem_st32(tS + 32 * c, x);
+            }
+            tmem_wait_st();
+          }
           uint32_t sc[kKeys / 32][32];
 #pragma unroll
           for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(tS + 32 * c, sc[c]);
@@ -657,32 +726,6 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
           if constexpr (C::kSplitP) {
             tc_fence_before();
             mbar_arrive(&bar->s_free[x]);  // S is in registers
-          }
-          const int kt = s.k0 + j;
-          const uint32_t ninf = __float_as_uint(-INFINITY);
-          if (kt >= s.ct) {
-            // drafts: 64 mask bits a word; none at or past the sequence's last node
-            const int d0 = (kt - s.ct) * kKeys;
-#pragma unroll
-            for (int h = 0; h < kKeys / 64; ++h) {
-              const int wi = d0 / 64 + h, left = s.nq - 64 * wi;
-              uint64_t m = wi < a.mask_words ? bits[wi] : 0;
-              if (left < 64) m = left > 0 ? m & ((1ull << left) - 1) : 0;
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const uint32_t mm = static_cast<uint32_t>(m >> (32 * c));
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!(mm >> e & 1)) sc[2 * h + c][e] = ninf;
-              }
-            }
-          } else if ((kt + 1) * kKeys > s.nk) {
-            const int left = s.nk - kt * kKeys;  // keys of the context's last tile
-#pragma unroll
-            for (int c = 0; c < kKeys / 32; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (32 * c + e >= left) sc[c][e] = ninf;
           }
           float mx[kKeys / 32];
 #pragma unroll
@@ -733,7 +776,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
               if (!ok) break;
               tc_fence_after();
             }
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t ov[32];
               tmem_ld32(tO + c * 32, ov);
@@ -745,14 +788,17 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
             }
           }
           tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bar->p_full[x]);
           l += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
-        } else if (C::kSplitP) {
-          // a warp without rows may not run ahead either: its arrivals for the next P would count for this
-          mbar_arrive(&bar->s_free[x]);
-          if (n > 0 && !(ok = vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort)))) break;
+        } else {
+          if constexpr (C::kSplitP) {
+            // a warp without rows may not run ahead either: its arrivals for the next P would count for this
+            mbar_arrive(&bar->s_free[x]);
+            if (n > 0 && !(ok = vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort)))) break;
+          }
+          mbar_arrive(&bar->p_full[x]);
         }
-        tc_fence_before();
-        mbar_arrive(&bar->p_full[x]);
         ++n;
       }
       if (!ok) break;
@@ -770,7 +816,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
         ++xn;
         if (warp_ok) {
           xml[row] = make_float2(m_ref, l);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t ov[32];
             tmem_ld32(tO + c * 32, ov);
@@ -808,7 +854,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
         const int64_t orow = static_cast<int64_t>(s.tok0 + node) * a.Hq + head;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         float* part = a.partial + ((static_cast<int64_t>(blockIdx.x) * 2 + max(s.slot, 0)) * kTiles + rw) * (kTreeRows * (D + 2));
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           float o[32];
           if (have_o) {
@@ -978,7 +1024,8 @@ cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
   a.merge = static_cast<TreeMergeRec*>(workspace);
   a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kTreeMergeBytes);
   const int d = a.d, keys = d == 256 ? 64 : 128;
-  if ((e = make_map_bf16(&a.tm_q, a.q, d, a.Hq, a.total_q, d, a.q_stride, a.g, kTreeRows / a.g)) != cudaSuccess) return e;
+  a.tile_rows = tree_tile_rows(a.max_nodes, a.g, d);
+  if ((e = make_map_bf16(&a.tm_q, a.q, d, a.Hq, a.total_q, d, a.q_stride, a.g, a.tile_rows / a.g)) != cudaSuccess) return e;
   a.new_box = a.max_nodes < keys ? (a.max_nodes + 7) / 8 * 8 : keys;
   if ((e = make_map_bf16(&a.tm_kn, a.k_new, d, a.Hkv, a.total_q, d, a.k_new_stride, 1, a.new_box)) != cudaSuccess ||
       (e = make_map_bf16(&a.tm_vn, a.v_new, d, a.Hkv, a.total_q, d, a.v_new_stride, 1, a.new_box)) != cudaSuccess)
