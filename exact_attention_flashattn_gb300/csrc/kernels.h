@@ -137,8 +137,8 @@ cudaError_t launch_prefill_tc256(const TcFwdArgs& a, unsigned int* status, unsig
 // holds kTreeRows / g whole nodes, a unit one or two tiles (tree_row_tiles) of one KV head.
 constexpr int kTreeMaxNodes = 1024;  // drafted nodes a sequence
 constexpr int kTreeRows = 128;
-constexpr int kTreeMaxCtas = 152;    // persistent CTAs, at most one per SM
-constexpr int kTreeMergeBytes = 8192;
+constexpr int kTreeMaxCtas = 304;    // persistent CTAs, two per SM (tree_max_ctas)
+constexpr int kTreeMergeBytes = 12288;
 // What the merge has to do at the boundary between CTA c - 1 and CTA c, written by CTA c: something
 // if that is the first boundary inside a unit.
 struct TreeMergeRec {
@@ -184,13 +184,15 @@ struct TreeArgs {
 // Row tiles of a unit: two (d <= 128) when a sequence may fill more than one, so that the K and V
 // tiles of a unit serve twice the rows.
 inline int tree_row_tiles(int max_nodes, int g, int d) { return d <= 128 && max_nodes > kTreeRows / g ? 2 : 1; }
+inline int tree_max_ctas(int row_tiles, int d) { return row_tiles == 1 && d <= 128 ? kTreeMaxCtas : kTreeMaxCtas / 2; }
 // Rows of a tile that hold nodes: 64 where no sequence has more (d <= 128).
 inline int tree_tile_rows(int max_nodes, int g, int d) {
   return d <= 128 && static_cast<int64_t>(max_nodes) * g <= 64 ? 64 : kTreeRows;
 }
 inline size_t tree_ws_bytes(int max_nodes, int g, int d) {
+  const int tiles = tree_row_tiles(max_nodes, g, d);
   return kTreeMergeBytes +
-         static_cast<size_t>(kTreeMaxCtas) * 2 * tree_row_tiles(max_nodes, g, d) * kTreeRows * (d + 2) * sizeof(float);
+         static_cast<size_t>(tree_max_ctas(tiles, d)) * 2 * tiles * kTreeRows * (d + 2) * sizeof(float);
 }
 // The most key tiles that the lengths of a call may make (int in the kernel: the host refuses more).
 inline int64_t tree_most_tiles(const TreeArgs& a) {

@@ -20,20 +20,18 @@
 // dependent launch merges them in the order of the keys (no atomics: results do not depend on which
 // CTA ends first).
 //
-// Inside a CTA two streams run, each with its own S and O in tensor memory, its own MMA issuing warp
-// and its own softmax warpgroup (thread = row = TMEM lane):
-//   kTiles == 2   stream w is row tile w; both read the same K and V tiles.
-//   kTiles == 1   both streams have the same rows; of the CTA's key tiles the even ones go to stream 0,
-//                 the odd ones to stream 1 (counted over all its units, so that a ring slot always
-//                 serves the same stream: a stream's waits on a slot's barrier then never skip a
-//                 phase, which their parity could not tell from the one before), and stream 1's o is
-//                 added to stream 0's through shared memory at the unit's end.
-//                 A tile of at most 64 rows is laid out twice, for stream 1 on lanes 64 to 127: a warp's
-//                 softmax costs the same for one row as for 32, so the streams share the SM's four
-//                 sub-partitions instead of two of them.
-//   d == 256      (O alone takes half of tensor memory) one stream of 64-key tiles, two S buffers.
-// A stream's S -> softmax -> P.V is a serial chain per tile; two of them, out of step, cover it. A
-// producer warp streams K and V tiles (TMA, 128-byte swizzle; from a paged cache one copy per run of
+// Inside a CTA a stream has an S and an O in tensor memory, an MMA issuing warp and a softmax warpgroup
+// (thread = row = TMEM lane):
+//   kTiles == 2   two streams, one per row tile, reading the same K and V tiles; one CTA per SM.
+//   kTiles == 1   one stream, two CTAs per SM: each has its own units, so one's hand-over from unit to
+//                 unit runs beside the other's tiles (both in one CTA on one unit's even and odd tiles
+//                 took 8 us a unit more). Where a tile has at most 64 rows, the second half of the CTAs
+//                 puts them on lanes 64 to 127: a warp's softmax costs the same for one row as for 32, and
+//                 so the two CTAs of an SM use all four of its sub-partitions.
+//   d == 256      (O alone takes half of tensor memory) one stream of 64-key tiles, two S buffers, one
+//                 CTA per SM.
+// A stream's S -> softmax -> P.V is a serial chain per tile; two of them, out of step, cover it.
+// Producer warps stream K and V tiles (TMA, 128-byte swizzle; from a paged cache one copy per run of
 // rows inside a page, a lane each) through a ring of shared-memory slots that runs on across units.
 // The tail tile of the context and the tiles of drafts may hold rows that do not count (keys past
 // the end, other sequences' drafts) and values that some rows must not see; 0 * NaN would still
@@ -56,36 +54,36 @@ constexpr int kBarBytes = 1024;
 
 template <int D, int kTiles>
 struct Cfg {
-  static constexpr int kStreams = D == 256 ? 1 : 2;
+  static constexpr int kStreams = kTiles;
   static constexpr int kKeys = D == 256 ? 64 : 128;  // keys per tile
   static constexpr int kHalves = D / 64;             // 128-byte swizzle atoms across the head dim
+  static constexpr int kCtasPerSm = kTiles == 1 && D <= 128 ? 2 : 1;
   static constexpr uint32_t kQBytes = kTreeRows * D * 2;
   static constexpr uint32_t kTileBytes = kKeys * D * 2;
-  static constexpr int kStages = D == 64 ? 8 : 4;  // even: V tiles always land in odd slots
-  static constexpr bool kExchange = kTiles == 1 && kStreams == 2;
+  // ring slots, K tiles in the even ones, V tiles in the odd
+  static constexpr int kStages = (D == 64 ? 8 : 4) / kCtasPerSm;
   static constexpr uint32_t kRing = kTiles * kQBytes;
-  static constexpr uint32_t kXch = kRing + kStages * kTileBytes;
-  static constexpr uint32_t kXml = kXch + (kExchange ? kTreeRows * D * 4 : 0);
-  static constexpr uint32_t kBar = kXml + (kExchange ? kTreeRows * 8 : 0);
+  static constexpr uint32_t kBar = kRing + kStages * kTileBytes;
   static constexpr uint32_t kSmem = kBar + kBarBytes + 1024;  // + alignment slack
   static constexpr int kTmaWarp = 4 * kStreams;  // K tiles, Q and the list of segments
   static constexpr int kMmaWarp = kTmaWarp + 1;
   static constexpr int kTmaVWarp = kMmaWarp + kStreams;
-  // more warps that issue copies of K, and as many of V (with two row tiles the MMAs set the pace)
-  static constexpr int kHelpers = kTiles == 1 ? 2 : 0;
-  static constexpr int kHelpWarp = kTmaVWarp + 1;
-  static constexpr int kWarps = kHelpWarp + 2 * kHelpers;
+  // a warp more that issues copies of K and V (with two row tiles the MMAs set the pace)
+  static constexpr int kHelpers = kTiles == 1 ? 1 : 0;
+  static constexpr int kWarps = kTmaVWarp + 1 + kHelpers;
   static constexpr int kThreads = 32 * kWarps;
   // S of a stream's next tile is issued ahead of the P.V of its current one where tensor memory has
   // the room: at d = 256 into the other S buffer, at d = 64 into the same one once the softmax has
   // read it, P having columns of its own
+  static constexpr bool kTwoS = D == 256;
   static constexpr bool kSplitP = D == 64;
   static constexpr bool kLook = D != 128;
   // tensor memory columns; without kSplitP, P (bf16 pairs) takes the place of the S it was made from
-  static constexpr uint32_t kColS = D == 256 ? 256 : 0;  // two buffers of kKeys columns
-  static constexpr uint32_t kColO = D == 256 ? 0 : 256;  // stream w: + w D
-  static constexpr uint32_t kColP = 384;                 // kSplitP, stream w: + w 64
-  static_assert(kSmem <= 232448, "shared memory");
+  static constexpr uint32_t kCols = 512 / kCtasPerSm;
+  static constexpr uint32_t kColS = D == 256 ? 256 : 0;                            // + kKeys a stream (or buffer)
+  static constexpr uint32_t kColO = D == 256 ? 0 : 128 * kStreams;                 // + D a stream
+  static constexpr uint32_t kColP = 128 * kStreams + D * kStreams;                 // kSplitP: + 64 a stream
+  static_assert(kSmem <= (kCtasPerSm == 2 ? 115712 : 232448), "shared memory");
   static_assert(kTiles == 1 || D <= 128, "tiles");
 };
 
@@ -104,10 +102,9 @@ struct Barriers {
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2];
   uint64_t s_free[2];   // kSplitP: the softmax has read S
-  uint64_t pv_done[2];  // kLook: the P.V of buffer (stream) x has completed
+  uint64_t pv_done[2];  // kLook: the P.V of S buffer (stream) x has completed
   uint64_t turn[2];     // two row tiles at d = 128: P.V turns, 0: stream 0 to 1, 1: back
   uint64_t o_full[2], o_empty[2];
-  uint64_t xch_full, xch_empty;
   uint64_t mma_done[2];
   uint64_t kv_full[8], kv_empty[8];
   uint64_t v_ready[8];  // two row tiles: stream 0 has looked over the V tile, in turn for those that need it
@@ -178,7 +175,7 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32
       : "memory");
 }
 
-// V tile in shared memory, [atom][kKeys rows][128 bytes]: rows from `valid` on become zero, and with
+// V tile in shared memory, [atom][kKeys rows][128 bytes]: rows from `valid` to the next 16 become zero, and with
 // `scan` the infinities and NaN of the others (returns whether there were any). A converged warp.
 template <int kHalves, int kKeys>
 __device__ __forceinline__ bool clean_v(uint8_t* tile, int valid, bool scan, int lane) {
@@ -206,7 +203,7 @@ __device__ __forceinline__ bool clean_v(uint8_t* tile, int valid, bool scan, int
         bad |= hit;
       }
     }
-    for (int off = valid * 128 + lane * 16; off < kKeys * 128; off += 512)
+    for (int off = valid * 128 + lane * 16; off < (valid + 15) / 16 * 2048; off += 512)
       *reinterpret_cast<uint4*>(atom + off) = make_uint4(0u, 0u, 0u, 0u);
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the tensor pipe reads the tile
@@ -214,10 +211,10 @@ __device__ __forceinline__ bool clean_v(uint8_t* tile, int valid, bool scan, int
   return __any_sync(0xffffffffu, bad);
 }
 
-// Registers: a softmax thread holds a row's 128 scores, the other eight warps of a block with helpers
-// little. Such a block of two streams has 512 x 128 of them; 256 x 184 + 256 x 72 is the same number.
+// Registers: a softmax thread holds a row's 128 scores, the other four warps little. A block of 256
+// threads (two of them on an SM) has 256 x 128; 128 x 184 + 128 x 72 is the same number.
 constexpr int kSoftRegs = 184, kOtherRegs = 72;
-static_assert(256 * kSoftRegs + 256 * kOtherRegs <= 512 * 128, "register split");
+static_assert(128 * kSoftRegs + 128 * kOtherRegs <= 256 * 128, "register split");
 template <bool kSplit>
 __device__ __forceinline__ void give_registers() {
   if constexpr (kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -228,7 +225,7 @@ __device__ __forceinline__ void take_registers() {
 }
 
 template <int D, int kTiles>
-__global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCtasPerSm) tree_kernel(const __grid_constant__ TreeArgs a) {
   using C = Cfg<D, kTiles>;
   constexpr int kStreams = C::kStreams, kKeys = C::kKeys, kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -260,7 +257,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->q_full[i], 1);
-      mbar_init(&bar->q_empty[i], kTiles == 2 ? 1 : kStreams);
+      mbar_init(&bar->q_empty[i], 1);
       mbar_init(&bar->s_full[i], 1);
       mbar_init(&bar->p_full[i], kTreeRows);
       mbar_init(&bar->s_free[i], kTreeRows);
@@ -270,8 +267,6 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       mbar_init(&bar->o_empty[i], kTreeRows);
       mbar_init(&bar->mma_done[i], 1);
     }
-    mbar_init(&bar->xch_full, kTreeRows);
-    mbar_init(&bar->xch_empty, kTreeRows);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar->kv_full[i], 1);
       mbar_init(&bar->kv_empty[i], kTiles);  // one commit per stream that reads the slot
@@ -279,13 +274,13 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
     }
     for (int i = 0; i < kSegSlots; ++i) {
       mbar_init(&bar->seg_full[i], 1);
-      mbar_init(&bar->seg_empty[i], 5 * kStreams + 1 + 2 * C::kHelpers);  // all but the K producer
+      mbar_init(&bar->seg_empty[i], 5 * kStreams + 1 + C::kHelpers);  // all but the K producer
     }
     bar->abort = 0;
     fence_mbar_init();
   }
   if (warp == C::kMmaWarp) {
-    tmem_alloc(&bar->tmem_base, 512);
+    tmem_alloc(&bar->tmem_base, C::kCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -318,6 +313,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
   volatile int* abort = &bar->abort;
   const uint64_t tmo = a.timeout_ns;
   const int tile_nodes = a.tile_rows / a.g;
+  // TMEM lane of a tile's first row
+  const int first_lane = a.tile_rows == 64 && 2 * blockIdx.x >= gridDim.x ? 64 : 0;
   const int no_abort = 0;
 
   // consumer side of the segment queue, called by a converged warp
@@ -331,19 +328,52 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
   // rows of the unit's row tile w that exist
   auto tile_rows = [&](const Seg& s, int w) { return max(0, min(tile_nodes, s.nq - s.node0 - w * tile_nodes)) * a.g; };
 
+  // paged: the copy of a tile (atom copy % kHalves of piece copy / kHalves) that is this lane's; with a
+  // helper, of each three the first two are the producer's
+  auto share_copy = [&](int member) {
+    if (C::kHelpers == 0) return lane;
+    return member > 0 ? 3 * lane + 2 : lane / 2 * 3 + (lane & 1);
+  };
   // K (kv = 0) or V (1) of a segment's tiles into the even or odd ring slots; `n` counts the tiles over
   // all segments. A lane's copy of 16 rows takes its warp about 70 ns to issue, and a tile out of 16-row
-  // pages is 8 to 16 such copies of K and as many of V, so kHelpers warps beside the K and the V producer
-  // take a share of them (a tile's one warp for both held the paged d = 128 cache at 4400 GB/s where a
-  // contiguous one ran at 6270). `member` 0 is the producer itself, which alone announces the bytes; a
-  // helper's copies may land before that, but the phase waits for the announcement.
-  auto load_tiles = [&](const Seg& s, int kv, int member, int& n, auto before_tile) -> bool {
+  // pages is 8 to 16 such copies of K and as many of V, so a helper warp takes a third of both (one warp
+  // for K and V held the paged d = 128 cache at 4400 GB/s where a contiguous one ran at 6270). The K and
+  // V producers (member 0) announce a tile's bytes; the helper's copies (member 1) may land before that,
+  // but the phase waits for the announcement.
+  auto load_tile = [&](const Seg& s, int kv, int member, int kt, int n, int row) -> bool {
     const CUtensorMap* old_map = kv ? &a.tm_v : &a.tm_k;
-    const CUtensorMap* new_map = kv ? &a.tm_vn : &a.tm_kn;
-    // paged: this lane's copy (number lane (1 + kHelpers) + member) is atom `hfl` of a piece of a tile; the
-    // pool row of the piece in the next tile is looked up one tile ahead
-    const int copy = lane * (1 + C::kHelpers) + member;
-    const int hfl = copy % C::kHalves, my_piece = (copy / C::kHalves) * a.piece;
+    const int i = 2 * n + kv, slot = i % kStages, round = i / kStages;
+    if (round > 0 && !vote(mbar_wait(&bar->kv_empty[slot], (round - 1) & 1, tmo, abort))) return false;
+    uint8_t* dst = sRing + slot * C::kTileBytes;
+    const int copy = share_copy(member), hfl = copy % C::kHalves, my_piece = (copy / C::kHalves) * a.piece;
+    if (member > 0) {
+      if (row >= 0)
+        tma_load_3d_lane(dst + hfl * (kKeys * 128) + my_piece * 128, old_map, &bar->kv_full[slot], 64 * hfl, s.hkv, row);
+      __syncwarp();
+    } else if (kt >= s.ct) {
+      const CUtensorMap* new_map = kv ? &a.tm_vn : &a.tm_kn;
+      mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(a.new_box) * 128 * C::kHalves);
+      for (int hf = 0; hf < C::kHalves; ++hf)
+        tma_load_3d(dst + hf * (kKeys * 128), new_map, &bar->kv_full[slot], 64 * hf, s.hkv, s.tok0 + (kt - s.ct) * kKeys);
+    } else if (a.block_table) {
+      // pieces past the last key are not copied: their K scores are masked, their V rows zeroed
+      const int pieces = min(kKeys / a.piece, (s.nk - kt * kKeys + a.piece - 1) / a.piece);
+      mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(pieces * a.piece) * 128 * C::kHalves);
+      __syncwarp();
+      if (row >= 0)
+        tma_load_3d_lane(dst + hfl * (kKeys * 128) + my_piece * 128, old_map, &bar->kv_full[slot], 64 * hfl, s.hkv, row);
+      __syncwarp();
+    } else {
+      mbar_arrive_expect_tx(&bar->kv_full[slot], C::kTileBytes);
+      for (int hf = 0; hf < C::kHalves; ++hf)
+        tma_load_3d(dst + hf * (kKeys * 128), old_map, &bar->kv_full[slot], 64 * hf, kt * kKeys, s.b * a.Hkv + s.hkv);
+    }
+    return true;
+  };
+  // all tiles of a segment: kv0 .. kv1 - 1 of K and V, `before_tile` ahead of each tile
+  auto load_tiles = [&](const Seg& s, int kv0, int kv1, int member, int& n, auto before_tile) -> bool {
+    // paged: the pool row of this lane's piece in the next tile is looked up one tile ahead
+    const int my_piece = (share_copy(member) / C::kHalves) * a.piece;
     auto pool_row = [&](int kt) -> int {
       const int key = kt * kKeys + my_piece;
       if (!a.block_table || my_piece >= kKeys || kt >= s.ct || key >= s.nk) return -1;
@@ -356,30 +386,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       if (!before_tile(j)) return false;
       const int kt = s.k0 + j, row = row_next;
       if (a.block_table) row_next = pool_row(kt + 1);
-      const int i = 2 * n + kv, slot = i % kStages, round = i / kStages;
-      if (round > 0 && !vote(mbar_wait(&bar->kv_empty[slot], (round - 1) & 1, tmo, abort))) return false;
-      uint8_t* dst = sRing + slot * C::kTileBytes;
-      if (member > 0) {
-        if (row >= 0)
-          tma_load_3d_lane(dst + hfl * (kKeys * 128) + my_piece * 128, old_map, &bar->kv_full[slot], 64 * hfl, s.hkv, row);
-        __syncwarp();
-      } else if (kt >= s.ct) {
-        mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(a.new_box) * 128 * C::kHalves);
-        for (int hf = 0; hf < C::kHalves; ++hf)
-          tma_load_3d(dst + hf * (kKeys * 128), new_map, &bar->kv_full[slot], 64 * hf, s.hkv, s.tok0 + (kt - s.ct) * kKeys);
-      } else if (a.block_table) {
-        // pieces past the last key are not copied: their K scores are masked, their V rows zeroed
-        const int pieces = min(kKeys / a.piece, (s.nk - kt * kKeys + a.piece - 1) / a.piece);
-        mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(pieces * a.piece) * 128 * C::kHalves);
-        __syncwarp();
-        if (row >= 0)
-          tma_load_3d_lane(dst + hfl * (kKeys * 128) + my_piece * 128, old_map, &bar->kv_full[slot], 64 * hfl, s.hkv, row);
-        __syncwarp();
-      } else {
-        mbar_arrive_expect_tx(&bar->kv_full[slot], C::kTileBytes);
-        for (int hf = 0; hf < C::kHalves; ++hf)
-          tma_load_3d(dst + hf * (kKeys * 128), old_map, &bar->kv_full[slot], 64 * hf, kt * kKeys, s.b * a.Hkv + s.hkv);
-      }
+      for (int kv = kv0; kv < kv1; ++kv)
+        if (!load_tile(s, kv, member, kt, n, row)) return false;
     }
     return true;
   };
@@ -393,7 +401,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
 
   if (warp == C::kTmaWarp) {
     // ------------------------------------------------------------ segments, Q and K tiles
-    give_registers<C::kThreads == 512>();
+    give_registers<C::kCtasPerSm == 2>();
     if (lane == 0) {
       prefetch_tmap(&a.tm_q);
       prefetch_tmap(&a.tm_k);
@@ -455,18 +463,16 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
 #pragma unroll
         for (int w = 0; w < kTiles; ++w) {
           if (nq[w] > 0 && !vote(mbar_wait(&bar->q_empty[w], (nq[w] - 1) & 1, tmo, abort))) return false;
-          const int copies = kTreeRows / a.tile_rows;
-          mbar_arrive_expect_tx(&bar->q_full[w], static_cast<uint32_t>(copies * tile_nodes * a.g) * 128 * C::kHalves);
-          for (int i = 0; i < copies; ++i)
-            for (int hf = 0; hf < C::kHalves; ++hf)
-              tma_load_3d(sQ + w * C::kQBytes + hf * (kTreeRows * 128) + i * a.tile_rows * 128, &a.tm_q, &bar->q_full[w],
-                          64 * hf, s.hkv * a.g, s.tok0 + s.node0 + w * tile_nodes);
+          mbar_arrive_expect_tx(&bar->q_full[w], static_cast<uint32_t>(tile_nodes * a.g) * 128 * C::kHalves);
+          for (int hf = 0; hf < C::kHalves; ++hf)
+            tma_load_3d(sQ + w * C::kQBytes + hf * (kTreeRows * 128) + first_lane * 128, &a.tm_q, &bar->q_full[w], 64 * hf,
+                        s.hkv * a.g, s.tok0 + s.node0 + w * tile_nodes);
           ++nq[w];
         }
         return true;
       };
-      const int q_at = min(s.nt, kStages / 4);  // the first loads need ring slots only, not Q's buffer
-      ok = load_tiles(s, 0, 0, nload, [&](int j) { return j != q_at || load_q(); });
+      const int q_at = min(s.nt, (kStages + 3) / 4);  // the first loads need ring slots only, not Q's buffer
+      ok = load_tiles(s, 0, 1, 0, nload, [&](int j) { return j != q_at || load_q(); });
       if (ok && q_at == s.nt) ok = load_q();
     }
     if (!ok && lane == 0) raise_timeout(abort, a.status);
@@ -476,11 +482,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       if (nq[w] > 0) mbar_wait(&bar->q_full[w], (nq[w] - 1) & 1, tmo, &no_abort);
     drain(0, nload);
   } else if (warp >= C::kTmaVWarp) {
-    // ------------------------------------------------------------ V tiles, and the helpers (K's, then V's)
-    give_registers<C::kThreads == 512>();
-    const int help = warp - C::kHelpWarp;
-    const int kv = warp == C::kTmaVWarp || help >= C::kHelpers ? 1 : 0;
-    const int member = warp == C::kTmaVWarp ? 0 : 1 + (help & 1);
+    // ------------------------------------------------------------ V tiles, or the helper's share of both
+    give_registers<C::kCtasPerSm == 2>();
+    const bool helper = warp > C::kTmaVWarp;
     int nload = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -489,14 +493,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       const Seg s = *sp;
       release_seg(k);
       if (!s.valid) break;
-      if (member > 0 && !a.block_table) continue;  // a contiguous cache's tile is kHalves copies
-      ok = load_tiles(s, kv, member, nload, [](int) { return true; });
+      if (helper && !a.block_table) continue;  // a contiguous cache's tile is kHalves copies
+      ok = load_tiles(s, helper ? 0 : 1, 2, helper ? 1 : 0, nload, [](int) { return true; });
     }
     if (!ok && lane == 0) raise_timeout(abort, a.status);
-    drain(kv, nload);
+    drain(1, nload);
+    if (helper) drain(0, nload);
   } else if (warp >= C::kMmaWarp) {
     // ------------------------------------------------------------ MMA issuers, one per stream
-    give_registers<C::kThreads == 512>();
+    give_registers<C::kCtasPerSm == 2>();
     const int w = warp - C::kMmaWarp;
     constexpr uint32_t idesc_qk = idesc_bf16_f32(kTreeRows, kKeys, 0, 0);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(kTreeRows, D, 0, 1);
@@ -515,8 +520,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       return r;
     };
     // S buffer of a stream's n-th tile, and how often the buffer was used before
-    auto buf = [&](int n) { return kStreams == 2 ? w : n & 1; };
-    auto use = [&](int n) { return kStreams == 2 ? n : n >> 1; };
+    auto buf = [&](int n) { return C::kTwoS ? n & 1 : w; };
+    auto use = [&](int n) { return C::kTwoS ? n >> 1 : n; };
     // S of load i, whose K has landed
     auto issue_s = [&](int i) {
       const uint32_t kl = k_lo + (i % kStages) * slot_step;
@@ -541,14 +546,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       issue_s(i);
       return true;
     };
-    auto issue_pv = [&](int i, bool accumulate) {
+    // P.V of load i over the first `valid` keys (whole K = 16 steps)
+    auto issue_pv = [&](int i, bool accumulate, int valid) {
       const uint32_t tP = tbase + (C::kSplitP ? C::kColP + w * 64 : C::kColS + buf(np) * kKeys);
       const uint32_t vl = v_lo + (i % kStages) * slot_step;
-      if constexpr (kKeys == 128) {
+      if (kKeys == 128 && valid == 128) {
         umma_ts_k128(tO, tP, vl, hi, idesc_pv, accumulate ? 1u : 0u);
       } else {
-#pragma unroll
-        for (int s = 0; s < kKeys / 16; ++s) umma_ts(tO, tP + 8 * s, vl + 128 * s, hi, idesc_pv, (accumulate || s) ? 1u : 0u);
+#pragma unroll 1
+        for (int s = 0; 16 * s < valid; ++s) umma_ts(tO, tP + 8 * s, vl + 128 * s, hi, idesc_pv, (accumulate || s) ? 1u : 0u);
       }
       if constexpr (C::kLook) umma_commit(&bar->pv_done[buf(np)]);
       ++np;
@@ -565,19 +571,16 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       tc_fence_after();
       const int base = nload;
       nload += 2 * s.nt;
-      // this stream's tiles: j0, j0 + step, ... below s.nt
-      const int step = C::kExchange ? 2 : 1;
-      const int j0 = C::kExchange ? (base / 2 + w) & 1 : 0;
       const bool idle = kTiles == 2 && tile_rows(s, w) == 0;  // no rows: only gives the slots back
       const int special_from = s.nk % kKeys ? s.ct - 1 : s.ct;
       const bool turns = kTiles == 2 && !C::kLook && tile_rows(s, 1) > 0;
-      if (idle || j0 >= s.nt) {
+      if (idle) {
         umma_commit(&bar->q_empty[qb]);
       } else {
-        if (!(ok = start_s(base + 2 * j0))) break;
-        if (j0 + step >= s.nt) umma_commit(&bar->q_empty[qb]);
+        if (!(ok = start_s(base))) break;
+        if (s.nt == 1) umma_commit(&bar->q_empty[qb]);
       }
-      for (int j = j0; j < s.nt; j += step) {
+      for (int j = 0; j < s.nt; ++j) {
         const int ik = base + 2 * j, iv = ik + 1;
         if (idle && !(ok = wait_load(ik))) break;
         umma_commit(&bar->kv_empty[ik % kStages]);  // S of this tile was issued before
@@ -587,22 +590,24 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
           nspecial += s.k0 + j >= special_from;
           continue;
         }
-        const int inext = ik + 2 * step;
-        const bool more = j + step < s.nt, last_s = j + 2 * step >= s.nt;
+        const int inext = ik + 2;
+        const bool more = j + 1 < s.nt, last_s = j + 2 >= s.nt;
         if (C::kLook && more) {
           // S of the next tile goes ahead of this tile's P.V
           if (!(ok = start_s(inext))) break;
           if (last_s) umma_commit(&bar->q_empty[qb]);
         }
         if (!(ok = wait_load(iv))) break;
+        int valid = kKeys;  // keys of the tile that count
         if (s.k0 + j >= special_from) {
-          // V rows that do not count, and drafts' infinities and NaN (two row tiles read one V tile:
-          // stream 0 looks it over for both)
+          // the context's last tile, or drafts: P.V stops at the 16 keys that hold the last one; V rows from
+          // there to the 16's end are zeroed, and drafts' infinities and NaN (two row tiles read one V
+          // tile: stream 0 looks it over for both)
           const int kt = s.k0 + j;
           const bool draft = kt >= s.ct;
           uint64_t* ready = &bar->v_ready[nspecial % (kStages / 2)];
+          valid = min(kKeys, draft ? s.nq - (kt - s.ct) * kKeys : s.nk - kt * kKeys);
           if (kTiles == 1 || w == 0) {
-            const int valid = min(kKeys, draft ? s.nq - (kt - s.ct) * kKeys : s.nk - kt * kKeys);
             if (clean_v<C::kHalves, kKeys>(sRing + (iv % kStages) * C::kTileBytes, valid, draft, lane) && lane == 0)
               atomicOr(&sp->bad, 1);
             __syncwarp();
@@ -619,10 +624,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
                      : nturn > 0 && !(ok = vote(mbar_wait(&bar->turn[1], (nturn - 1) & 1, tmo, abort))))
             break;
         }
-        if (j == j0 && ou > 0 && !(ok = vote(mbar_wait(&bar->o_empty[w], (ou - 1) & 1, tmo, abort)))) break;
+        if (j == 0 && ou > 0 && !(ok = vote(mbar_wait(&bar->o_empty[w], (ou - 1) & 1, tmo, abort)))) break;
         if (!(ok = vote(mbar_wait(&bar->p_full[buf(np)], use(np) & 1, tmo, abort)))) break;
         tc_fence_after();
-        issue_pv(iv, j > j0);
+        issue_pv(iv, j > 0, valid);
         if (turns) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar->turn[w]);
@@ -647,17 +652,13 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
     mbar_wait(&bar->mma_done[w], 0, tmo, &no_abort);
   } else {
     // ------------------------------------------------------------ softmax warpgroups
-    take_registers<C::kThreads == 512>();
+    take_registers<C::kCtasPerSm == 2>();
     const int w = warp >> 2;
-    // row of the tile: the TMEM lane, less 64 in stream 1 where a tile has 64 rows (it works on the second
-    // copy of them, on the other two of the SM's four sub-partitions)
-    const int row = (warp & 3) * 32 + lane - w * (kTreeRows - a.tile_rows);
+    const int row = (warp & 3) * 32 + lane - first_lane;  // of the tile: the TMEM lane less that of the first row
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tO = tbase + lane_base + C::kColO + w * D;
     const float sl2 = a.scale_log2;
-    float* xo = reinterpret_cast<float*>(smem + C::kXch);   // [D][kTreeRows]
-    float2* xml = reinterpret_cast<float2*>(smem + C::kXml);  // [kTreeRows]
-    int n = 0, oused = 0, xn = 0, tiles = 0;
+    int n = 0, oused = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const Seg* sp = wait_seg(k);
@@ -678,14 +679,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       const int node = s.node0 + rw * tile_nodes + some_row / a.g;  // within the sequence
       const int head = s.hkv * a.g + some_row % a.g;
       const uint64_t* bits = a.mask + static_cast<int64_t>(s.tok0 + node) * a.mask_words;
-      const int step = C::kExchange ? 2 : 1;
-      const int first = tiles & 1;  // the stream of the segment's first tile
-      const int j0 = C::kExchange ? first ^ w : 0;
-      tiles += s.nt;
       const int masked_from = s.nk % kKeys ? s.ct - 1 : s.ct;  // first tile with keys that some row does not see
       float m_ref = -INFINITY, l = 0.f;
-      for (int j = j0; j < s.nt; j += step) {
-        const int x = kStreams == 2 ? w : n & 1, phase = (kStreams == 2 ? n : n >> 1) & 1;
+      for (int j = 0; j < s.nt; ++j) {
+        const int x = C::kTwoS ? n & 1 : w, phase = (C::kTwoS ? n >> 1 : n) & 1;
         const uint32_t tS = tbase + lane_base + C::kColS + x * kKeys;
         const uint32_t tP = C::kSplitP ? tbase + lane_base + C::kColP + w * 64 : tS;
         if (!(ok = vote(mbar_wait(&bar->s_full[x], phase, tmo, abort)))) break;
@@ -743,7 +740,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
           if (m_new > m_ref + kRescaleThreshold) {
             const float alpha = (m_ref == -INFINITY) ? 0.f : ex2(m_ref - m_new);
             l *= alpha;
-            if (j > j0) alpha_o = alpha;
+            if (j > 0) alpha_o = alpha;
             m_ref = m_new;
           }
           const float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
@@ -770,7 +767,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
           }
           // O must carry the new reference maximum before this tile's P.V (rare)
           if (__any_sync(0xffffffffu, alpha_o != 1.f)) {
-            if (kStreams == 1) {
+            if (C::kTwoS) {
               // S(j) was issued ahead of P.V(j - 1): that one has to be done
               ok = vote(mbar_wait(&bar->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, tmo, abort));
               if (!ok) break;
@@ -803,52 +800,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
       }
       if (!ok) break;
       // ---- the unit's end in this CTA
-      const bool have_o = j0 < s.nt;
-      if (have_o) {
-        if (!(ok = vote(mbar_wait(&bar->o_full[w], oused & 1, tmo, abort)))) break;
-        ++oused;
-        tc_fence_after();
-      }
-      const bool exchange = C::kExchange && (s.nt > 1 || first == 1);  // stream 1 had a tile
-      if (exchange && w == 1) {
-        // stream 1 hands its state over
-        if (xn > 0 && !(ok = vote(mbar_wait(&bar->xch_empty, (xn - 1) & 1, tmo, abort)))) break;
-        ++xn;
-        if (warp_ok) {
-          xml[row] = make_float2(m_ref, l);
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t ov[32];
-            tmem_ld32(tO + c * 32, ov);
-            tmem_wait_ld();
-            tmem_reg_fence(ov);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) xo[(c * 32 + e) * kTreeRows + row] = __uint_as_float(ov[e]);
-          }
-        }
-        tc_fence_before();
-        mbar_arrive(&bar->o_empty[w]);
-        mbar_arrive(&bar->xch_full);
-        release_seg(k);
-        continue;
-      }
-      if (C::kExchange && w == 1) {  // stream 0 had the only tile
-        release_seg(k);
-        continue;
-      }
-      float f0 = 1.f, f1 = 0.f;
-      if (exchange) {
-        if (!(ok = vote(mbar_wait(&bar->xch_full, xn & 1, tmo, abort)))) break;
-        ++xn;
-        if (warp_ok) {
-          const float2 o1 = xml[row];
-          const float m = fmaxf(m_ref, o1.x);
-          f0 = m_ref == -INFINITY ? 0.f : ex2(m_ref - m);
-          f1 = o1.x == -INFINITY ? 0.f : ex2(o1.x - m);
-          l = l * f0 + o1.y * f1;
-          m_ref = m;
-        }
-      }
+      if (!(ok = vote(mbar_wait(&bar->o_full[w], oused & 1, tmo, abort)))) break;
+      ++oused;
+      tc_fence_after();
       if (warp_ok) {
         const bool bad = *const_cast<const volatile int*>(&sp->bad) != 0;
         const int64_t orow = static_cast<int64_t>(s.tok0 + node) * a.Hq + head;
@@ -856,22 +810,13 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
         float* part = a.partial + ((static_cast<int64_t>(blockIdx.x) * 2 + max(s.slot, 0)) * kTiles + rw) * (kTreeRows * (D + 2));
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(tO + c * 32, ov);
+          tmem_wait_ld();
+          tmem_reg_fence(ov);
           float o[32];
-          if (have_o) {
-            uint32_t ov[32];
-            tmem_ld32(tO + c * 32, ov);
-            tmem_wait_ld();
-            tmem_reg_fence(ov);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]) * f0;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.f;
-          }
-          if (exchange) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] += xo[(c * 32 + e) * kTreeRows + row] * f1;
-          }
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]);
           if (bad && row_ok) {
             // the infinities and NaN among the drafts that this row sees
             const int d0 = max(s.k0 - s.ct, 0) * kKeys, d1 = min((s.k0 + s.nt - s.ct) * kKeys, s.nq);
@@ -905,8 +850,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
         if (row_ok && s.slot >= 0) *reinterpret_cast<float2*>(part + kTreeRows * D + 2 * row) = make_float2(m_ref, l);
       }
       tc_fence_before();
-      if (have_o) mbar_arrive(&bar->o_empty[w]);
-      if (exchange) mbar_arrive(&bar->xch_empty);
+      mbar_arrive(&bar->o_empty[w]);
       release_seg(k);
     }
     if (!ok && lane == 0) raise_timeout(abort, a.status);
@@ -916,7 +860,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) tree_kernel(const
   if (warp == C::kMmaWarp) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tbase, 512);
+    tmem_dealloc(tbase, C::kCols);
   }
 }
 
@@ -1052,10 +996,10 @@ cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   const int tiles = tree_row_tiles(a.max_nodes, a.g, d);
-  // no more CTAs than tiles there can be
   const int64_t most = tree_most_tiles(a);  // no more CTAs than tiles there can be
-  a.ctas = static_cast<int>(most < kTreeMaxCtas ? most : kTreeMaxCtas);
-  if (a.ctas > sms) a.ctas = sms;
+  const int fit = tiles == 1 && d <= 128 ? 2 * sms : sms;
+  a.ctas = tree_max_ctas(tiles, d) < fit ? tree_max_ctas(tiles, d) : fit;
+  if (a.ctas > most) a.ctas = static_cast<int>(most);
   if (d == 64) return tiles == 2 ? launch<64, 2>(a, stream) : launch<64, 1>(a, stream);
   if (d == 128) return tiles == 2 ? launch<128, 2>(a, stream) : launch<128, 1>(a, stream);
   return launch<256, 1>(a, stream);
