@@ -167,7 +167,8 @@ int kv_plan_paged(const int32_t* nk, const int32_t* n_new, int32_t* block_table,
                   int32_t* cu_seqlens, int32_t* slots, int32_t* free_count_out, int B, int page_size,
                   int max_pages_per_seq, int free_capacity, int num_tokens, void* stream) {
   if (B < 0 || num_tokens < 0 || free_capacity < 0 || max_pages_per_seq <= 0 || !page_sizes(page_size, 1) ||
-      static_cast<int64_t>(max_pages_per_seq) * page_size > 0x7fffffff)
+      static_cast<int64_t>(max_pages_per_seq) * page_size > 0x7fffffff ||
+      static_cast<int64_t>(B) * max_pages_per_seq > 0x7fffffff)
     return BWATTN_ERR_INVALID_ARG;
   if (!good(free_count, 4) || !good(free_count_out, 4) || !good(cu_seqlens, 4) || !good_or_null(free_pages, 4) ||
       (free_capacity > 0 && !free_pages) || !good_or_null(slots, 4) || (num_tokens > 0 && !slots))

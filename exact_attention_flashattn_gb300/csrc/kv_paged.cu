@@ -9,35 +9,59 @@ namespace {
 
 // ---------------------------------------------------------------- tree masks
 //
-// mask[i] = mask[parent(i)] | bit i, position[i] = nk + depth(i). A parent precedes its children
-// (anything else counts as a root), so a walk from node i up its parents visits falling indices and
-// ends. One CTA per sequence holds the parents in shared memory; a thread makes one 64-bit word of
-// one node's mask: it walks from the node until the indices fall below its word, and the thread of
-// word 0, which walks to the root, counts the depth.
-constexpr int kMaskThreads = 256;
-constexpr int kMaskMaxNodes = 1024;
+// mask[i] = mask[parent(i)] | bit i, position[i] = nk + depth(i), depth(i) = bits of mask[i] - 1. A
+// parent precedes its children (anything else counts as a root), so the links have no cycle, and they
+// are followed by doubling: with mask the nodes within 2^r - 1 steps up and up the node 2^r steps up,
+// mask[i] |= mask[up[i]], up[i] = up[up[i]], until no node has one left: log2(depth) rounds whatever the
+// tree (a walk per node took 5 us at depth 60, and as long as its longest line). One CTA per sequence, a
+// thread per node, masks and links in shared memory; the new values are read before a barrier and
+// written behind it.
+constexpr int kMaskMaxNodes = kTreeMaxNodes;
 
-__global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const TreeMaskArgs a) {
-  __shared__ int16_t parent[kMaskMaxNodes];
+template <int kWords>  // at least the call's words
+__global__ void __launch_bounds__(kMaskMaxNodes) tree_mask_kernel(const TreeMaskArgs a) {
+  extern __shared__ uint64_t sm_mask[];  // [kWords][threads], then int16_t up[threads]
+  const int threads = blockDim.x, i = threadIdx.x;
+  int16_t* up = reinterpret_cast<int16_t*>(sm_mask + static_cast<size_t>(kWords) * threads);
   const int seq = blockIdx.x;
   const int t0 = min(max(a.cu_q[seq], 0), a.total_q);
-  const int n = min(min(max(a.cu_q[seq + 1] - t0, 0), a.total_q - t0), a.max_nodes);
-  for (int i = threadIdx.x; i < n; i += kMaskThreads) {
-    const int p = a.parents[t0 + i];
-    parent[i] = static_cast<int16_t>(p >= 0 && p < i ? p : -1);
-  }
-  __syncthreads();
+  const int n = min(min(max(a.cu_q[seq + 1], t0), a.total_q) - t0, a.max_nodes);
   const int base = a.nk ? a.nk[seq] : 0;
-  for (int it = threadIdx.x; it < n * a.words; it += kMaskThreads) {
-    const int i = it / a.words, w = it % a.words;
-    uint64_t bits = 0;
-    int depth = -1;
-    for (int j = i; j >= 64 * w; j = parent[j]) {
-      if ((j >> 6) == w) bits |= 1ull << (j & 63);
-      ++depth;
+  int link = -1;
+  if (i < n) {
+    const int p = a.parents[t0 + i];
+    if (p >= 0 && p < i) link = p;
+  }
+  uint64_t bits[kWords];
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) {
+    bits[w] = (i >> 6) == w ? 1ull << (i & 63) : 0;
+    sm_mask[w * threads + i] = bits[w];
+  }
+  up[i] = static_cast<int16_t>(link);
+  while (__syncthreads_or(link >= 0)) {
+    int next = -1;
+    if (link >= 0) {
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) bits[w] |= sm_mask[w * threads + link];
+      next = up[link];
     }
-    a.mask[static_cast<int64_t>(t0 + i) * a.words + w] = bits;
-    if (w == 0 && a.positions) a.positions[t0 + i] = base + depth;
+    __syncthreads();
+    if (link >= 0) {
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) sm_mask[w * threads + i] = bits[w];
+      up[i] = static_cast<int16_t>(next);
+    }
+    link = next;
+  }
+  // the rows of the sequence are contiguous in a.mask: written in order from shared memory
+  uint64_t* out = a.mask + static_cast<int64_t>(t0) * a.words;
+  for (int x = i; x < n * a.words; x += threads) out[x] = sm_mask[x % a.words * threads + x / a.words];
+  if (i < n && a.positions) {
+    int depth = -1;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) depth += __popcll(bits[w]);
+    a.positions[t0 + i] = base + depth;
   }
 }
 
@@ -46,11 +70,13 @@ __global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const TreeMaskA
 // need_b = max(0, min(ceil((nk_b + new_b) / P), max_pages) - held_b) pages are taken from the top of
 // the free stack, request after request: page k >= held_b of request b is
 // free[count - 1 - (first_b + k - held_b)], first_b the sum of the needs before b. Every CTA scans
-// all requests, kPlanThreads at a time (two prefix sums, 64-bit: lengths come from the device and
-// their sum may pass 32 bits), and writes its share of the tokens' slots, of the new table entries
-// and of the per-request outputs, so no CTA waits for another: a token's page is worked out from
-// the old table or the free stack, never read from what this launch writes.
-constexpr int kPlanThreads = 512;
+// all requests, kPlanThreads x kPlanRun at a time (two prefix sums; the tokens' in 64 bits, their sum may
+// pass 32), and writes its share of the tokens' slots, of the new table entries and of the per-request
+// outputs, so no CTA waits for another: a token's page is worked out from the old table or the free
+// stack, never read from what this launch writes.
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanRun = 2;
+constexpr int kPlanChunk = kPlanThreads * kPlanRun;
 
 __device__ __forceinline__ int plan_page(const PlanArgs& a, int count, int64_t i) {
   return i < count ? a.free_pages[count - 1 - i] : -1;  // past the stack: no page
@@ -58,29 +84,44 @@ __device__ __forceinline__ int plan_page(const PlanArgs& a, int count, int64_t i
 
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a) {
   constexpr int kW = kPlanThreads / 32;
-  __shared__ int64_t s_tok[kPlanThreads + 1], s_page[kPlanThreads + 1];  // exclusive sums of the chunk
-  __shared__ int s_nk[kPlanThreads], s_held[kPlanThreads];
-  __shared__ int64_t s_wt[kW], s_wp[kW];
+  // exclusive sums of the chunk's requests from its start, tokens cut off at the slots (`most`)
+  __shared__ int s_tok[kPlanChunk], s_page[kPlanChunk], s_nk[kPlanChunk], s_held[kPlanChunk];
+  __shared__ int64_t s_wt[kW];
+  __shared__ int s_wp[kW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int count = min(max(*a.free_count, 0), a.free_cap);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kPlanThreads;
   const int64_t me = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid;
-  int64_t tok_sum = 0, page_sum = 0;
-  for (int b0 = 0, chunk = 0; b0 < a.B; b0 += kPlanThreads, ++chunk) {
-    const int b = b0 + tid;
-    int nk = 0, held = 0;
-    int64_t add = 0, need = 0;
-    if (b < a.B) {
-      nk = max(a.nk[b], 0);
-      held = min(max(a.held[b], 0), a.max_pages);
-      add = max(a.n_new[b], 0);
-      const int64_t want = min((nk + add + a.page_size - 1) / a.page_size, static_cast<int64_t>(a.max_pages));
-      need = max(want - held, static_cast<int64_t>(0));
+  int64_t tok_sum = 0;
+  int page_sum = 0;  // B x max_pages fits
+  for (int b0 = 0, chunk = 0; b0 < a.B; b0 += kPlanChunk, ++chunk) {
+    if (b0 > 0) __syncthreads();  // the last chunk's sums have been read
+    int nk[kPlanRun], held[kPlanRun], need[kPlanRun], add[kPlanRun];
+#pragma unroll
+    for (int r = 0; r < kPlanRun; ++r) {
+      const int b = b0 + tid * kPlanRun + r;
+      nk[r] = b < a.B ? max(a.nk[b], 0) : 0;
+      add[r] = b < a.B ? max(a.n_new[b], 0) : 0;
+      held[r] = b < a.B ? min(max(a.held[b], 0), a.max_pages) : 0;
     }
-    int64_t st = add, sp = need;  // inclusive sums over the warp, then the block
+    int64_t tok = 0;
+    int page = 0;
+#pragma unroll
+    for (int r = 0; r < kPlanRun; ++r) {
+      const int64_t keys = static_cast<int64_t>(nk[r]) + add[r];
+      const int want = keys < static_cast<int64_t>(a.max_pages) * a.page_size
+                           ? (static_cast<int>(keys) + a.page_size - 1) / a.page_size
+                           : a.max_pages;
+      need[r] = b0 + tid * kPlanRun + r < a.B ? max(want - held[r], 0) : 0;
+      tok += add[r];
+      page += need[r];
+    }
+    int64_t st = tok;  // inclusive sums over the warp, then the block
+    int sp = page;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, st, off), y = __shfl_up_sync(0xffffffffu, sp, off);
+      const int64_t x = __shfl_up_sync(0xffffffffu, st, off);
+      const int y = __shfl_up_sync(0xffffffffu, sp, off);
       if (lane >= off) {
         st += x;
         sp += y;
@@ -91,63 +132,77 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
       s_wp[warp] = sp;
     }
     __syncthreads();
-    int64_t ct = 0, cp = 0;  // chunk totals; the warps before this one
+    // the sums of the warps before this one, and of all, from a scan of the warps' totals by each warp
+    int64_t vt = s_wt[lane];
+    int vp = s_wp[lane];
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      if (w == warp) {
-        st += ct;
-        sp += cp;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, vt, off);
+      const int y = __shfl_up_sync(0xffffffffu, vp, off);
+      if (lane >= off) {
+        vt += x;
+        vp += y;
       }
-      ct += s_wt[w];
-      cp += s_wp[w];
     }
-    s_tok[tid] = tok_sum + st - add;
-    s_page[tid] = page_sum + sp - need;
-    s_nk[tid] = nk;
-    s_held[tid] = held;
-    if (b < a.B && chunk % gridDim.x == blockIdx.x) {
-      a.nk_out[b] = static_cast<int>(min(nk + add, static_cast<int64_t>(0x7fffffff)));
-      a.held_out[b] = held + static_cast<int>(need);
-      a.cu[b] = static_cast<int>(min(tok_sum + st - add, static_cast<int64_t>(0x7fffffff)));
+    const int64_t chunk_tok = __shfl_sync(0xffffffffu, vt, 31);
+    const int chunk_page = __shfl_sync(0xffffffffu, vp, 31);
+    const int64_t before_t = __shfl_sync(0xffffffffu, vt, (warp + 31) & 31);
+    const int before_p = __shfl_sync(0xffffffffu, vp, (warp + 31) & 31);
+    if (warp > 0) {
+      st += before_t;
+      sp += before_p;
     }
-    if (tid == 0) {
-      s_tok[kPlanThreads] = tok_sum + ct;
-      s_page[kPlanThreads] = page_sum + cp;
+    st -= tok;
+    sp -= page;
+    const int64_t most = min(chunk_tok, max(a.num_tokens - tok_sum, static_cast<int64_t>(0)));
+#pragma unroll
+    for (int r = 0; r < kPlanRun; ++r) {
+      const int x = tid * kPlanRun + r, b = b0 + x;
+      s_tok[x] = static_cast<int>(min(st, most));
+      s_page[x] = sp;
+      s_nk[x] = nk[r];
+      s_held[x] = held[r];
+      if (b < a.B && chunk % gridDim.x == blockIdx.x) {
+        a.nk_out[b] = static_cast<int>(min(static_cast<int64_t>(nk[r]) + add[r], static_cast<int64_t>(0x7fffffff)));
+        a.held_out[b] = held[r] + need[r];
+        a.cu[b] = static_cast<int>(min(tok_sum + st, static_cast<int64_t>(0x7fffffff)));
+      }
+      st += add[r];
+      sp += need[r];
     }
     __syncthreads();
     // the request of an item: the last one whose exclusive sum is at most the item's index
-    auto request = [&](const int64_t* sums, int64_t x) {
+    auto request = [&](const int* sums, int x) {
       int lo = 0;
 #pragma unroll
-      for (int w = kPlanThreads / 2; w > 0; w >>= 1)
+      for (int w = kPlanChunk / 2; w > 0; w >>= 1)
         if (sums[lo + w] <= x) lo += w;
       return lo;
     };
-    for (int64_t x = page_sum + me; x < page_sum + cp; x += step) {
-      const int r = request(s_page, x);
-      const int64_t k = s_held[r] + (x - s_page[r]);
-      a.table[static_cast<int64_t>(b0 + r) * a.max_pages + k] = plan_page(a, count, x);
+    for (int64_t x = me; x < chunk_page; x += step) {
+      const int r = request(s_page, static_cast<int>(x));
+      const int k = s_held[r] + (static_cast<int>(x) - s_page[r]);
+      a.table[static_cast<int64_t>(b0 + r) * a.max_pages + k] = plan_page(a, count, static_cast<int64_t>(page_sum) + x);
     }
-    for (int64_t x = tok_sum + me; x < min(tok_sum + ct, static_cast<int64_t>(a.num_tokens)); x += step) {
-      const int r = request(s_tok, x);
-      const int64_t pos = s_nk[r] + (x - s_tok[r]);
-      const int64_t k = pos / a.page_size;
+    for (int64_t x = me; x < most; x += step) {
+      const int r = request(s_tok, static_cast<int>(x));
+      const int64_t pos = static_cast<int64_t>(s_nk[r]) + (static_cast<int>(x) - s_tok[r]);
       int64_t slot = -1;
-      if (k < a.max_pages) {
-        const int page = k < s_held[r] ? a.table[static_cast<int64_t>(b0 + r) * a.max_pages + k]
-                                       : plan_page(a, count, s_page[r] + (k - s_held[r]));
-        if (page >= 0) slot = static_cast<int64_t>(page) * a.page_size + pos % a.page_size;
+      if (pos < static_cast<int64_t>(a.max_pages) * a.page_size) {
+        const int k = static_cast<int>(pos) / a.page_size;
+        const int p = k < s_held[r] ? a.table[static_cast<int64_t>(b0 + r) * a.max_pages + k]
+                                    : plan_page(a, count, static_cast<int64_t>(page_sum) + s_page[r] + (k - s_held[r]));
+        if (p >= 0) slot = static_cast<int64_t>(p) * a.page_size + (static_cast<int>(pos) - k * a.page_size);
       }
-      a.slots[x] = slot <= 0x7fffffff ? static_cast<int>(slot) : -1;
+      a.slots[tok_sum + x] = slot <= 0x7fffffff ? static_cast<int>(slot) : -1;
     }
-    tok_sum += ct;
-    page_sum += cp;
-    __syncthreads();  // the next chunk overwrites the sums
+    tok_sum += chunk_tok;
+    page_sum += chunk_page;
   }
   for (int64_t x = tok_sum + me; x < a.num_tokens; x += step) a.slots[x] = -1;
   if (me == 0) {
     a.cu[a.B] = static_cast<int>(min(tok_sum, static_cast<int64_t>(0x7fffffff)));
-    *a.free_out = static_cast<int>(max(count - page_sum, static_cast<int64_t>(-0x7fffffff)));
+    *a.free_out = count - page_sum;
   }
 }
 
@@ -155,7 +210,19 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
 //
 // A copy of row_elems elements from row rows[i] (or i) of k_new and v_new to row slots[i] of the
 // pool; slots or rows outside their range are skipped. A thread moves 16 bytes of a row.
+//
+// A thread keeps its channels (kVec of them, 16 bytes of output) and takes rows a grid apart, kAppendRows
+// at a time: their slots first, then their data, so that its loads overlap; with E4M3 pages the
+// channels' scales and reciprocals stay in registers (reading and inverting them for every element took
+// 47 us on 20001 rows of 8 x 128, twice the bytes' time).
 constexpr int kAppendThreads = 256;
+constexpr int kAppendRows = 4;
+
+__device__ __forceinline__ uint4 load_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 
 // The E4M3 code nearest to x / s (ties to even, magnitudes past 448 to 448, NaN to NaN), two at a
 // time. r = RN(1 / s); q = x r corrected once by its remainder is RN(x / s) (Markstein's division,
@@ -178,71 +245,110 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-__global__ void __launch_bounds__(kAppendThreads) kv_append_bf16_kernel(const AppendArgs a) {
-  const bool is_v = blockIdx.y == 1;
-  const uint16_t* src = is_v ? a.v_new : a.k_new;
-  uint16_t* dst = static_cast<uint16_t*>(is_v ? a.v_pages : a.k_pages);
-  const int64_t stride = is_v ? a.v_stride : a.k_stride;
-  const int per_row = a.row_elems / 8;
-  const int64_t total = static_cast<int64_t>(a.num_slots) * per_row;
-  for (int64_t x = static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x; x < total;
-       x += static_cast<int64_t>(gridDim.x) * kAppendThreads) {
-    const int i = static_cast<int>(x / per_row), c = static_cast<int>(x % per_row);
-    const int slot = a.slots[i], row = a.rows ? a.rows[i] : i;
-    if (slot < 0 || slot >= a.pool_rows || row < 0 || row >= a.num_rows) continue;
-    *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(slot) * a.row_elems + 8 * c) =
-        *reinterpret_cast<const uint4*>(src + row * stride + 8 * c);
-  }
-}
-
-__global__ void __launch_bounds__(kAppendThreads) kv_append_fp8_kernel(const AppendArgs a) {
+template <bool kFp8>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a, int threads) {
+  constexpr int kVec = kFp8 ? 16 : 8;
+  constexpr int kLoads = kVec / 8;
   const bool is_v = blockIdx.y == 1;
   const uint16_t* src = is_v ? a.v_new : a.k_new;
   uint8_t* dst = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages);
-  const float* scale = is_v ? a.v_scale : a.k_scale;
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
-  const int per_row = a.row_elems / 8;
-  const int64_t total = static_cast<int64_t>(a.num_slots) * per_row;
-  for (int64_t x = static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x; x < total;
-       x += static_cast<int64_t>(gridDim.x) * kAppendThreads) {
-    const int i = static_cast<int>(x / per_row), c = static_cast<int>(x % per_row);
-    const int slot = a.slots[i], row = a.rows ? a.rows[i] : i;
-    if (slot < 0 || slot >= a.pool_rows || row < 0 || row >= a.num_rows) continue;
-    const uint4 u = *reinterpret_cast<const uint4*>(src + row * stride + 8 * c);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    uint32_t code[4];
+  const int per_row = a.row_elems / kVec;
+  const int me = blockIdx.x * kAppendThreads + threadIdx.x;
+  if (me >= threads) return;  // `threads` is a multiple of per_row
+  const int c = me % per_row, step = threads / per_row;
+  float sc[kVec], inv[kVec];
+  if constexpr (kFp8) {
+    const float* scale = (is_v ? a.v_scale : a.k_scale) + kVec * c;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float s0 = scale[8 * c + 2 * e], s1 = scale[8 * c + 2 * e + 1];
-      code[e] = e4m3x2(quotient_to_odd(__uint_as_float(w[e] << 16), s0, __frcp_rn(s0)),
-                       quotient_to_odd(__uint_as_float(w[e] & 0xffff0000u), s1, __frcp_rn(s1)));
+    for (int e = 0; e < kVec; e += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(scale + e);
+      sc[e] = v.x, sc[e + 1] = v.y, sc[e + 2] = v.z, sc[e + 3] = v.w;
     }
-    *reinterpret_cast<uint2*>(dst + static_cast<int64_t>(slot) * a.row_elems + 8 * c) =
-        make_uint2(code[0] | (code[1] << 16), code[2] | (code[3] << 16));
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) inv[e] = __frcp_rn(sc[e]);
+  }
+  for (int64_t i0 = me / per_row; i0 < a.num_slots; i0 += static_cast<int64_t>(step) * kAppendRows) {
+    int slot[kAppendRows], row[kAppendRows];
+#pragma unroll
+    for (int r = 0; r < kAppendRows; ++r) {
+      const int64_t i = i0 + static_cast<int64_t>(r) * step;
+      slot[r] = i < a.num_slots ? a.slots[i] : -1;
+      row[r] = static_cast<int>(i);
+      if (a.rows) row[r] = i < a.num_slots ? a.rows[i] : -1;
+      if (slot[r] >= a.pool_rows || row[r] < 0 || row[r] >= a.num_rows) slot[r] = -1;
+    }
+    uint4 u[kAppendRows][kLoads];
+#pragma unroll
+    for (int r = 0; r < kAppendRows; ++r)
+      if (slot[r] >= 0)
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) u[r][q] = load_once(src + row[r] * stride + kVec * c + 8 * q);
+#pragma unroll
+    for (int r = 0; r < kAppendRows; ++r) {
+      if (slot[r] < 0) continue;
+      const int64_t at = static_cast<int64_t>(slot[r]) * a.row_elems + kVec * c;
+      if constexpr (kFp8) {
+        uint32_t code[4];
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) {
+          const uint32_t w[4] = {u[r][q].x, u[r][q].y, u[r][q].z, u[r][q].w};
+          uint32_t half[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int x = 8 * q + 2 * e;
+            half[e] = e4m3x2(quotient_to_odd(__uint_as_float(w[e] << 16), sc[x], inv[x]),
+                             quotient_to_odd(__uint_as_float(w[e] & 0xffff0000u), sc[x + 1], inv[x + 1]));
+          }
+          code[2 * q] = half[0] | (half[1] << 16);
+          code[2 * q + 1] = half[2] | (half[3] << 16);
+        }
+        *reinterpret_cast<uint4*>(dst + at) = make_uint4(code[0], code[1], code[2], code[3]);
+      } else {
+        *reinterpret_cast<uint4*>(dst + 2 * at) = u[r][0];
+      }
+    }
   }
 }
 
 }  // namespace
 
 cudaError_t launch_tree_mask(const TreeMaskArgs& a, cudaStream_t stream) {
-  tree_mask_kernel<<<a.num_seqs, kMaskThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  const int threads = (a.max_nodes + 31) / 32 * 32;
+  auto go = [&](auto kernel, int words) {
+    const size_t smem = static_cast<size_t>(threads) * (words * sizeof(uint64_t) + sizeof(int16_t));
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (e != cudaSuccess) return e;
+    }
+    kernel<<<a.num_seqs, threads, smem, stream>>>(a);
+    return cudaGetLastError();
+  };
+  if (a.words == 1) return go(tree_mask_kernel<1>, 1);
+  if (a.words == 2) return go(tree_mask_kernel<2>, 2);
+  if (a.words <= 4) return go(tree_mask_kernel<4>, 4);
+  return go(tree_mask_kernel<16>, 16);
 }
 
 cudaError_t launch_kv_plan(const PlanArgs& a, cudaStream_t stream) {
-  const int blocks = min(152, (a.num_tokens + kPlanThreads - 1) / kPlanThreads);
-  kv_plan_kernel<<<max(blocks, 1), kPlanThreads, 0, stream>>>(a);
+  const int blocks = min(152, a.num_tokens / kPlanThreads + 1);
+  kv_plan_kernel<<<blocks, kPlanThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
-  const int64_t total = static_cast<int64_t>(a.num_slots) * (a.row_elems / 8);
-  const int64_t blocks = (total + kAppendThreads - 1) / kAppendThreads;
-  const dim3 grid(static_cast<unsigned>(blocks < 152 * 8 ? blocks : 152 * 8), 2);
+  const int per_row = a.row_elems / (a.k_scale ? 16 : 8);
+  // eight blocks an SM for each of K and V (E4M3: four, a thread inverts 16 scales before its rows), in
+  // whole rows, no more than there are rows
+  const int64_t most = static_cast<int64_t>(a.num_slots) * per_row;
+  int64_t threads = 152 * (a.k_scale ? 4 : 8) * kAppendThreads / per_row * per_row;
+  if (threads == 0) threads = per_row;
+  if (threads > most) threads = most;
+  const dim3 grid(static_cast<unsigned>((threads + kAppendThreads - 1) / kAppendThreads), 2);
   if (a.k_scale)
-    kv_append_fp8_kernel<<<grid, kAppendThreads, 0, stream>>>(a);
+    kv_append_kernel<true><<<grid, kAppendThreads, 0, stream>>>(a, static_cast<int>(threads));
   else
-    kv_append_bf16_kernel<<<grid, kAppendThreads, 0, stream>>>(a);
+    kv_append_kernel<false><<<grid, kAppendThreads, 0, stream>>>(a, static_cast<int>(threads));
   return cudaGetLastError();
 }
 

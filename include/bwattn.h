@@ -367,7 +367,8 @@ int attn_tree_mask(const int32_t* parents, const int32_t* cu_seqlens_q, const in
  *                 whose table entries are -1: nothing of the plan may then be used, release pages and
  *                 plan again
  * The outputs must not overlap the inputs (equal pointers: INVALID_ARG). page_size is a multiple of 16,
- * 16..1024. The call may be repeated on the same inputs with the same results.
+ * 16..1024, B * max_pages_per_seq below 2^31. The call may be repeated on the same inputs with the same
+ * results.
  */
 int kv_plan_paged(const int32_t* nk, const int32_t* n_new, int32_t* block_table, const int32_t* held,
                   const int32_t* free_pages, const int32_t* free_count, int32_t* nk_out, int32_t* held_out,
