@@ -239,6 +239,13 @@ __device__ __forceinline__ float quotient_to_odd(float x, float s, float r) {
   // beyond 1024 the conversion saturates (or keeps NaN), whatever the last bits; -0 stays -0
   return copysignf(fabsf(q0) <= 1024.f ? __int_as_float(bits) : q0, x);
 }
+// Whether x r may round to another code than x / s does: it is within two steps of the last bit of the
+// quotient (r and the product round once each), so only next to a border, which has the format's three
+// fraction bits and a half; below 2^-6, where the format's steps no longer shrink, always.
+__device__ __forceinline__ bool near_border(float q) {
+  const uint32_t b = __float_as_uint(q);
+  return ((b - 0x80000u + 4u) & 0xfffffu) <= 8u || (b & 0x7fffffffu) < 0x3c800000u;
+}
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
@@ -289,20 +296,29 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
       if (slot[r] < 0) continue;
       const int64_t at = static_cast<int64_t>(slot[r]) * a.row_elems + kVec * c;
       if constexpr (kFp8) {
+        // the products first; where one is next to a border (one thread in some 10^4) the exact quotients
+        float q[kVec];
+        bool near = false;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          const uint4& w4 = u[r][e / 8];
+          const uint32_t w = (e / 2) % 4 == 0 ? w4.x : (e / 2) % 4 == 1 ? w4.y : (e / 2) % 4 == 2 ? w4.z : w4.w;
+          q[e] = __uint_as_float(e % 2 ? w & 0xffff0000u : w << 16);
+        }
+        float x[kVec];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          x[e] = q[e] * inv[e];
+          near |= near_border(x[e]);
+        }
+        if (near) {
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) x[e] = quotient_to_odd(q[e], sc[e], inv[e]);
+        }
         uint32_t code[4];
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q) {
-          const uint32_t w[4] = {u[r][q].x, u[r][q].y, u[r][q].z, u[r][q].w};
-          uint32_t half[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int x = 8 * q + 2 * e;
-            half[e] = e4m3x2(quotient_to_odd(__uint_as_float(w[e] << 16), sc[x], inv[x]),
-                             quotient_to_odd(__uint_as_float(w[e] & 0xffff0000u), sc[x + 1], inv[x + 1]));
-          }
-          code[2 * q] = half[0] | (half[1] << 16);
-          code[2 * q + 1] = half[2] | (half[3] << 16);
-        }
+        for (int e = 0; e < 4; ++e)
+          code[e] = e4m3x2(x[4 * e], x[4 * e + 1]) | (e4m3x2(x[4 * e + 2], x[4 * e + 3]) << 16);
         *reinterpret_cast<uint4*>(dst + at) = make_uint4(code[0], code[1], code[2], code[3]);
       } else {
         *reinterpret_cast<uint4*>(dst + 2 * at) = u[r][0];

@@ -13,9 +13,9 @@
 // may have more than 128 rows, so that a cache byte serves up to 256.
 //
 // Split: lengths are on the device, and one long sequence has to fill the GPU as well as many short
-// ones. The key tiles of all units form one list (unit after unit, context tiles, then drafts), and
-// CTA c of G takes tiles [c T / G, (c + 1) T / G): no CTA has more than one tile above another,
-// whatever the lengths. A unit that lies within one CTA's range is finished there; otherwise each
+// ones. The key tiles of all units form one list (unit after unit: tree_unit_cost places for what a unit
+// costs beside its tiles, its context tiles, then its drafts), and CTA c of G takes places
+// [c T / G, (c + 1) T / G), whatever the lengths. A unit that lies within one CTA's range is finished there; otherwise each
 // CTA that has a part of it writes its (m, l, o), at most two such parts per CTA, and a second,
 // dependent launch merges them in the order of the keys (no atomics: results do not depend on which
 // CTA ends first).
@@ -40,6 +40,8 @@
 // Every wait is bounded; a timed-out wait sets the device status word, the CTA stops producing
 // output, waits for its own copies and MMAs and frees its TMEM.
 #include <math.h>
+
+#include <atomic>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -120,16 +122,18 @@ static_assert(sizeof(Barriers) <= kBarBytes, "barrier block");
 __device__ __forceinline__ bool vote(bool x) { return __all_sync(0xffffffffu, x); }
 
 // Tiles of one sequence.
+template <int D>
 struct SeqTiles {
   int tok0, nq, nk;
   int ct, per_unit;  // context tiles, all tiles of a unit
   int row_units;     // units of a KV head
-  __device__ __forceinline__ int all(int Hkv) const { return per_unit * row_units * Hkv; }  // the host bounds the sum
+  // places of the list; the host bounds their sum
+  __device__ __forceinline__ int all(int Hkv) const { return (per_unit + tree_unit_cost(D)) * row_units * Hkv; }
 };
 template <int D, int kTiles>
-__device__ __forceinline__ SeqTiles seq_tiles(const TreeArgs& a, int b) {
+__device__ __forceinline__ SeqTiles<D> seq_tiles(const TreeArgs& a, int b) {
   constexpr int kKeys = Cfg<D, kTiles>::kKeys;
-  SeqTiles s;
+  SeqTiles<D> s;
   s.tok0 = min(max(a.cu_q[b], 0), a.total_q);
   s.nq = min(min(max(a.cu_q[b + 1], s.tok0), a.total_q) - s.tok0, a.max_nodes);
   s.nk = min(max(a.nk[b], 0), a.kv_cap);
@@ -222,6 +226,63 @@ __device__ __forceinline__ void give_registers() {
 template <bool kSplit>
 __device__ __forceinline__ void take_registers() {
   if constexpr (kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+}
+
+// Softmax of a row's tile in which not every key counts: the context's last tile (the first `left` keys)
+// and the tiles of drafts (those of them whose bit is set, from bit `bit0` of `bits` on; null: no mask). 32
+// keys at a time and no further than the last that counts, S read twice, for the maximum and for the
+// weights; P of chunk c goes to columns 16 c on, over S that has been read if that is where it goes.
+// Out of line: few tiles take it, and in the loop its code and registers cost the others 10 to 30 %.
+// Returns the new reference maximum, the sum of the weights and the factor for l and o.
+struct MaskedTile {
+  float m, l, alpha;
+};
+__device__ __noinline__ MaskedTile masked_tile(uint32_t tS, uint32_t tP, int left, const uint64_t* bits, int bit0, float sl2,
+                                               float m_ref) {
+  const int chunks = (left + 31) / 32;
+  auto load = [&](int c, uint32_t (&v)[32]) {
+    const int rest = left - 32 * c, bit = bit0 + 32 * c;
+    uint32_t keep = rest >= 32 ? 0xffffffffu : (1u << rest) - 1u;
+    if (bits) keep &= static_cast<uint32_t>(bits[bit >> 6] >> (bit & 32));
+    tmem_ld32(tS + 32 * c, v);
+    tmem_wait_ld();
+    tmem_reg_fence(v);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!(keep >> e & 1)) v[e] = __float_as_uint(-INFINITY);
+  };
+  float mt = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    uint32_t v[32];
+    load(c, v);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) mt = max3f(mt, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+  }
+  MaskedTile r{m_ref, 0.f, 1.f};
+  const float m_new = fmaxf(m_ref, mt * sl2);
+  if (m_new > m_ref + kRescaleThreshold) {
+    r.alpha = (m_ref == -INFINITY) ? 0.f : ex2(m_ref - m_new);
+    r.m = m_new;
+  }
+  const float nm = (r.m == -INFINITY) ? 0.f : -r.m;
+  float l0 = 0.f, l1 = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    uint32_t v[32], pk[16];
+    load(c, v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float x0, x1;
+      ffma2(x0, x1, __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]), sl2, nm);
+      const float p0 = ex2(x0), p1 = ex2(x1);
+      fadd2(l0, l1, p0, p1);
+      pk[e] = pack_bf16x2(p0, p1);
+    }
+    tmem_st16(tP + 16 * c, pk);
+  }
+  r.l = l0 + l1;
+  return r;
 }
 
 template <int D, int kTiles>
@@ -414,16 +475,21 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     int pos = begin, b = pos < end ? bar->list[1] : 0, seq_at = pos < end ? bar->list[2] : 0;
     int nload = 0, nq[2] = {0, 0};  // K tiles, and Q tiles into each buffer
     bool ok = true;
-    if (begin == end && lane == 0) a.merge[c] = TreeMergeRec{};  // no part here
     for (int k = 0; ok; ++k) {
       Seg s{};
-      if (pos < end) {
-        SeqTiles q = seq_tiles<D, kTiles>(a, b);
+      while (pos < end && !s.valid) {
+        SeqTiles<D> q = seq_tiles<D, kTiles>(a, b);
         while (pos >= seq_at + q.all(a.Hkv)) {
           seq_at += q.all(a.Hkv);
           q = seq_tiles<D, kTiles>(a, ++b);
         }
-        const int local = pos - seq_at, unit = local / q.per_unit;
+        const int size = q.per_unit + tree_unit_cost(D), local = pos - seq_at, unit = local / size;
+        const int at = local - unit * size, to = min(size, at + end - pos);  // places of the unit
+        const int u0 = pos - at;
+        pos += to - at;
+        s.k0 = max(at - tree_unit_cost(D), 0);
+        s.nt = to - tree_unit_cost(D) - s.k0;
+        if (s.nt <= 0) break;  // the range ends before the unit's first tile
         s.valid = 1;
         s.b = b;
         s.tok0 = q.tok0;
@@ -431,26 +497,23 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         s.nk = q.nk;
         s.hkv = unit / q.row_units;
         s.node0 = (unit - s.hkv * q.row_units) * (kTiles * tile_nodes);
-        s.k0 = local - unit * q.per_unit;
-        s.nt = min(q.per_unit - s.k0, end - pos);
         s.ct = q.ct;
-        s.slot = s.nt == q.per_unit ? -1 : (pos == begin ? 0 : 1);
-        pos += s.nt;
+        s.slot = s.nt == q.per_unit ? -1 : (k == 0 ? 0 : 1);
         if (k == 0 && lane == 0) {
           TreeMergeRec r{};
-          const int u0 = begin - s.k0;
-          if (s.k0 > 0 && share.owner(u0) == c - 1) {
+          if (s.k0 > 0 && share.owner(u0 + tree_unit_cost(D)) == c - 1) {
             r.rows0 = tile_rows(s, 0);
             r.rows1 = kTiles == 2 ? tile_rows(s, 1) : 0;
             r.node0 = s.tok0 + s.node0;
             r.node_step = tile_nodes;
             r.hkv = s.hkv;
-            r.slot0 = u0 == share.begin(c - 1) ? 0 : 1;
-            r.last = share.owner(u0 + q.per_unit - 1);
+            r.slot0 = u0 <= share.begin(c - 1) ? 0 : 1;
+            r.last = share.owner(u0 + size - 1);
           }
           a.merge[c] = r;
         }
       }
+      if (k == 0 && !s.valid && lane == 0) a.merge[c] = TreeMergeRec{};  // no part here
       if (k >= kSegSlots && !(ok = vote(mbar_wait(&bar->seg_empty[k % kSegSlots], (k / kSegSlots - 1) & 1, tmo, abort))))
         break;
       if (lane == 0) {
@@ -689,81 +752,74 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         tc_fence_after();
         if (warp_ok) {
           const int kt = s.k0 + j;
+          float alpha_o = 1.f;
           if (kt >= masked_from) {
-            // keys that the row does not see become -inf in tensor memory, 32 at a time (rolled, and apart
-            // from the common path: code that is jumped over still costs the loop its instruction fetches):
-            // the context's last tile ends at nk, drafts go by the mask's bits, none past the last node
+            if (C::kSplitP && n > 0) {
+              if (!(ok = vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort)))) break;
+              tc_fence_after();
+            }
             const bool draft = kt >= s.ct;
             const int left = draft ? s.nq - (kt - s.ct) * kKeys : s.nk - kt * kKeys;
-#pragma unroll 1
+            const MaskedTile r = masked_tile(tS, tP, min(left, kKeys), draft ? bits : nullptr, (kt - s.ct) * kKeys, sl2, m_ref);
+            m_ref = r.m;
+            l = l * r.alpha + r.l;
+            if (j > 0) alpha_o = r.alpha;
+            if constexpr (C::kSplitP) {
+              tc_fence_before();
+              mbar_arrive(&bar->s_free[x]);
+            }
+          } else {
+            uint32_t sc[kKeys / 32][32];
+#pragma unroll
+            for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(tS + 32 * c, sc[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < kKeys / 32; ++c) tmem_reg_fence(sc[c]);
+            if constexpr (C::kSplitP) {
+              tc_fence_before();
+              mbar_arrive(&bar->s_free[x]);  // S is in registers
+            }
+            float mx[kKeys / 32];
+#pragma unroll
             for (int c = 0; c < kKeys / 32; ++c) {
-              const int rest = left - 32 * c;
-              uint32_t keep = rest >= 32 ? 0xffffffffu : rest > 0 ? (1u << rest) - 1u : 0u;
-              if (draft) {
-                const int bit = (kt - s.ct) * kKeys + 32 * c;  // of the row's mask
-                keep &= bit < 64 * a.mask_words ? static_cast<uint32_t>(bits[bit >> 6] >> (bit & 32)) : 0u;
+              mx[c] = __uint_as_float(sc[c][0]);
+#pragma unroll
+              for (int e = 1; e < 31; e += 2) mx[c] = max3f(mx[c], __uint_as_float(sc[c][e]), __uint_as_float(sc[c][e + 1]));
+              mx[c] = fmaxf(mx[c], __uint_as_float(sc[c][31]));
+            }
+            float mt = mx[0];
+#pragma unroll
+            for (int c = 1; c < kKeys / 32; ++c) mt = fmaxf(mt, mx[c]);
+            const float m_new = fmaxf(m_ref, mt * sl2);
+            if (m_new > m_ref + kRescaleThreshold) {
+              const float alpha = (m_ref == -INFINITY) ? 0.f : ex2(m_ref - m_new);
+              l *= alpha;
+              if (j > 0) alpha_o = alpha;
+              m_ref = m_new;
+            }
+            const float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
+            if (C::kSplitP && n > 0) {
+              // the stream's previous P.V has read the P columns, and O holds it
+              if (!(ok = vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort)))) break;
+              tc_fence_after();
+            }
+            // p = 2^(s scale log2e - m) as bf16 pairs into the first half of the S columns; l is the fp32
+            // sum before that rounding
+            float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < kKeys / 32; ++c) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float x0, x1;
+                ffma2(x0, x1, __uint_as_float(sc[c][2 * e]), __uint_as_float(sc[c][2 * e + 1]), sl2, nm);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                fadd2(ls[(2 * e) & 7], ls[(2 * e + 1) & 7], p0, p1);
+                pk[e] = pack_bf16x2(p0, p1);
               }
-              uint32_t x[32];
-              tmem_ld32(tS + 32 * c, x);
-              tmem_wait_ld();
-              tmem_reg_fence(x);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(keep >> e & 1)) x[e] = __float_as_uint(-INFINITY);
-              tmem_st32(tS + 32 * c, x);
+              tmem_st16(tP + 16 * c, pk);
             }
-            tmem_wait_st();
-          }
-          uint32_t sc[kKeys / 32][32];
-#pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(tS + 32 * c, sc[c]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) tmem_reg_fence(sc[c]);
-          if constexpr (C::kSplitP) {
-            tc_fence_before();
-            mbar_arrive(&bar->s_free[x]);  // S is in registers
-          }
-          float mx[kKeys / 32];
-#pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) {
-            mx[c] = __uint_as_float(sc[c][0]);
-#pragma unroll
-            for (int e = 1; e < 31; e += 2) mx[c] = max3f(mx[c], __uint_as_float(sc[c][e]), __uint_as_float(sc[c][e + 1]));
-            mx[c] = fmaxf(mx[c], __uint_as_float(sc[c][31]));
-          }
-          float mt = mx[0];
-#pragma unroll
-          for (int c = 1; c < kKeys / 32; ++c) mt = fmaxf(mt, mx[c]);
-          const float m_new = fmaxf(m_ref, mt * sl2);
-          float alpha_o = 1.f;
-          if (m_new > m_ref + kRescaleThreshold) {
-            const float alpha = (m_ref == -INFINITY) ? 0.f : ex2(m_ref - m_new);
-            l *= alpha;
-            if (j > 0) alpha_o = alpha;
-            m_ref = m_new;
-          }
-          const float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
-          if (C::kSplitP && n > 0) {
-            // the stream's previous P.V has read the P columns, and O holds it
-            if (!(ok = vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort)))) break;
-            tc_fence_after();
-          }
-          // p = 2^(s scale log2e - m) as bf16 pairs into the first half of the S columns; l is the fp32
-          // sum before that rounding
-          float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float x0, x1;
-              ffma2(x0, x1, __uint_as_float(sc[c][2 * e]), __uint_as_float(sc[c][2 * e + 1]), sl2, nm);
-              const float p0 = ex2(x0), p1 = ex2(x1);
-              fadd2(ls[(2 * e) & 7], ls[(2 * e + 1) & 7], p0, p1);
-              pk[e] = pack_bf16x2(p0, p1);
-            }
-            tmem_st16(tP + 16 * c, pk);
+            l += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
           }
           // O must carry the new reference maximum before this tile's P.V (rare)
           if (__any_sync(0xffffffffu, alpha_o != 1.f)) {
@@ -787,7 +843,6 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&bar->p_full[x]);
-          l += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
         } else {
           if constexpr (C::kSplitP) {
             // a warp without rows may not run ahead either: its arrivals for the next P would count for this
@@ -936,10 +991,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const floa
 }
 
 template <int D, int kTiles>
-cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
+cudaError_t launch(const TreeArgs& a, int dev, cudaStream_t stream) {
   using C = Cfg<D, kTiles>;
-  cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
-  if (e != cudaSuccess) return e;
+  // once per device (the attribute stays with the device's copy of the kernel)
+  static std::atomic<uint64_t> set{0};
+  cudaError_t e;
+  if (dev >= 64 || !(set.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(tree_kernel<D, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set.fetch_or(1ull << dev);
+  }
   tree_kernel<D, kTiles><<<a.ctas, C::kThreads, C::kSmem, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   count_launch();
@@ -1000,9 +1061,9 @@ cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
   const int fit = tiles == 1 && d <= 128 ? 2 * sms : sms;
   a.ctas = tree_max_ctas(tiles, d) < fit ? tree_max_ctas(tiles, d) : fit;
   if (a.ctas > most) a.ctas = static_cast<int>(most);
-  if (d == 64) return tiles == 2 ? launch<64, 2>(a, stream) : launch<64, 1>(a, stream);
-  if (d == 128) return tiles == 2 ? launch<128, 2>(a, stream) : launch<128, 1>(a, stream);
-  return launch<256, 1>(a, stream);
+  if (d == 64) return tiles == 2 ? launch<64, 2>(a, dev, stream) : launch<64, 1>(a, dev, stream);
+  if (d == 128) return tiles == 2 ? launch<128, 2>(a, dev, stream) : launch<128, 1>(a, dev, stream);
+  return launch<256, 1>(a, dev, stream);
 }
 
 }  // namespace bw
