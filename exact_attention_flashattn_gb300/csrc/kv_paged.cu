@@ -211,12 +211,13 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
 // A copy of row_elems elements from row rows[i] (or i) of k_new and v_new to row slots[i] of the
 // pool; slots or rows outside their range are skipped. A thread moves 16 bytes of a row.
 //
-// A thread keeps its channels (kVec of them, 16 bytes of output) and takes rows a grid apart, kAppendRows
-// at a time: their slots first, then their data, so that its loads overlap; with E4M3 pages the
-// channels' scales and reciprocals stay in registers (reading and inverting them for every element took
-// 47 us on 20001 rows of 8 x 128, twice the bytes' time).
+// A thread keeps its channels (kVec of them, 16 bytes of output) and takes rows a grid apart, kRows
+// at a time: their slots first, then their data, so that its loads overlap. With E4M3 pages the
+// reciprocals of the channels' scales stay in registers (reading and inverting the scales for every
+// element took 47 us on 20001 rows of 8 x 128, dividing each element exactly 36 us, a bracket around
+// each 22 us, 5.5 TB/s; without the check 20.5 us). The bytes bound the copy: 32768 rows of 8 x 128 in
+// 42 us, 6.4 TB/s.
 constexpr int kAppendThreads = 256;
-constexpr int kAppendRows = 4;
 
 __device__ __forceinline__ uint4 load_once(const void* p) {
   uint4 v;
@@ -224,27 +225,32 @@ __device__ __forceinline__ uint4 load_once(const void* p) {
   return v;
 }
 
-// The E4M3 code nearest to x / s (ties to even, magnitudes past 448 to 448, NaN to NaN), two at a
-// time. r = RN(1 / s); q = x r corrected once by its remainder is RN(x / s) (Markstein's division,
-// 1990). Its 24 bits may fall on a border between two codes, or on the wrong side of one, where the
-// quotient does not; the exact remainder says on which side of q the quotient lies, so q is turned
-// into the quotient cut off towards zero with its last bit set where it is inexact (rounding to
-// odd), and the conversion of that rounds the quotient itself.
-__device__ __forceinline__ float quotient_to_odd(float x, float s, float r) {
-  const float q0 = x * r;
-  const float q1 = fmaf(fmaf(-q0, s, x), r, q0);
-  const float rem = fmaf(-q1, s, x);
-  int bits = __float_as_int(q1);
+// The E4M3 code nearest to x / s (ties to even, magnitudes past 448 to 448, NaN to NaN). Rounding is
+// monotonic, so where x r_lo and x r_hi, which bracket x / s, have the same code it is the quotient's:
+// r_lo and r_hi are RN(1 / s) less and more 2^-22 of it, twice what the reciprocal and the product
+// round together. Where the codes differ (one warp in some hundred) a border between two codes is near,
+// and the quotient is rounded to odd: RN(x / s) may fall on a border, or on the wrong side of one, where
+// the quotient does not; the exact remainder says on which side of it the quotient lies, so it is
+// turned into the quotient cut off towards zero with its last bit set where it is inexact, and the
+// conversion of that rounds the quotient itself. A power of two has an exact reciprocal and exact
+// products, borders among them: r_lo = r_hi.
+struct Bracket {
+  float lo, hi;
+};
+__device__ __forceinline__ Bracket bracket(float s) {
+  const float r = __frcp_rn(s);
+  if ((__float_as_uint(s) & 0x7fffffu) == 0) return {r, r};
+  if (r < 0x1p-126f) return {0.f, __int_as_float(0x7f800000)};  // too few bits left: always the quotient
+  return {fmaf(r, -0x1p-22f, r), fmaf(r, 0x1p-22f, r)};
+}
+__device__ __noinline__ float quotient_to_odd(float x, float s) {
+  if (s < 0x1p-64f) x *= 0x1p64f, s *= 0x1p64f;  // keeps the remainder above the smallest number
+  const float q = __fdiv_rn(x, s);
+  const float rem = fmaf(-q, s, x);
+  int bits = __float_as_int(q);
   if (rem != 0.f) bits = (bits + ((__float_as_int(rem) ^ __float_as_int(x)) >> 31)) | 1;
   // beyond 1024 the conversion saturates (or keeps NaN), whatever the last bits; -0 stays -0
-  return copysignf(fabsf(q0) <= 1024.f ? __int_as_float(bits) : q0, x);
-}
-// Whether x r may round to another code than x / s does: it is within two steps of the last bit of the
-// quotient (r and the product round once each), so only next to a border, which has the format's three
-// fraction bits and a half; below 2^-6, where the format's steps no longer shrink, always.
-__device__ __forceinline__ bool near_border(float q) {
-  const uint32_t b = __float_as_uint(q);
-  return ((b - 0x80000u + 4u) & 0xfffffu) <= 8u || (b & 0x7fffffffu) < 0x3c800000u;
+  return copysignf(fabsf(q) <= 1024.f ? __int_as_float(bits) : q, x);
 }
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
@@ -256,6 +262,7 @@ template <bool kFp8>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a, int threads) {
   constexpr int kVec = kFp8 ? 16 : 8;
   constexpr int kLoads = kVec / 8;
+  constexpr int kRows = kFp8 ? 6 : 4;
   const bool is_v = blockIdx.y == 1;
   const uint16_t* src = is_v ? a.v_new : a.k_new;
   uint8_t* dst = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages);
@@ -264,66 +271,76 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
   const int me = blockIdx.x * kAppendThreads + threadIdx.x;
   if (me >= threads) return;  // `threads` is a multiple of per_row
   const int c = me % per_row, step = threads / per_row;
-  float sc[kVec], inv[kVec];
-  if constexpr (kFp8) {
-    const float* scale = (is_v ? a.v_scale : a.k_scale) + kVec * c;
+  const float* scale = (is_v ? a.v_scale : a.k_scale) + kVec * c;
+  struct Rows {
+    int slot[kRows];
+    uint4 u[kRows][kLoads];
+  };
+  const int64_t stride_i = static_cast<int64_t>(step) * kRows;
+  auto fetch = [&](Rows& w, int64_t i0) {
+    int row[kRows];
 #pragma unroll
-    for (int e = 0; e < kVec; e += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(scale + e);
-      sc[e] = v.x, sc[e + 1] = v.y, sc[e + 2] = v.z, sc[e + 3] = v.w;
-    }
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) inv[e] = __frcp_rn(sc[e]);
-  }
-  for (int64_t i0 = me / per_row; i0 < a.num_slots; i0 += static_cast<int64_t>(step) * kAppendRows) {
-    int slot[kAppendRows], row[kAppendRows];
-#pragma unroll
-    for (int r = 0; r < kAppendRows; ++r) {
+    for (int r = 0; r < kRows; ++r) {
       const int64_t i = i0 + static_cast<int64_t>(r) * step;
-      slot[r] = i < a.num_slots ? a.slots[i] : -1;
+      w.slot[r] = i < a.num_slots ? a.slots[i] : -1;
       row[r] = static_cast<int>(i);
       if (a.rows) row[r] = i < a.num_slots ? a.rows[i] : -1;
-      if (slot[r] >= a.pool_rows || row[r] < 0 || row[r] >= a.num_rows) slot[r] = -1;
+      if (w.slot[r] >= a.pool_rows || row[r] < 0 || row[r] >= a.num_rows) w.slot[r] = -1;
     }
-    uint4 u[kAppendRows][kLoads];
 #pragma unroll
-    for (int r = 0; r < kAppendRows; ++r)
-      if (slot[r] >= 0)
+    for (int r = 0; r < kRows; ++r)
+      if (w.slot[r] >= 0)
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q) u[r][q] = load_once(src + row[r] * stride + kVec * c + 8 * q);
+        for (int q = 0; q < kLoads; ++q) w.u[r][q] = load_once(src + row[r] * stride + kVec * c + 8 * q);
+  };
+  Bracket inv[kVec];
+  auto store = [&](const Rows& w) {
 #pragma unroll
-    for (int r = 0; r < kAppendRows; ++r) {
-      if (slot[r] < 0) continue;
-      const int64_t at = static_cast<int64_t>(slot[r]) * a.row_elems + kVec * c;
+    for (int r = 0; r < kRows; ++r) {
+      if (w.slot[r] < 0) continue;
+      const int64_t at = static_cast<int64_t>(w.slot[r]) * a.row_elems + kVec * c;
       if constexpr (kFp8) {
-        // the products first; where one is next to a border (one thread in some 10^4) the exact quotients
-        float q[kVec];
-        bool near = false;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          const uint4& w4 = u[r][e / 8];
-          const uint32_t w = (e / 2) % 4 == 0 ? w4.x : (e / 2) % 4 == 1 ? w4.y : (e / 2) % 4 == 2 ? w4.z : w4.w;
-          q[e] = __uint_as_float(e % 2 ? w & 0xffff0000u : w << 16);
-        }
         float x[kVec];
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-          x[e] = q[e] * inv[e];
-          near |= near_border(x[e]);
+          const uint4& w4 = w.u[r][e / 8];
+          const uint32_t h = (e / 2) % 4 == 0 ? w4.x : (e / 2) % 4 == 1 ? w4.y : (e / 2) % 4 == 2 ? w4.z : w4.w;
+          x[e] = __uint_as_float(e % 2 ? h & 0xffff0000u : h << 16);
         }
-        if (near) {
+        uint32_t code[4], differ = 0;
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) x[e] = quotient_to_odd(q[e], sc[e], inv[e]);
+        for (int e = 0; e < kVec; e += 4) {
+          code[e / 4] = e4m3x2(x[e] * inv[e].lo, x[e + 1] * inv[e + 1].lo) |
+                        (e4m3x2(x[e + 2] * inv[e + 2].lo, x[e + 3] * inv[e + 3].lo) << 16);
+          differ |= code[e / 4] ^ (e4m3x2(x[e] * inv[e].hi, x[e + 1] * inv[e + 1].hi) |
+                                   (e4m3x2(x[e + 2] * inv[e + 2].hi, x[e + 3] * inv[e + 3].hi) << 16));
         }
-        uint32_t code[4];
+        if (differ) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          code[e] = e4m3x2(x[4 * e], x[4 * e + 1]) | (e4m3x2(x[4 * e + 2], x[4 * e + 3]) << 16);
+          for (int e = 0; e < kVec; e += 4)
+            code[e / 4] = e4m3x2(quotient_to_odd(x[e], scale[e]), quotient_to_odd(x[e + 1], scale[e + 1])) |
+                          (e4m3x2(quotient_to_odd(x[e + 2], scale[e + 2]), quotient_to_odd(x[e + 3], scale[e + 3])) << 16);
+        }
         *reinterpret_cast<uint4*>(dst + at) = make_uint4(code[0], code[1], code[2], code[3]);
       } else {
-        *reinterpret_cast<uint4*>(dst + 2 * at) = u[r][0];
+        *reinterpret_cast<uint4*>(dst + 2 * at) = w.u[r][0];
       }
     }
+  };
+  int64_t i0 = me / per_row;
+  Rows w;
+  fetch(w, i0);
+  if constexpr (kFp8) {
+#pragma unroll
+    for (int e = 0; e < kVec; e += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(scale + e);
+      inv[e] = bracket(v.x), inv[e + 1] = bracket(v.y), inv[e + 2] = bracket(v.z), inv[e + 3] = bracket(v.w);
+    }
+  }
+  for (;;) {
+    store(w);
+    if ((i0 += stride_i) >= a.num_slots) break;
+    fetch(w, i0);
   }
 }
 
@@ -354,10 +371,11 @@ cudaError_t launch_kv_plan(const PlanArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
   const int per_row = a.row_elems / (a.k_scale ? 16 : 8);
-  // eight blocks an SM for each of K and V (E4M3: four, a thread inverts 16 scales before its rows), in
-  // whole rows, no more than there are rows
+  // E4M3: one block an SM for each of K and V, as a thread inverts 16 scales before its rows (20001 rows
+  // of 8 x 128: 23.1 us, four blocks 29.9); a copy has nothing to set up and 32 even out the SMs (32768
+  // rows: 41.9 us, eight 42.5). In whole rows, no more than there are rows.
   const int64_t most = static_cast<int64_t>(a.num_slots) * per_row;
-  int64_t threads = 152 * (a.k_scale ? 4 : 8) * kAppendThreads / per_row * per_row;
+  int64_t threads = 152 * (a.k_scale ? 1 : 32) * kAppendThreads / per_row * per_row;
   if (threads == 0) threads = per_row;
   if (threads > most) threads = most;
   const dim3 grid(static_cast<unsigned>((threads + kAppendThreads - 1) / kAppendThreads), 2);
