@@ -42,6 +42,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -62,8 +63,8 @@ struct Cfg {
   static constexpr int kCtasPerSm = kTiles == 1 && D <= 128 ? 2 : 1;
   static constexpr uint32_t kQBytes = kTreeRows * D * 2;
   static constexpr uint32_t kTileBytes = kKeys * D * 2;
-  // ring slots, K tiles in the even ones, V tiles in the odd
-  static constexpr int kStages = (D == 64 ? 8 : 4) / kCtasPerSm;
+  // ring slots, which tiles of K and V take in turns: as many as fit
+  static constexpr int kStages = kCtasPerSm == 2 ? (D == 64 ? 4 : 2) : (D == 64 ? 8 : 5);
   static constexpr uint32_t kRing = kTiles * kQBytes;
   static constexpr uint32_t kBar = kRing + kStages * kTileBytes;
   static constexpr uint32_t kSmem = kBar + kBarBytes + 1024;  // + alignment slack
@@ -215,18 +216,21 @@ __device__ __forceinline__ bool clean_v(uint8_t* tile, int valid, bool scan, int
   return __any_sync(0xffffffffu, bad);
 }
 
-// Registers: a softmax thread holds a row's 128 scores, the other four warps little. A block of 256
-// threads (two of them on an SM) has 256 x 128; 128 x 184 + 128 x 72 is the same number.
-constexpr int kSoftRegs = 184, kOtherRegs = 72;
-static_assert(128 * kSoftRegs + 128 * kOtherRegs <= 256 * 128, "register split");
-template <bool kSplit>
-__device__ __forceinline__ void give_registers() {
-  if constexpr (kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-}
-template <bool kSplit>
-__device__ __forceinline__ void take_registers() {
-  if constexpr (kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-}
+// Registers: a softmax thread holds a row's 128 scores, the other four warps little; at d = 256 a row has 64
+// and all have enough. A block's threads share what they were launched with: 256 x 128 (two on an SM) or
+// 384 x 168.
+template <int D, int kTiles>
+struct Regs {
+  static constexpr bool kSplit = D <= 128;
+  static constexpr int kSoft = kTiles == 1 ? 184 : 192, kOther = kTiles == 1 ? 72 : 112;
+  static_assert(!kSplit || kTiles * 128 * kSoft + 128 * kOther <= (kTiles == 1 ? 256 * 128 : 384 * 168), "register split");
+  static __device__ __forceinline__ void give() {
+    if constexpr (kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOther));
+  }
+  static __device__ __forceinline__ void take() {
+    if constexpr (kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoft));
+  }
+};
 
 // Softmax of a row's tile in which not every key counts: the context's last tile (the first `left` keys)
 // and the tiles of drafts (those of them whose bit is set, from bit `bit0` of `bits` on; null: no mask). 32
@@ -288,7 +292,7 @@ __device__ __noinline__ MaskedTile masked_tile(uint32_t tS, uint32_t tP, int lef
 template <int D, int kTiles>
 __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCtasPerSm) tree_kernel(const __grid_constant__ TreeArgs a) {
   using C = Cfg<D, kTiles>;
-  constexpr int kStreams = C::kStreams, kKeys = C::kKeys, kStages = C::kStages;
+  constexpr int kStreams = C::kStreams, kKeys = C::kKeys, kStages = C::kStages, kVSlots = (kStages + 1) / 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     if (C::kHelpers == 0) return lane;
     return member > 0 ? 3 * lane + 2 : lane / 2 * 3 + (lane & 1);
   };
-  // K (kv = 0) or V (1) of a segment's tiles into the even or odd ring slots; `n` counts the tiles over
+  // K (kv = 0) or V (1) of a segment's tiles into the ring; `n` counts the tiles over
   // all segments. A lane's copy of 16 rows takes its warp about 70 ns to issue, and a tile out of 16-row
   // pages is 8 to 16 such copies of K and as many of V, so a helper warp takes a third of both (one warp
   // for K and V held the paged d = 128 cache at 4400 GB/s where a contiguous one ran at 6270). The K and
@@ -452,17 +456,16 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     }
     return true;
   };
-  // the copies a producer warp issued last, of n tiles in all, have landed
+  // the copies a producer warp issued last, of n tiles in all, have landed: those whose slot no later tile took
   auto drain = [&](int kv, int n) {
-    for (int t = max(0, n - kStages / 2); t < n; ++t) {
-      const int i = 2 * t + kv;
-      mbar_wait(&bar->kv_full[i % kStages], (i / kStages) & 1, tmo, &no_abort);
+    for (int i = 2 * n - 1; i >= max(0, 2 * n - kStages); --i) {
+      if ((i & 1) == kv) mbar_wait(&bar->kv_full[i % kStages], (i / kStages) & 1, tmo, &no_abort);
     }
   };
 
   if (warp == C::kTmaWarp) {
     // ------------------------------------------------------------ segments, Q and K tiles
-    give_registers<C::kCtasPerSm == 2>();
+    Regs<D, kTiles>::give();
     if (lane == 0) {
       prefetch_tmap(&a.tm_q);
       prefetch_tmap(&a.tm_k);
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     drain(0, nload);
   } else if (warp >= C::kTmaVWarp) {
     // ------------------------------------------------------------ V tiles, or the helper's share of both
-    give_registers<C::kCtasPerSm == 2>();
+    Regs<D, kTiles>::give();
     const bool helper = warp > C::kTmaVWarp;
     int nload = 0;
     bool ok = true;
@@ -564,7 +567,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     if (helper) drain(0, nload);
   } else if (warp >= C::kMmaWarp) {
     // ------------------------------------------------------------ MMA issuers, one per stream
-    give_registers<C::kCtasPerSm == 2>();
+    Regs<D, kTiles>::give();
     const int w = warp - C::kMmaWarp;
     constexpr uint32_t idesc_qk = idesc_bf16_f32(kTreeRows, kKeys, 0, 0);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(kTreeRows, D, 0, 1);
@@ -610,11 +613,14 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       return true;
     };
     // P.V of load i over the first `valid` keys (whole K = 16 steps)
-    auto issue_pv = [&](int i, bool accumulate, int valid) {
+    auto issue_pv = [&](int i, bool accumulate, int valid, auto special) {
       const uint32_t tP = tbase + (C::kSplitP ? C::kColP + w * 64 : C::kColS + buf(np) * kKeys);
       const uint32_t vl = v_lo + (i % kStages) * slot_step;
-      if (kKeys == 128 && valid == 128) {
+      if constexpr (kKeys == 128 && !special) {
         umma_ts_k128(tO, tP, vl, hi, idesc_pv, accumulate ? 1u : 0u);
+      } else if constexpr (!special) {
+#pragma unroll
+        for (int s = 0; s < kKeys / 16; ++s) umma_ts(tO, tP + 8 * s, vl + 128 * s, hi, idesc_pv, (accumulate || s) ? 1u : 0u);
       } else {
 #pragma unroll 1
         for (int s = 0; 16 * s < valid; ++s) umma_ts(tO, tP + 8 * s, vl + 128 * s, hi, idesc_pv, (accumulate || s) ? 1u : 0u);
@@ -625,87 +631,91 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     for (int k = 0; ok; ++k) {
       Seg* sp = wait_seg(k);
       if (!(ok = sp != nullptr)) break;
-      const Seg s = *sp;
+      const Seg& s = *sp;
       if (!s.valid) {
         release_seg(k);
         break;
       }
       if (!(ok = vote(mbar_wait(&bar->q_full[qb], k & 1, tmo, abort)))) break;
       tc_fence_after();
-      const int base = nload;
-      nload += 2 * s.nt;
-      const bool idle = kTiles == 2 && tile_rows(s, w) == 0;  // no rows: only gives the slots back
-      const int special_from = s.nk % kKeys ? s.ct - 1 : s.ct;
+      const int nt = s.nt, base = nload;
+      nload += 2 * nt;
+      // the tiles from `plain` on: the context's last one, if it is not whole, and the drafts
+      const int plain = min(max((s.nk % kKeys ? s.ct - 1 : s.ct) - s.k0, 0), nt);
       const bool turns = kTiles == 2 && !C::kLook && tile_rows(s, 1) > 0;
-      if (idle) {
+      if (kTiles == 2 && tile_rows(s, w) == 0) {  // no rows: only gives the slots back
         umma_commit(&bar->q_empty[qb]);
-      } else {
-        if (!(ok = start_s(base))) break;
-        if (s.nt == 1) umma_commit(&bar->q_empty[qb]);
+        for (int i = base; ok && i < nload; ++i)
+          if ((ok = wait_load(i))) umma_commit(&bar->kv_empty[i % kStages]);
+        if (!ok) break;
+        nspecial += nt - plain;
+        release_seg(k);
+        continue;
       }
-      for (int j = 0; j < s.nt; ++j) {
-        const int ik = base + 2 * j, iv = ik + 1;
-        if (idle && !(ok = wait_load(ik))) break;
+      if (!(ok = start_s(base))) break;
+      if (nt == 1) umma_commit(&bar->q_empty[qb]);
+      // one tile; the special ones are apart, as the issuing warp's time per tile bounds two row tiles
+      auto tile = [&](int j, auto special) -> bool {
+        const int ik = base + 2 * j, iv = ik + 1, inext = ik + 2;
         umma_commit(&bar->kv_empty[ik % kStages]);  // S of this tile was issued before
-        if (idle) {
-          if (!(ok = wait_load(iv))) break;
-          umma_commit(&bar->kv_empty[iv % kStages]);
-          nspecial += s.k0 + j >= special_from;
-          continue;
-        }
-        const int inext = ik + 2;
-        const bool more = j + 1 < s.nt, last_s = j + 2 >= s.nt;
+        const bool more = j + 1 < nt, last_s = j + 2 >= nt;
         if (C::kLook && more) {
           // S of the next tile goes ahead of this tile's P.V
-          if (!(ok = start_s(inext))) break;
+          if (!start_s(inext)) return false;
           if (last_s) umma_commit(&bar->q_empty[qb]);
         }
-        if (!(ok = wait_load(iv))) break;
+        if (!wait_load(iv)) return false;
         int valid = kKeys;  // keys of the tile that count
-        if (s.k0 + j >= special_from) {
-          // the context's last tile, or drafts: P.V stops at the 16 keys that hold the last one; V rows from
-          // there to the 16's end are zeroed, and drafts' infinities and NaN (two row tiles read one V
-          // tile: stream 0 looks it over for both)
+        if constexpr (special) {
+          // P.V stops at the 16 keys that hold the last one that counts; V rows from there to the 16's end
+          // are zeroed, and drafts' infinities and NaN (two row tiles read one V tile: stream 0 looks it
+          // over for both)
           const int kt = s.k0 + j;
           const bool draft = kt >= s.ct;
-          uint64_t* ready = &bar->v_ready[nspecial % (kStages / 2)];
+          uint64_t* ready = &bar->v_ready[nspecial % kVSlots];
           valid = min(kKeys, draft ? s.nq - (kt - s.ct) * kKeys : s.nk - kt * kKeys);
           if (kTiles == 1 || w == 0) {
             if (clean_v<C::kHalves, kKeys>(sRing + (iv % kStages) * C::kTileBytes, valid, draft, lane) && lane == 0)
               atomicOr(&sp->bad, 1);
             __syncwarp();
             if (kTiles == 2 && lane == 0) mbar_arrive(ready);
-          } else if (!(ok = vote(mbar_wait(ready, (nspecial / (kStages / 2)) & 1, tmo, abort)))) {
-            break;
+          } else if (!vote(mbar_wait(ready, (nspecial / kVSlots) & 1, tmo, abort))) {
+            return false;
           }
           ++nspecial;
         }
         // two row tiles: P.V in turns (0, 1, 0, ...), which keeps the streams out of step, one's softmax
         // beside the other's MMAs
         if (turns) {
-          if (w == 1 ? !(ok = vote(mbar_wait(&bar->turn[0], nturn & 1, tmo, abort)))
-                     : nturn > 0 && !(ok = vote(mbar_wait(&bar->turn[1], (nturn - 1) & 1, tmo, abort))))
-            break;
+          if (w == 1 ? !vote(mbar_wait(&bar->turn[0], nturn & 1, tmo, abort))
+                     : nturn > 0 && !vote(mbar_wait(&bar->turn[1], (nturn - 1) & 1, tmo, abort)))
+            return false;
         }
-        if (j == 0 && ou > 0 && !(ok = vote(mbar_wait(&bar->o_empty[w], (ou - 1) & 1, tmo, abort)))) break;
-        if (!(ok = vote(mbar_wait(&bar->p_full[buf(np)], use(np) & 1, tmo, abort)))) break;
+        if (j == 0 && ou > 0 && !vote(mbar_wait(&bar->o_empty[w], (ou - 1) & 1, tmo, abort))) return false;
+        if (!vote(mbar_wait(&bar->p_full[buf(np)], use(np) & 1, tmo, abort))) return false;
         tc_fence_after();
-        issue_pv(iv, j > 0, valid);
-        if (turns) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar->turn[w]);
-          ++nturn;
-        }
+        issue_pv(iv, j > 0, valid, special);
         if (!more) {
           umma_commit(&bar->o_full[w]);
           ++ou;
         } else if (!C::kLook) {
           // S of the next tile overwrites P: it follows this P.V in the warp's stream
-          if (!(ok = start_s(inext))) break;
+          if (!start_s(inext)) return false;
           if (last_s) umma_commit(&bar->q_empty[qb]);
         }
+        if (turns) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->turn[w]);
+          ++nturn;
+        }
         umma_commit(&bar->kv_empty[iv % kStages]);
-      }
+        return true;
+      };
+      int j = 0;
+#pragma unroll 1
+      for (; ok && j < plain; ++j) ok = tile(j, std::false_type());
+#pragma unroll 1
+      for (; ok && j < nt; ++j) ok = tile(j, std::true_type());
       if (!ok) break;
       release_seg(k);
     }
@@ -715,7 +725,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     mbar_wait(&bar->mma_done[w], 0, tmo, &no_abort);
   } else {
     // ------------------------------------------------------------ softmax warpgroups
-    take_registers<C::kCtasPerSm == 2>();
+    Regs<D, kTiles>::take();
     const int w = warp >> 2;
     const int row = (warp & 3) * 32 + lane - first_lane;  // of the tile: the TMEM lane less that of the first row
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -742,20 +752,21 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       const int node = s.node0 + rw * tile_nodes + some_row / a.g;  // within the sequence
       const int head = s.hkv * a.g + some_row % a.g;
       const uint64_t* bits = a.mask + static_cast<int64_t>(s.tok0 + node) * a.mask_words;
-      const int masked_from = s.nk % kKeys ? s.ct - 1 : s.ct;  // first tile with keys that some row does not see
+      // the tiles from `plain` on have keys that some row does not see
+      const int plain = min(max((s.nk % kKeys ? s.ct - 1 : s.ct) - s.k0, 0), s.nt);
       float m_ref = -INFINITY, l = 0.f;
-      for (int j = 0; j < s.nt; ++j) {
+      auto tile = [&](int j, auto masked) -> bool {
         const int x = C::kTwoS ? n & 1 : w, phase = (C::kTwoS ? n >> 1 : n) & 1;
         const uint32_t tS = tbase + lane_base + C::kColS + x * kKeys;
         const uint32_t tP = C::kSplitP ? tbase + lane_base + C::kColP + w * 64 : tS;
-        if (!(ok = vote(mbar_wait(&bar->s_full[x], phase, tmo, abort)))) break;
+        if (!vote(mbar_wait(&bar->s_full[x], phase, tmo, abort))) return false;
         tc_fence_after();
         if (warp_ok) {
-          const int kt = s.k0 + j;
           float alpha_o = 1.f;
-          if (kt >= masked_from) {
+          if constexpr (masked) {
+            const int kt = s.k0 + j;
             if (C::kSplitP && n > 0) {
-              if (!(ok = vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort)))) break;
+              if (!vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort))) return false;
               tc_fence_after();
             }
             const bool draft = kt >= s.ct;
@@ -800,7 +811,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             const float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
             if (C::kSplitP && n > 0) {
               // the stream's previous P.V has read the P columns, and O holds it
-              if (!(ok = vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort)))) break;
+              if (!vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort))) return false;
               tc_fence_after();
             }
             // p = 2^(s scale log2e - m) as bf16 pairs into the first half of the S columns; l is the fp32
@@ -825,8 +836,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
           if (__any_sync(0xffffffffu, alpha_o != 1.f)) {
             if (C::kTwoS) {
               // S(j) was issued ahead of P.V(j - 1): that one has to be done
-              ok = vote(mbar_wait(&bar->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, tmo, abort));
-              if (!ok) break;
+              if (!vote(mbar_wait(&bar->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, tmo, abort))) return false;
               tc_fence_after();
             }
 #pragma unroll 1
@@ -847,12 +857,18 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
           if constexpr (C::kSplitP) {
             // a warp without rows may not run ahead either: its arrivals for the next P would count for this
             mbar_arrive(&bar->s_free[x]);
-            if (n > 0 && !(ok = vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort)))) break;
+            if (n > 0 && !vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort))) return false;
           }
           mbar_arrive(&bar->p_full[x]);
         }
         ++n;
-      }
+        return true;
+      };
+      int j = 0;
+#pragma unroll 1
+      for (; ok && j < plain; ++j) ok = tile(j, std::false_type());
+#pragma unroll 1
+      for (; ok && j < s.nt; ++j) ok = tile(j, std::true_type());
       if (!ok) break;
       // ---- the unit's end in this CTA
       if (!(ok = vote(mbar_wait(&bar->o_full[w], oused & 1, tmo, abort)))) break;
