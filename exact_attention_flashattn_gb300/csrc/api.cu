@@ -118,8 +118,7 @@ cudaError_t encoder(EncodeTiledFn* out) {
 // 3-D bf16 map {d, dim1, dim2} with row strides in elements, box {64, box1, box2},
 // 128-byte swizzle, zero fill out of bounds.
 cudaError_t make_map(CUtensorMap* m, const void* base, int d, int64_t dim1, int64_t dim2, int64_t stride1_elems,
-                     int64_t stride2_elems, int box1, int box2,
-                     CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
+                     int64_t stride2_elems, int box1, int box2) {
   EncodeTiledFn enc = nullptr;
   cudaError_t e = encoder(&enc);
   if (e != cudaSuccess) return e;
@@ -130,7 +129,7 @@ cudaError_t make_map(CUtensorMap* m, const void* base, int d, int64_t dim1, int6
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2)};
   const cuuint32_t es[3] = {1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -195,9 +194,8 @@ namespace bw {
 void record_cuda_error(cudaError_t e) { t_last_cuda_error = static_cast<int>(e); }
 void count_launch() { g_launches.fetch_add(1); }
 cudaError_t make_map_bf16(CUtensorMap* m, const void* base, int d, int64_t dim1, int64_t dim2, int64_t stride1_elems,
-                          int64_t stride2_elems, int box1, int box2, bool narrow) {
-  return make_map(m, base, d, dim1, dim2, stride1_elems, stride2_elems, box1, box2,
-                  narrow ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+                          int64_t stride2_elems, int box1, int box2) {
+  return make_map(m, base, d, dim1, dim2, stride1_elems, stride2_elems, box1, box2);
 }
 cudaError_t status_word(unsigned int** out) { return status_ptr(out); }
 uint64_t wait_timeout_ns() { return g_timeout_ns.load(); }

@@ -179,7 +179,8 @@ struct TreeArgs {
   int tile_rows;          // tree_tile_rows(max_nodes, g, d)
   int piece;              // paged: rows of a copy, a power of two that divides page_size
   int new_box;            // rows of a copy of drafted rows
-  int ctas;               // CTAs of the attention kernel
+  int head_group, head_groups;  // KV heads that a group of CTAs takes side by side; Hkv / head_group
+  int groups;             // groups of CTAs of the attention kernel
   float scale_log2;
   unsigned int* status;
   uint64_t timeout_ns;
@@ -197,7 +198,8 @@ inline size_t tree_ws_bytes(int max_nodes, int g, int d) {
   return kTreeMergeBytes +
          static_cast<size_t>(tree_max_ctas(tiles, d)) * 2 * tiles * kTreeRows * (d + 2) * sizeof(float);
 }
-// The most places (tree_unit_cost and the key tiles of every unit) that the lengths of a call may make (int in the kernel: the host refuses more).
+// The most places (tree_unit_cost and the key tiles of every unit) that the lengths of a call may make (int in
+// the kernel: the host refuses more).
 inline int64_t tree_most_tiles(const TreeArgs& a) {
   const int keys = a.d == 256 ? 64 : 128, unit_nodes = tree_row_tiles(a.max_nodes, a.g, a.d) * (tree_tile_rows(a.max_nodes, a.g, a.d) / a.g);
   const int64_t seqs = a.num_seqs < a.total_q ? a.num_seqs : a.total_q;
@@ -261,9 +263,9 @@ void count_launch();
 // when the request exceeds the ticket pool: the caller then launches the merge kernel).
 cudaError_t merge_tickets(int n, unsigned int** out);
 // 3-D bf16 tensor map {d, dim1, dim2} with strides in elements, box {64, box1, box2}, 128-byte
-// swizzle, zero fill out of bounds. `narrow`: L2 fetches of 128 bytes instead of 256.
+// swizzle, zero fill out of bounds.
 cudaError_t make_map_bf16(CUtensorMap* m, const void* base, int d, int64_t dim1, int64_t dim2, int64_t stride1_elems,
-                          int64_t stride2_elems, int box1, int box2, bool narrow = false);
+                          int64_t stride2_elems, int box1, int box2);
 // The device status word of the current device and the bound on a kernel's waits.
 cudaError_t status_word(unsigned int** out);
 uint64_t wait_timeout_ns();

@@ -15,7 +15,8 @@
 // Split: lengths are on the device, and one long sequence has to fill the GPU as well as many short
 // ones. The key tiles of all units form one list (unit after unit: tree_unit_cost places for what a unit
 // costs beside its tiles, its context tiles, then its drafts), and CTA c of G takes places
-// [c T / G, (c + 1) T / G), whatever the lengths. A unit that lies within one CTA's range is finished there; otherwise each
+// [c T / G, (c + 1) T / G), whatever the lengths (with pages, a group of CTAs, each for another KV head: the
+// list is then of the units of head groups). A unit that lies within one CTA's range is finished there; otherwise each
 // CTA that has a part of it writes its (m, l, o), at most two such parts per CTA, and a second,
 // dependent launch merges them in the order of the keys (no atomics: results do not depend on which
 // CTA ends first).
@@ -129,7 +130,7 @@ struct SeqTiles {
   int ct, per_unit;  // context tiles, all tiles of a unit
   int row_units;     // units of a KV head
   // places of the list; the host bounds their sum
-  __device__ __forceinline__ int all(int Hkv) const { return (per_unit + tree_unit_cost(D)) * row_units * Hkv; }
+  __device__ __forceinline__ int all(int head_groups) const { return (per_unit + tree_unit_cost(D)) * row_units * head_groups; }
 };
 template <int D, int kTiles>
 __device__ __forceinline__ SeqTiles<D> seq_tiles(const TreeArgs& a, int b) {
@@ -298,6 +299,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   uint8_t* sQ = smem;
   uint8_t* sRing = smem + C::kRing;
   Barriers* bar = reinterpret_cast<Barriers*>(smem + C::kBar);
+  const int group = static_cast<int>(blockIdx.x) / a.head_group;  // of CTAs with the same places
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   asm volatile("griddepcontrol.launch_dependents;");  // the merge waits for this grid to complete
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   int mine = 0, incl = 0;
   if (wide || warp == C::kTmaWarp) {
 #pragma unroll 4
-    for (int b = run0; b < run1; ++b) mine += seq_tiles<D, kTiles>(a, b).all(a.Hkv);
+    for (int b = run0; b < run1; ++b) mine += seq_tiles<D, kTiles>(a, b).all(a.head_groups);
     incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -360,11 +362,11 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         T += bar->scan[w];
       }
     }
-    const Share share(T, a.ctas);
-    const int begin = share.begin(blockIdx.x);
-    if (static_cast<int>(blockIdx.x) < share.G && before <= begin && begin < before + mine) {
+    const Share share(T, a.groups);
+    const int begin = share.begin(group);
+    if (group < share.G && before <= begin && begin < before + mine) {
       int b = run0;
-      for (int n; begin >= before + (n = seq_tiles<D, kTiles>(a, b).all(a.Hkv)); ++b) before += n;
+      for (int n; begin >= before + (n = seq_tiles<D, kTiles>(a, b).all(a.head_groups)); ++b) before += n;
       bar->list[1] = b;
       bar->list[2] = before;
     }
@@ -473,8 +475,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       prefetch_tmap(&a.tm_kn);
       prefetch_tmap(&a.tm_vn);
     }
-    const Share share(bar->list[0], a.ctas);
-    const int c = blockIdx.x, begin = c < share.G ? share.begin(c) : 0, end = c < share.G && bar->list[0] > 0 ? share.begin(c + 1) : 0;
+    const Share share(bar->list[0], a.groups);
+    const int c = group, head0 = static_cast<int>(blockIdx.x) - group * a.head_group;
+    const int begin = c < share.G ? share.begin(c) : 0, end = c < share.G && bar->list[0] > 0 ? share.begin(c + 1) : 0;
     int pos = begin, b = pos < end ? bar->list[1] : 0, seq_at = pos < end ? bar->list[2] : 0;
     int nload = 0, nq[2] = {0, 0};  // K tiles, and Q tiles into each buffer
     bool ok = true;
@@ -482,8 +485,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       Seg s{};
       while (pos < end && !s.valid) {
         SeqTiles<D> q = seq_tiles<D, kTiles>(a, b);
-        while (pos >= seq_at + q.all(a.Hkv)) {
-          seq_at += q.all(a.Hkv);
+        while (pos >= seq_at + q.all(a.head_groups)) {
+          seq_at += q.all(a.head_groups);
           q = seq_tiles<D, kTiles>(a, ++b);
         }
         const int size = q.per_unit + tree_unit_cost(D), local = pos - seq_at, unit = local / size;
@@ -498,8 +501,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         s.tok0 = q.tok0;
         s.nq = q.nq;
         s.nk = q.nk;
-        s.hkv = unit / q.row_units;
-        s.node0 = (unit - s.hkv * q.row_units) * (kTiles * tile_nodes);
+        const int heads = unit / q.row_units;
+        s.hkv = heads * a.head_group + head0;
+        s.node0 = (unit - heads * q.row_units) * (kTiles * tile_nodes);
         s.ct = q.ct;
         s.slot = s.nt == q.per_unit ? -1 : (k == 0 ? 0 : 1);
         if (k == 0 && lane == 0) {
@@ -511,12 +515,12 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             r.node_step = tile_nodes;
             r.hkv = s.hkv;
             r.slot0 = u0 <= share.begin(c - 1) ? 0 : 1;
-            r.last = share.owner(u0 + size - 1);
+            r.last = share.owner(u0 + size - 1) * a.head_group + head0;
           }
-          a.merge[c] = r;
+          a.merge[blockIdx.x] = r;
         }
       }
-      if (k == 0 && !s.valid && lane == 0) a.merge[c] = TreeMergeRec{};  // no part here
+      if (k == 0 && !s.valid && lane == 0) a.merge[blockIdx.x] = TreeMergeRec{};  // no part here
       if (k >= kSegSlots && !(ok = vote(mbar_wait(&bar->seg_empty[k % kSegSlots], (k / kSegSlots - 1) & 1, tmo, abort))))
         break;
       if (lane == 0) {
@@ -942,12 +946,12 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
 //   m = max m_c, l = sum l_c 2^(m_c - m), o likewise.
 constexpr int kMergeWarps = 8;
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const float* partial, const TreeMergeRec* merge, uint16_t* out,
-                                                                       float* lse, int D, int tiles, int g, int Hq) {
+                                                                       float* lse, int D, int tiles, int g, int Hq, int head_group) {
   __shared__ float4 sm_o[kMergeWarps][8][33];  // 33: the joining threads' columns fall on different banks
   __shared__ float2 sm_ml[kMergeWarps][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts and records are complete and visible
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x + 1, w = blockIdx.y >> 2, quarter = blockIdx.y & 3, cg = blockIdx.z;
+  const int c = blockIdx.x + head_group, w = blockIdx.y >> 2, quarter = blockIdx.y & 3, cg = blockIdx.z;
   const int4 r0 = __ldcg(reinterpret_cast<const int4*>(merge + c)), r1 = __ldcg(reinterpret_cast<const int4*>(merge + c) + 1);
   const int rows = w ? r0.y : r0.x, hkv = r1.x, slot0 = r1.y, last = r1.z;
   if (32 * quarter >= rows) return;
@@ -958,8 +962,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const floa
 #pragma unroll
   for (int q = 0; q < 8; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (row < rows) {
-    for (int x = c - 1 + warp; x <= last; x += kMergeWarps) {
-      const float* p = partial + ((static_cast<int64_t>(x) * 2 + (x == c - 1 ? slot0 : 0)) * tiles + w) * size;
+    for (int x = c + (warp - 1) * head_group; x <= last; x += kMergeWarps * head_group) {
+      const float* p = partial + ((static_cast<int64_t>(x) * 2 + (x < c ? slot0 : 0)) * tiles + w) * size;
       const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + kTreeRows * D + 2 * row));
       float4 v[8];
 #pragma unroll
@@ -984,7 +988,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const floa
   // thread = (row, channel quad): 8 threads write a row's 64 bytes
   const int jr = threadIdx.x >> 3, jq = threadIdx.x & 7;
   if (32 * quarter + jr >= rows) return;
-  const int used = min(kMergeWarps, last - c + 2);
+  const int used = min(kMergeWarps, (last - c) / head_group + 2);
   float M = -INFINITY, L = 0.f;
   for (int x = 0; x < used; ++x) M = fmaxf(M, sm_ml[x][jr].x);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1017,12 +1021,12 @@ cudaError_t launch(const TreeArgs& a, int dev, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev < 64) set.fetch_or(1ull << dev);
   }
-  tree_kernel<D, kTiles><<<a.ctas, C::kThreads, C::kSmem, stream>>>(a);
+  tree_kernel<D, kTiles><<<a.groups * a.head_group, C::kThreads, C::kSmem, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   count_launch();
-  if (a.ctas == 1) return cudaSuccess;
+  if (a.groups == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.ctas - 1, 4 * kTiles, D / 32);
+  cfg.gridDim = dim3((a.groups - 1) * a.head_group, 4 * kTiles, D / 32);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1031,7 +1035,7 @@ cudaError_t launch(const TreeArgs& a, int dev, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, static_cast<const float*>(a.partial), static_cast<const TreeMergeRec*>(a.merge), a.o,
-                         a.lse, D, kTiles, a.g, a.Hq);
+                         a.lse, D, kTiles, a.g, a.Hq, a.head_group);
   if (e == cudaSuccess) count_launch();
   return e;
 }
@@ -1058,10 +1062,8 @@ cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
     a.piece = 16;
     while (a.piece < keys && a.page_size % (2 * a.piece) == 0) a.piece *= 2;
     const int64_t rows = static_cast<int64_t>(a.num_pages) * a.page_size, step = static_cast<int64_t>(a.Hkv) * d;
-    // a head's row is 128 bytes at d = 64: wider fetches would bring the next head's along
-    const bool narrow = d == 64;
-    if ((e = make_map_bf16(&a.tm_k, a.k, d, a.Hkv, rows, d, step, 1, a.piece, narrow)) != cudaSuccess ||
-        (e = make_map_bf16(&a.tm_v, a.v, d, a.Hkv, rows, d, step, 1, a.piece, narrow)) != cudaSuccess)
+    if ((e = make_map_bf16(&a.tm_k, a.k, d, a.Hkv, rows, d, step, 1, a.piece)) != cudaSuccess ||
+        (e = make_map_bf16(&a.tm_v, a.v, d, a.Hkv, rows, d, step, 1, a.piece)) != cudaSuccess)
       return e;
   } else {
     const int64_t heads = static_cast<int64_t>(a.num_seqs) * a.Hkv, step = static_cast<int64_t>(a.kv_cap) * d;
@@ -1075,8 +1077,16 @@ cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
   const int tiles = tree_row_tiles(a.max_nodes, a.g, d);
   const int64_t most = tree_most_tiles(a);  // no more CTAs than tiles there can be
   const int fit = tiles == 1 && d <= 128 ? 2 * sms : sms;
-  a.ctas = tree_max_ctas(tiles, d) < fit ? tree_max_ctas(tiles, d) : fit;
-  if (a.ctas > most) a.ctas = static_cast<int>(most);
+  const int ctas = tree_max_ctas(tiles, d) < fit ? tree_max_ctas(tiles, d) : fit;
+  // a page holds the rows of all KV heads side by side: CTAs that read the same keys of different heads at
+  // the same time share the pages of HBM that these lie in
+  a.head_group = 1;
+  if (a.block_table)
+    for (int n = 2; n <= 8 && n <= ctas; ++n)
+      if (a.Hkv % n == 0) a.head_group = n;
+  a.head_groups = a.Hkv / a.head_group;
+  a.groups = ctas / a.head_group;
+  if (a.groups > most / a.head_group) a.groups = static_cast<int>(most / a.head_group);
   if (d == 64) return tiles == 2 ? launch<64, 2>(a, dev, stream) : launch<64, 1>(a, dev, stream);
   if (d == 128) return tiles == 2 ? launch<128, 2>(a, dev, stream) : launch<128, 1>(a, dev, stream);
   return launch<256, 1>(a, dev, stream);
