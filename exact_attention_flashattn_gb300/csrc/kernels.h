@@ -181,6 +181,7 @@ struct TreeArgs {
   int new_box;            // rows of a copy of drafted rows
   int head_group, head_groups;  // KV heads that a group of CTAs takes side by side; Hkv / head_group
   int groups;             // groups of CTAs of the attention kernel
+  int merges;             // units that may have to be merged
   float scale_log2;
   unsigned int* status;
   uint64_t timeout_ns;
@@ -198,12 +199,16 @@ inline size_t tree_ws_bytes(int max_nodes, int g, int d) {
   return kTreeMergeBytes +
          static_cast<size_t>(tree_max_ctas(tiles, d)) * 2 * tiles * kTreeRows * (d + 2) * sizeof(float);
 }
-// The most places (tree_unit_cost and the key tiles of every unit) that the lengths of a call may make (int in
-// the kernel: the host refuses more).
-inline int64_t tree_most_tiles(const TreeArgs& a) {
-  const int keys = a.d == 256 ? 64 : 128, unit_nodes = tree_row_tiles(a.max_nodes, a.g, a.d) * (tree_tile_rows(a.max_nodes, a.g, a.d) / a.g);
+// The most units, and places (tree_unit_cost and the key tiles of every unit), that the lengths of a call may
+// make (places are int in the kernel: the host refuses more).
+inline int64_t tree_most_units(const TreeArgs& a) {
+  const int unit_nodes = tree_row_tiles(a.max_nodes, a.g, a.d) * (tree_tile_rows(a.max_nodes, a.g, a.d) / a.g);
   const int64_t seqs = a.num_seqs < a.total_q ? a.num_seqs : a.total_q;
-  return a.Hkv * (seqs + a.total_q / unit_nodes) *
+  return a.Hkv * (seqs + a.total_q / unit_nodes);
+}
+inline int64_t tree_most_tiles(const TreeArgs& a) {
+  const int keys = a.d == 256 ? 64 : 128;
+  return tree_most_units(a) *
          ((static_cast<int64_t>(a.kv_cap) + keys - 1) / keys + (a.max_nodes + keys - 1) / keys + tree_unit_cost(a.d));
 }
 // Fills the maps and sizes that follow from the others, launches the attention and the merge.

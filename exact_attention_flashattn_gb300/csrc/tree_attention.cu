@@ -941,17 +941,53 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
 
 // The parts of units that several CTAs shared. At most one unit per boundary between two CTAs has to
 // be merged, so the grid is (boundaries, quarters of a row tile x row tiles, groups of 32 channels),
-// whatever the lengths. Lanes are rows; the warps share out the parts, each with its own running
+// whatever the lengths; or, where the call has far fewer units than that, (units, ...), each block counting
+// its way to its record (2 x 8 units of 8192 keys on 304 CTAs: 23.0 us in all, with a block for every
+// boundary, most of them empty, 24.7; one warp a block reads the records, as all eight made their few lines
+// of L2 a bottleneck and took 4 us). Lanes are rows; the warps share out the parts, each with its own running
 // maximum, and are joined in shared memory in their order:
 //   m = max m_c, l = sum l_c 2^(m_c - m), o likewise.
 constexpr int kMergeWarps = 8;
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const float* partial, const TreeMergeRec* merge, uint16_t* out,
-                                                                       float* lse, int D, int tiles, int g, int Hq, int head_group) {
+                                                                       float* lse, int D, int tiles, int g, int Hq, int head_group, int ctas) {
   __shared__ float4 sm_o[kMergeWarps][8][33];  // 33: the joining threads' columns fall on different banks
   __shared__ float2 sm_ml[kMergeWarps][32];
+  __shared__ int sm_c;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts and records are complete and visible
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x + head_group, w = blockIdx.y >> 2, quarter = blockIdx.y & 3, cg = blockIdx.z;
+  int c = blockIdx.x + head_group;
+  if (head_group + static_cast<int>(gridDim.x) < ctas) {
+    if (warp == 0) {
+      // the blockIdx.x-th record with rows: lane i holds those of records 32 i .. 32 i + 31 as bits
+      constexpr int kWords = (kTreeMaxCtas + 31) / 32;
+      int rows[kWords];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+        rows[i] = head_group + 32 * i + lane < ctas ? __ldcg(&merge[head_group + 32 * i + lane].rows0) : 0;
+      unsigned some = 0;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const unsigned bits = __ballot_sync(0xffffffffu, rows[i] > 0);
+        if (lane == i) some = bits;
+      }
+      int upto = __popc(some);
+#pragma unroll
+      for (int off = 1; off < kWords; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += x;
+      }
+      int left = blockIdx.x - (upto - __popc(some));  // of this lane's bits
+      if (left >= 0 && left < __popc(some)) {
+        for (; left > 0; --left) some &= some - 1;
+        sm_c = head_group + 32 * lane + __ffs(some) - 1;
+      }
+      if (lane == kWords - 1 && upto <= static_cast<int>(blockIdx.x)) sm_c = 0;  // no such record
+    }
+    __syncthreads();
+    c = sm_c;
+    if (c == 0) return;
+  }
+  const int w = blockIdx.y >> 2, quarter = blockIdx.y & 3, cg = blockIdx.z;
   const int4 r0 = __ldcg(reinterpret_cast<const int4*>(merge + c)), r1 = __ldcg(reinterpret_cast<const int4*>(merge + c) + 1);
   const int rows = w ? r0.y : r0.x, hkv = r1.x, slot0 = r1.y, last = r1.z;
   if (32 * quarter >= rows) return;
@@ -1026,7 +1062,7 @@ cudaError_t launch(const TreeArgs& a, int dev, cudaStream_t stream) {
   count_launch();
   if (a.groups == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.groups - 1) * a.head_group, 4 * kTiles, D / 32);
+  cfg.gridDim = dim3(a.merges, 4 * kTiles, D / 32);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1035,7 +1071,7 @@ cudaError_t launch(const TreeArgs& a, int dev, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, static_cast<const float*>(a.partial), static_cast<const TreeMergeRec*>(a.merge), a.o,
-                         a.lse, D, kTiles, a.g, a.Hq, a.head_group);
+                         a.lse, D, kTiles, a.g, a.Hq, a.head_group, a.groups * a.head_group);
   if (e == cudaSuccess) count_launch();
   return e;
 }
@@ -1079,7 +1115,8 @@ cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
   const int fit = tiles == 1 && d <= 128 ? 2 * sms : sms;
   const int ctas = tree_max_ctas(tiles, d) < fit ? tree_max_ctas(tiles, d) : fit;
   // a page holds the rows of all KV heads side by side: CTAs that read the same keys of different heads at
-  // the same time share the pages of HBM that these lie in
+  // the same time share the pages of HBM that these lie in (16 x 32768 keys, d = 64, 16-token pages: 179 us,
+  // each head on its own 202)
   a.head_group = 1;
   if (a.block_table)
     for (int n = 2; n <= 8 && n <= ctas; ++n)
@@ -1087,6 +1124,11 @@ cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
   a.head_groups = a.Hkv / a.head_group;
   a.groups = ctas / a.head_group;
   if (a.groups > most / a.head_group) a.groups = static_cast<int>(most / a.head_group);
+  const int64_t boundaries = static_cast<int64_t>(a.groups - 1) * a.head_group, units = tree_most_units(a);
+  // up to two waves of blocks (six an SM) the empty ones cost less than finding the records (10 parts of 8
+  // heads, 1280 blocks: 12.3 against 12.9 us; 273 parts of them, 4400 blocks: 18.2 against 17.4)
+  const bool few = boundaries * 4 * tiles * (d / 32) <= 12 * sms;
+  a.merges = static_cast<int>(few || units > boundaries ? boundaries : units);
   if (d == 64) return tiles == 2 ? launch<64, 2>(a, dev, stream) : launch<64, 1>(a, dev, stream);
   if (d == 128) return tiles == 2 ? launch<128, 2>(a, dev, stream) : launch<128, 1>(a, dev, stream);
   return launch<256, 1>(a, dev, stream);

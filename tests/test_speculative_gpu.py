@@ -579,6 +579,40 @@ def test_append_fp8_every_value():
             assert bool(((got[nan] & 127) == 127).all())
 
 
+def test_append_fp8_extreme_scales():
+    # the ends of the normal range, where a reciprocal or a remainder runs out of exponents, and powers of
+    # two, whose quotients fall on the borders themselves; any two channels of a thread differ
+    bits = np.arange(1 << 16, dtype=np.uint16)
+    x = torch.from_numpy(bits.view(np.int16)).cuda().view(torch.bfloat16).view(256, 1, 256)
+    slots = torch.arange(256, dtype=torch.int32, device="cuda")
+    kp = torch.zeros((16, 16, 1, 256), dtype=torch.uint8, device="cuda")
+    vp = torch.zeros_like(kp)
+    tops = [1.0, 1.9999999, 1.3333334, 1.0000001, 1.5, 1.0625]
+    exps = [-126, -125, -100, -66, -65, -64, -63, -9, 0, 9, 64, 100, 124, 125, 126, 127]
+    s = [np.float32(m) * np.float32(2.0) ** np.float32(e) for e in exps for m in tops]
+    s = torch.tensor(np.array(s, np.float32), device="cuda")
+    assert bool(torch.isfinite(s).all()) and bool((s >= torch.finfo(torch.float32).tiny).all())
+    g = gen(6)
+    for _ in range(4):
+        ks, vs = (s[torch.randint(0, s.numel(), (1, 256), generator=g, device="cuda")] for _ in range(2))
+        bw.kv_append_paged_fp8(x, x, slots, kp, vp, ks, vs)
+        for p, sc in ((kp, ks), (vp, vs)):
+            got, want = p.view(256, 1, 256), codes_of(x, sc)
+            nan = torch.isnan(x)
+            assert torch.equal(got[~nan], want[~nan]), int((got != want).sum())
+            assert bool(((got[nan] & 127) == 127).all())
+
+
+def test_merge_many_units_and_few():
+    # parts of a few units among many CTAs (their records are searched for) and a part at every boundary
+    for i, (Hq, Hkv, d, page, nks, nqs) in enumerate([
+            (8, 2, 128, 0, [9000, 3], [3, 1]), (12, 3, 64, 48, [9001], [5]), (6, 6, 256, 16, [7000, 1, 0, 5000], [9, 2, 1, 4]),
+            (10, 5, 128, 16, [3000] * 7 + [0, 4111], [30] * 9), (7, 7, 64, 0, [1500 + 97 * x for x in range(40)], [2] * 40),
+            (11, 11, 64, 16, [700] * 60, [33] * 60), (24, 8, 128, 32, [6000] * 3, [64, 1, 50])]):
+        t = Case(Hq, Hkv, d, page, nks, nqs, seed=40 + i)
+        t.check(*t.run(), what=(Hq, Hkv, d, page))
+
+
 # ------------------------------------------------------------------ together
 
 
