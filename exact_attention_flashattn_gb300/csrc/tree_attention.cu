@@ -401,60 +401,76 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     if (C::kHelpers == 0) return lane;
     return member > 0 ? 3 * lane + 2 : lane / 2 * 3 + (lane & 1);
   };
-  // K (kv = 0) or V (1) of a segment's tiles into the ring; `n` counts the tiles over
-  // all segments. A lane's copy of 16 rows takes its warp about 70 ns to issue, and a tile out of 16-row
-  // pages is 8 to 16 such copies of K and as many of V, so a helper warp takes a third of both (one warp
-  // for K and V held the paged d = 128 cache at 4400 GB/s where a contiguous one ran at 6270). The K and
-  // V producers (member 0) announce a tile's bytes; the helper's copies (member 1) may land before that,
-  // but the phase waits for the announcement.
-  auto load_tile = [&](const Seg& s, int kv, int member, int kt, int n, int row) -> bool {
-    const CUtensorMap* old_map = kv ? &a.tm_v : &a.tm_k;
-    const int i = 2 * n + kv, slot = i % kStages, round = i / kStages;
-    if (round > 0 && !vote(mbar_wait(&bar->kv_empty[slot], (round - 1) & 1, tmo, abort))) return false;
-    uint8_t* dst = sRing + slot * C::kTileBytes;
-    const int copy = share_copy(member), hfl = copy % C::kHalves, my_piece = (copy / C::kHalves) * a.piece;
-    if (member > 0) {
-      if (row >= 0)
-        tma_load_3d_lane(dst + hfl * (kKeys * 128) + my_piece * 128, old_map, &bar->kv_full[slot], 64 * hfl, s.hkv, row);
-      __syncwarp();
-    } else if (kt >= s.ct) {
-      const CUtensorMap* new_map = kv ? &a.tm_vn : &a.tm_kn;
-      mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(a.new_box) * 128 * C::kHalves);
-      for (int hf = 0; hf < C::kHalves; ++hf)
-        tma_load_3d(dst + hf * (kKeys * 128), new_map, &bar->kv_full[slot], 64 * hf, s.hkv, s.tok0 + (kt - s.ct) * kKeys);
-    } else if (a.block_table) {
-      // pieces past the last key are not copied: their K scores are masked, their V rows zeroed
-      const int pieces = min(kKeys / a.piece, (s.nk - kt * kKeys + a.piece - 1) / a.piece);
-      mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(pieces * a.piece) * 128 * C::kHalves);
-      __syncwarp();
-      if (row >= 0)
-        tma_load_3d_lane(dst + hfl * (kKeys * 128) + my_piece * 128, old_map, &bar->kv_full[slot], 64 * hfl, s.hkv, row);
-      __syncwarp();
-    } else {
-      mbar_arrive_expect_tx(&bar->kv_full[slot], C::kTileBytes);
-      for (int hf = 0; hf < C::kHalves; ++hf)
-        tma_load_3d(dst + hf * (kKeys * 128), old_map, &bar->kv_full[slot], 64 * hf, kt * kKeys, s.b * a.Hkv + s.hkv);
-    }
-    return true;
+  auto wait_slot = [&](int i) -> bool {  // for load i
+    return i < kStages || vote(mbar_wait(&bar->kv_empty[i % kStages], (i / kStages - 1) & 1, tmo, abort));
   };
-  // all tiles of a segment: kv0 .. kv1 - 1 of K and V, `before_tile` ahead of each tile
+  // K (kv = 0) and V (1) of a segment's tiles, kv0 .. kv1 - 1 of them, into the ring, `before_tile` ahead of
+  // each tile; `n` counts the tiles over all segments. A lane's copy of 16 rows takes its warp about 70 ns
+  // to issue, and a tile out of 16-row pages is 8 to 16 such copies of K and as many of V, so a helper warp
+  // takes a third of both (one warp for K and V held the paged d = 128 cache at 4400 GB/s where a contiguous
+  // one ran at 6270). The K and V producers (member 0) announce a tile's bytes; the helper's copies (member
+  // 1) may land before that, but the phase waits for the announcement.
   auto load_tiles = [&](const Seg& s, int kv0, int kv1, int member, int& n, auto before_tile) -> bool {
-    // paged: the pool row of this lane's piece in the next tile is looked up one tile ahead
-    const int my_piece = (share_copy(member) / C::kHalves) * a.piece;
-    auto pool_row = [&](int kt) -> int {
-      const int key = kt * kKeys + my_piece;
-      if (!a.block_table || my_piece >= kKeys || kt >= s.ct || key >= s.nk) return -1;
-      int page = a.block_table[static_cast<int64_t>(s.b) * a.max_pages + key / a.page_size];
-      page = min(max(page, 0), a.num_pages - 1);  // a bad entry reads a wrong page, never outside the pool
-      return page * a.page_size + key % a.page_size;
-    };
-    int row_next = pool_row(s.k0);
-    for (int j = 0; j < s.nt; ++j, ++n) {
+    const int nctx = min(max(s.ct - s.k0, 0), s.nt);
+    int j = 0;
+    if (a.block_table) {
+      const int copy = share_copy(member), hfl = copy % C::kHalves, my_piece = (copy / C::kHalves) * a.piece;
+      const int* table = a.block_table + static_cast<int64_t>(s.b) * a.max_pages;
+      const int first = s.k0 * kKeys + my_piece, pages_on = kKeys / a.page_size, rows_on = kKeys % a.page_size;
+      int page = first / a.page_size, at = first - page * a.page_size;
+      // the pool row of this lane's piece in the next tile, looked up one tile ahead
+      auto pool_row = [&](int kt) -> int {
+        if (my_piece >= kKeys || kt >= s.ct || kt * kKeys + my_piece >= s.nk) return -1;
+        // a bad entry reads a wrong page, never outside the pool
+        return min(max(table[page], 0), a.num_pages - 1) * a.page_size + at;
+      };
+      int row_next = pool_row(s.k0);
+#pragma unroll 1
+      for (; j < nctx; ++j, ++n) {
+        if (!before_tile(j)) return false;
+        const int kt = s.k0 + j, row = row_next;
+        page += pages_on;
+        if ((at += rows_on) >= a.page_size) at -= a.page_size, ++page;
+        row_next = pool_row(kt + 1);
+        for (int kv = kv0; kv < kv1; ++kv) {
+          const int i = 2 * n + kv, slot = i % kStages;
+          if (!wait_slot(i)) return false;
+          if (member == 0) {
+            // pieces past the last key are not copied: their K scores are masked, their V rows zeroed
+            const int pieces = min(kKeys / a.piece, (s.nk - kt * kKeys + a.piece - 1) / a.piece);
+            mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(pieces * a.piece) * 128 * C::kHalves);
+            __syncwarp();
+          }
+          if (row >= 0)
+            tma_load_3d_lane(sRing + slot * C::kTileBytes + hfl * (kKeys * 128) + my_piece * 128, kv ? &a.tm_v : &a.tm_k,
+                             &bar->kv_full[slot], 64 * hfl, s.hkv, row);
+          __syncwarp();
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (; j < nctx; ++j, ++n) {
+        if (!before_tile(j)) return false;
+        const int i = 2 * n + kv0, slot = i % kStages;
+        if (!wait_slot(i)) return false;
+        mbar_arrive_expect_tx(&bar->kv_full[slot], C::kTileBytes);
+        for (int hf = 0; hf < C::kHalves; ++hf)
+          tma_load_3d(sRing + slot * C::kTileBytes + hf * (kKeys * 128), kv0 ? &a.tm_v : &a.tm_k, &bar->kv_full[slot], 64 * hf,
+                      (s.k0 + j) * kKeys, s.b * a.Hkv + s.hkv);
+      }
+    }
+#pragma unroll 1
+    for (; j < s.nt; ++j, ++n) {
       if (!before_tile(j)) return false;
-      const int kt = s.k0 + j, row = row_next;
-      if (a.block_table) row_next = pool_row(kt + 1);
-      for (int kv = kv0; kv < kv1; ++kv)
-        if (!load_tile(s, kv, member, kt, n, row)) return false;
+      for (int kv = kv0; kv < kv1; ++kv) {
+        const int i = 2 * n + kv, slot = i % kStages;
+        if (!wait_slot(i)) return false;
+        if (member > 0) continue;  // drafts are the producers' alone; the helper keeps step
+        mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(a.new_box) * 128 * C::kHalves);
+        for (int hf = 0; hf < C::kHalves; ++hf)
+          tma_load_3d(sRing + slot * C::kTileBytes + hf * (kKeys * 128), kv ? &a.tm_vn : &a.tm_kn, &bar->kv_full[slot], 64 * hf,
+                      s.hkv, s.tok0 + (s.k0 + j - s.ct) * kKeys);
+      }
     }
     return true;
   };
