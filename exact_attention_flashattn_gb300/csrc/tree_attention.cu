@@ -304,6 +304,13 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
 
   asm volatile("griddepcontrol.launch_dependents;");  // the merge waits for this grid to complete
 
+  if (warp == C::kTmaWarp && lane == 0) {
+    prefetch_tmap(&a.tm_q);
+    prefetch_tmap(&a.tm_k);
+    prefetch_tmap(&a.tm_v);
+    prefetch_tmap(&a.tm_kn);
+    prefetch_tmap(&a.tm_vn);
+  }
   // ---- the list of tiles: a thread sums the tiles of a run of sequences. Up to 128 sequences the
   // producer warp does it alone (nobody else needs the list), beyond that the whole block
   const bool wide = a.num_seqs > 128;
@@ -484,13 +491,6 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   if (warp == C::kTmaWarp) {
     // ------------------------------------------------------------ segments, Q and K tiles
     Regs<D, kTiles>::give();
-    if (lane == 0) {
-      prefetch_tmap(&a.tm_q);
-      prefetch_tmap(&a.tm_k);
-      prefetch_tmap(&a.tm_v);
-      prefetch_tmap(&a.tm_kn);
-      prefetch_tmap(&a.tm_vn);
-    }
     const Share share(bar->list[0], a.groups);
     const int c = group, head0 = static_cast<int>(blockIdx.x) - group * a.head_group;
     const int begin = c < share.G ? share.begin(c) : 0, end = c < share.G && bar->list[0] > 0 ? share.begin(c + 1) : 0;
@@ -499,15 +499,17 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     bool ok = true;
     for (int k = 0; ok; ++k) {
       Seg s{};
+      int u0 = 0, size = 0;  // the unit's first place, and its places
       while (pos < end && !s.valid) {
         SeqTiles<D> q = seq_tiles<D, kTiles>(a, b);
         while (pos >= seq_at + q.all(a.head_groups)) {
           seq_at += q.all(a.head_groups);
           q = seq_tiles<D, kTiles>(a, ++b);
         }
-        const int size = q.per_unit + tree_unit_cost(D), local = pos - seq_at, unit = local / size;
+        size = q.per_unit + tree_unit_cost(D);
+        const int local = pos - seq_at, unit = local / size;
         const int at = local - unit * size, to = min(size, at + end - pos);  // places of the unit
-        const int u0 = pos - at;
+        u0 = pos - at;
         pos += to - at;
         s.k0 = max(at - tree_unit_cost(D), 0);
         s.nt = to - tree_unit_cost(D) - s.k0;
@@ -522,19 +524,6 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         s.node0 = (unit - heads * q.row_units) * (kTiles * tile_nodes);
         s.ct = q.ct;
         s.slot = s.nt == q.per_unit ? -1 : (k == 0 ? 0 : 1);
-        if (k == 0 && lane == 0) {
-          TreeMergeRec r{};
-          if (s.k0 > 0 && share.owner(u0 + tree_unit_cost(D)) == c - 1) {
-            r.rows0 = tile_rows(s, 0);
-            r.rows1 = kTiles == 2 ? tile_rows(s, 1) : 0;
-            r.node0 = s.tok0 + s.node0;
-            r.node_step = tile_nodes;
-            r.hkv = s.hkv;
-            r.slot0 = u0 <= share.begin(c - 1) ? 0 : 1;
-            r.last = share.owner(u0 + size - 1) * a.head_group + head0;
-          }
-          a.merge[blockIdx.x] = r;
-        }
       }
       if (k == 0 && !s.valid && lane == 0) a.merge[blockIdx.x] = TreeMergeRec{};  // no part here
       if (k >= kSegSlots && !(ok = vote(mbar_wait(&bar->seg_empty[k % kSegSlots], (k / kSegSlots - 1) & 1, tmo, abort))))
@@ -557,9 +546,24 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         }
         return true;
       };
-      const int q_at = min(s.nt, (kStages + 3) / 4);  // the first loads need ring slots only, not Q's buffer
+      // later segments: the first loads need ring slots only, not Q's buffer
+      const int q_at = k == 0 ? 0 : min(s.nt, (kStages + 3) / 4);
       ok = load_tiles(s, 0, 1, 0, nload, [&](int j) { return j != q_at || load_q(); });
       if (ok && q_at == s.nt) ok = load_q();
+      if (k == 0 && lane == 0) {
+        // what the merge has to know, once the loads are on their way
+        TreeMergeRec r{};
+        if (s.k0 > 0 && share.owner(u0 + tree_unit_cost(D)) == c - 1) {
+          r.rows0 = tile_rows(s, 0);
+          r.rows1 = kTiles == 2 ? tile_rows(s, 1) : 0;
+          r.node0 = s.tok0 + s.node0;
+          r.node_step = tile_nodes;
+          r.hkv = s.hkv;
+          r.slot0 = u0 <= share.begin(c - 1) ? 0 : 1;
+          r.last = share.owner(u0 + size - 1) * a.head_group + head0;
+        }
+        a.merge[blockIdx.x] = r;
+      }
     }
     if (!ok && lane == 0) raise_timeout(abort, a.status);
     // every copy this warp issued must have landed before the CTA may exit
