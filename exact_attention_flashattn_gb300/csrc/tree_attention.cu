@@ -186,32 +186,44 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32
 template <int kHalves, int kKeys>
 __device__ __forceinline__ bool clean_v(uint8_t* tile, int valid, bool scan, int lane) {
   bool bad = false;
+  if (scan) {
+    // four pieces of 16 bytes a lane at a time (one by one, 32 drafts at d = 256 took longer than their softmax)
+    constexpr int kRun = 4 / kHalves;
+    const int end = valid * 128;
 #pragma unroll 1
-  for (int hf = 0; hf < kHalves; ++hf) {
-    uint8_t* atom = tile + hf * (kKeys * 128);
-    if (scan) {
-      for (int off = lane * 16; off < valid * 128; off += 512) {
-        uint4 v = *reinterpret_cast<uint4*>(atom + off);
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int off = lane * 16; off < end; off += 512 * kRun) {
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = off + 512 * (i / kHalves);
+        v[i] = at < end ? *reinterpret_cast<const uint4*>(tile + i % kHalves * (kKeys * 128) + at) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
         bool hit = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if ((w[i] & 0x7f80u) == 0x7f80u) {
-            w[i] &= 0xffff0000u;
+        for (int e = 0; e < 4; ++e) {
+          if ((w[e] & 0x7f80u) == 0x7f80u) {
+            w[e] &= 0xffff0000u;
             hit = true;
           }
-          if ((w[i] & 0x7f800000u) == 0x7f800000u) {
-            w[i] &= 0xffffu;
+          if ((w[e] & 0x7f800000u) == 0x7f800000u) {
+            w[e] &= 0xffffu;
             hit = true;
           }
         }
-        if (hit) *reinterpret_cast<uint4*>(atom + off) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (hit)
+          *reinterpret_cast<uint4*>(tile + i % kHalves * (kKeys * 128) + off + 512 * (i / kHalves)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
         bad |= hit;
       }
     }
-    for (int off = valid * 128 + lane * 16; off < (valid + 15) / 16 * 2048; off += 512)
-      *reinterpret_cast<uint4*>(atom + off) = make_uint4(0u, 0u, 0u, 0u);
   }
+#pragma unroll
+  for (int hf = 0; hf < kHalves; ++hf)
+    for (int off = valid * 128 + lane * 16; off < (valid + 15) / 16 * 2048; off += 512)
+      *reinterpret_cast<uint4*>(tile + hf * (kKeys * 128) + off) = make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the tensor pipe reads the tile
   __syncwarp();
   return __any_sync(0xffffffffu, bad);
