@@ -181,7 +181,7 @@ struct TreeArgs {
   int new_box;            // rows of a copy of drafted rows
   int head_group, head_groups;  // KV heads that a group of CTAs takes side by side; Hkv / head_group
   int groups;             // groups of CTAs of the attention kernel
-  int merges;             // units that may have to be merged
+  int merges, merge_warps;  // units that may have to be merged; warps that share out one's parts
   float scale_log2;
   unsigned int* status;
   uint64_t timeout_ns;

@@ -973,17 +973,24 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
 
 // The parts of units that several CTAs shared. At most one unit per boundary between two CTAs has to
 // be merged, so the grid is (boundaries, quarters of a row tile x row tiles, groups of 32 channels),
-// whatever the lengths; or, where the call has far fewer units than that, (units, ...), each block counting
-// its way to its record (2 x 8 units of 8192 keys on 304 CTAs: 23.0 us in all, with a block for every
-// boundary, most of them empty, 24.7; one warp a block reads the records, as all eight made their few lines
-// of L2 a bottleneck and took 4 us). Lanes are rows; the warps share out the parts, each with its own running
-// maximum, and are joined in shared memory in their order:
+// whatever the lengths; or, where the call has fewer units than that, (units, ...), each block counting
+// its way to its record (2 x 8 units of 8192 keys on 304 CTAs: 21.5 us in all, with a block for every
+// boundary, most of them empty, 24.4; one warp a block reads the records, as all eight made their few lines
+// of L2 a bottleneck and took 4 us). Lanes are rows; the warps (as many as a unit has parts on average, up to
+// kMergeWarps) share out the parts, each with its own running maximum, and are joined in shared memory in
+// their order:
 //   m = max m_c, l = sum l_c 2^(m_c - m), o likewise.
+// What bounds it is latency: the records, then the parts. So a warp has two parts' loads under way (the parts
+// of 8 units of 4096 keys on 280 CTAs: 14.8 us in all, one at a time 16.6).
 constexpr int kMergeWarps = 8;
+constexpr int kMergeQuads = 8;  // channels of a block, in fours
+constexpr uint32_t merge_smem(int warps) { return warps * (kMergeQuads * 33 * 16 + 32 * 8); }
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const float* partial, const TreeMergeRec* merge, uint16_t* out,
-                                                                       float* lse, int D, int tiles, int g, int Hq, int head_group, int ctas) {
-  __shared__ float4 sm_o[kMergeWarps][8][33];  // 33: the joining threads' columns fall on different banks
-  __shared__ float2 sm_ml[kMergeWarps][32];
+                                                                       float* lse, int D, int quarters, int tiles, int g, int Hq, int head_group, int ctas) {
+  const int warps = blockDim.x / 32;
+  extern __shared__ float4 sm_merge[];
+  auto sm_o = reinterpret_cast<float4 (*)[kMergeQuads][33]>(sm_merge);  // 33: the joining threads' columns fall on different banks
+  auto sm_ml = reinterpret_cast<float2 (*)[32]>(sm_merge + warps * kMergeQuads * 33);
   __shared__ int sm_c;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts and records are complete and visible
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1019,63 +1026,82 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const floa
     c = sm_c;
     if (c == 0) return;
   }
-  const int w = blockIdx.y >> 2, quarter = blockIdx.y & 3, cg = blockIdx.z;
+  const int w = static_cast<int>(blockIdx.y) / quarters, quarter = static_cast<int>(blockIdx.y) - w * quarters, cg = blockIdx.z;
   const int4 r0 = __ldcg(reinterpret_cast<const int4*>(merge + c)), r1 = __ldcg(reinterpret_cast<const int4*>(merge + c) + 1);
   const int rows = w ? r0.y : r0.x, hkv = r1.x, slot0 = r1.y, last = r1.z;
   if (32 * quarter >= rows) return;
   const int row = 32 * quarter + lane;
-  const int64_t size = kTreeRows * (D + 2);
   float m = -INFINITY, l = 0.f;
-  float4 acc[8];
+  float4 acc[kMergeQuads];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int q = 0; q < kMergeQuads; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (row < rows) {
-    for (int x = c + (warp - 1) * head_group; x <= last; x += kMergeWarps * head_group) {
-      const float* p = partial + ((static_cast<int64_t>(x) * 2 + (x < c ? slot0 : 0)) * tiles + w) * size;
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + kTreeRows * D + 2 * row));
-      float4 v[8];
+    struct Part {
+      float2 ml;
+      float4 v[kMergeQuads];
+    };
+    auto load = [&](int x, Part& part) {
+      const float* p = partial + ((static_cast<int64_t>(x) * 2 + (x < c ? slot0 : 0)) * tiles + w) * (kTreeRows * (D + 2));
+      part.ml = __ldcg(reinterpret_cast<const float2*>(p + kTreeRows * D + 2 * row));
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = __ldcg(reinterpret_cast<const float4*>(p + ((cg * 8 + q) * kTreeRows + row) * 4));
-      const float mn = fmaxf(m, ml.x);
-      const float f0 = m == -INFINITY ? 0.f : ex2(m - mn), f1 = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
+      for (int q = 0; q < kMergeQuads; ++q)
+        part.v[q] = __ldcg(reinterpret_cast<const float4*>(p + ((cg * kMergeQuads + q) * kTreeRows + row) * 4));
+    };
+    const int step = warps * head_group;
+#pragma unroll 1
+    for (int x = c + (warp - 1) * head_group; x <= last; x += 2 * step) {
+      // two parts' loads at a time: the loop is as long as their latency
+      Part a, b;
+      load(x, a);
+      if (x + step <= last) {
+        load(x + step, b);
+      } else {
+        b.ml = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int q = 0; q < kMergeQuads; ++q) b.v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      const float mn = max3f(m, a.ml.x, b.ml.x);
+      const float f0 = m == -INFINITY ? 0.f : ex2(m - mn), f1 = a.ml.x == -INFINITY ? 0.f : ex2(a.ml.x - mn),
+                  f2 = b.ml.x == -INFINITY ? 0.f : ex2(b.ml.x - mn);
       m = mn;
-      l = l * f0 + ml.y * f1;
+      l = l * f0 + a.ml.y * f1 + b.ml.y * f2;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        acc[q].x = acc[q].x * f0 + v[q].x * f1;
-        acc[q].y = acc[q].y * f0 + v[q].y * f1;
-        acc[q].z = acc[q].z * f0 + v[q].z * f1;
-        acc[q].w = acc[q].w * f0 + v[q].w * f1;
+      for (int q = 0; q < kMergeQuads; ++q) {
+        acc[q].x = acc[q].x * f0 + a.v[q].x * f1 + b.v[q].x * f2;
+        acc[q].y = acc[q].y * f0 + a.v[q].y * f1 + b.v[q].y * f2;
+        acc[q].z = acc[q].z * f0 + a.v[q].z * f1 + b.v[q].z * f2;
+        acc[q].w = acc[q].w * f0 + a.v[q].w * f1 + b.v[q].w * f2;
       }
     }
   }
   sm_ml[warp][lane] = make_float2(m, l);
 #pragma unroll
-  for (int q = 0; q < 8; ++q) sm_o[warp][q][lane] = acc[q];
+  for (int q = 0; q < kMergeQuads; ++q) sm_o[warp][q][lane] = acc[q];
   __syncthreads();
-  // thread = (row, channel quad): 8 threads write a row's 64 bytes
-  const int jr = threadIdx.x >> 3, jq = threadIdx.x & 7;
-  if (32 * quarter + jr >= rows) return;
-  const int used = min(kMergeWarps, (last - c) / head_group + 2);
-  float M = -INFINITY, L = 0.f;
-  for (int x = 0; x < used; ++x) M = fmaxf(M, sm_ml[x][jr].x);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int x = 0; x < used; ++x) {
-    const float2 ml = sm_ml[x][jr];
-    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-    const float4 v = sm_o[x][jq][jr];
-    L += ml.y * f;
-    o.x += v.x * f;
-    o.y += v.y * f;
-    o.z += v.z * f;
-    o.w += v.w * f;
+  const int used = min(warps, (last - c) / head_group + 2);
+  for (int i = threadIdx.x; i < 32 * kMergeQuads; i += blockDim.x) {
+    const int jr = i / kMergeQuads, jq = i % kMergeQuads;  // row, channel quad
+    const int rr = 32 * quarter + jr;
+    if (rr >= rows) break;
+    float M = -INFINITY, L = 0.f;
+    for (int x = 0; x < used; ++x) M = fmaxf(M, sm_ml[x][jr].x);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < used; ++x) {
+      const float2 ml = sm_ml[x][jr];
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+      const float4 v = sm_o[x][jq][jr];
+      L += ml.y * f;
+      o.x += v.x * f;
+      o.y += v.y * f;
+      o.z += v.z * f;
+      o.w += v.w * f;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int64_t orow = static_cast<int64_t>(r0.z + w * r0.w + rr / g) * Hq + hkv * g + rr % g;
+    *reinterpret_cast<uint2*>(out + orow * D + 4 * (cg * kMergeQuads + jq)) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (lse && cg == 0 && jq == 0) lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  const int rr = 32 * quarter + jr;
-  const int64_t orow = static_cast<int64_t>(r0.z + w * r0.w + rr / g) * Hq + hkv * g + rr % g;
-  *reinterpret_cast<uint2*>(out + orow * D + cg * 32 + 4 * jq) =
-      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (lse && cg == 0 && jq == 0) lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 template <int D, int kTiles>
@@ -1094,8 +1120,10 @@ cudaError_t launch(const TreeArgs& a, int dev, cudaStream_t stream) {
   count_launch();
   if (a.groups == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.merges, 4 * kTiles, D / 32);
-  cfg.blockDim = dim3(kMergeWarps * 32);
+  const int quarters = a.tile_rows / 32;
+  cfg.gridDim = dim3(a.merges, quarters * kTiles, D / (4 * kMergeQuads));
+  cfg.blockDim = dim3(a.merge_warps * 32);
+  cfg.dynamicSmemBytes = merge_smem(a.merge_warps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1103,7 +1131,7 @@ cudaError_t launch(const TreeArgs& a, int dev, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, static_cast<const float*>(a.partial), static_cast<const TreeMergeRec*>(a.merge), a.o,
-                         a.lse, D, kTiles, a.g, a.Hq, a.head_group, a.groups * a.head_group);
+                         a.lse, D, quarters, kTiles, a.g, a.Hq, a.head_group, a.groups * a.head_group);
   if (e == cudaSuccess) count_launch();
   return e;
 }
@@ -1157,10 +1185,9 @@ cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
   a.groups = ctas / a.head_group;
   if (a.groups > most / a.head_group) a.groups = static_cast<int>(most / a.head_group);
   const int64_t boundaries = static_cast<int64_t>(a.groups - 1) * a.head_group, units = tree_most_units(a);
-  // up to two waves of blocks (six an SM) the empty ones cost less than finding the records (10 parts of 8
-  // heads, 1280 blocks: 12.3 against 12.9 us; 273 parts of them, 4400 blocks: 18.2 against 17.4)
-  const bool few = boundaries * 4 * tiles * (d / 32) <= 12 * sms;
-  a.merges = static_cast<int>(few || units > boundaries ? boundaries : units);
+  a.merges = static_cast<int>(units < boundaries ? units : boundaries);
+  a.merge_warps = kMergeWarps;  // a power of two, at least the parts of a unit on average
+  while (a.merge_warps > 2 && boundaries / units + 2 <= a.merge_warps / 2) a.merge_warps /= 2;
   if (d == 64) return tiles == 2 ? launch<64, 2>(a, dev, stream) : launch<64, 1>(a, dev, stream);
   if (d == 128) return tiles == 2 ? launch<128, 2>(a, dev, stream) : launch<128, 1>(a, dev, stream);
   return launch<256, 1>(a, dev, stream);
