@@ -176,7 +176,7 @@ struct TreeArgs {
   int Hq, Hkv, g, d;
   int kv_cap;             // keys a sequence's cache can hold
   int page_size, max_pages, num_pages;
-  int tile_rows;          // tree_tile_rows(max_nodes, g, d)
+  int tile_rows, tile_nodes;  // tree_tile_rows(max_nodes, g, d); / g
   int piece;              // paged: rows of a copy, a power of two that divides page_size
   int new_box;            // rows of a copy of drafted rows
   int head_group, head_groups;  // KV heads that a group of CTAs takes side by side; Hkv / head_group

@@ -141,8 +141,8 @@ __device__ __forceinline__ SeqTiles<D> seq_tiles(const TreeArgs& a, int b) {
   s.nk = min(max(a.nk[b], 0), a.kv_cap);
   s.ct = s.nk / kKeys + (s.nk % kKeys != 0);
   s.per_unit = s.ct + (s.nq + kKeys - 1) / kKeys;
-  const int unit_nodes = kTiles * (a.tile_rows / a.g);
-  s.row_units = (s.nq + unit_nodes - 1) / unit_nodes;  // 0 for a sequence without nodes
+  const int unit_nodes = kTiles * a.tile_nodes;
+  s.row_units = s.nq <= unit_nodes ? s.nq > 0 : (s.nq + unit_nodes - 1) / unit_nodes;  // 0 for a sequence without nodes
   return s;
 }
 
@@ -372,6 +372,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  int my_begin = 0, my_end = 0;  // the group's places
   if (wide || warp == C::kTmaWarp) {
     int T = __shfl_sync(0xffffffffu, incl, 31), before = incl - mine;
     if (wide) {
@@ -382,10 +383,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       }
     }
     const Share share(T, a.groups);
-    const int begin = share.begin(group);
-    if (group < share.G && before <= begin && begin < before + mine) {
+    if (group < share.G && T > 0) my_begin = share.begin(group), my_end = share.begin(group + 1);
+    if (my_begin < my_end && before <= my_begin && my_begin < before + mine) {
       int b = run0;
-      for (int n; begin >= before + (n = seq_tiles<D, kTiles>(a, b).all(a.head_groups)); ++b) before += n;
+      for (int n; my_begin >= before + (n = seq_tiles<D, kTiles>(a, b).all(a.head_groups)); ++b) before += n;
       bar->list[1] = b;
       bar->list[2] = before;
     }
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_base, 0);
   volatile int* abort = &bar->abort;
   const uint64_t tmo = a.timeout_ns;
-  const int tile_nodes = a.tile_rows / a.g;
+  const int tile_nodes = a.tile_nodes;
   // TMEM lane of a tile's first row
   const int first_lane = a.tile_rows == 64 && 2 * blockIdx.x >= gridDim.x ? 64 : 0;
   const int no_abort = 0;
@@ -503,10 +504,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   if (warp == C::kTmaWarp) {
     // ------------------------------------------------------------ segments, Q and K tiles
     Regs<D, kTiles>::give();
-    const Share share(bar->list[0], a.groups);
-    const int c = group, head0 = static_cast<int>(blockIdx.x) - group * a.head_group;
-    const int begin = c < share.G ? share.begin(c) : 0, end = c < share.G && bar->list[0] > 0 ? share.begin(c + 1) : 0;
-    int pos = begin, b = pos < end ? bar->list[1] : 0, seq_at = pos < end ? bar->list[2] : 0;
+    const int head0 = static_cast<int>(blockIdx.x) - group * a.head_group, end = my_end;
+    int pos = my_begin, b = pos < end ? bar->list[1] : 0, seq_at = pos < end ? bar->list[2] : 0;
     int nload = 0, nq[2] = {0, 0};  // K tiles, and Q tiles into each buffer
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -531,7 +530,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         s.tok0 = q.tok0;
         s.nq = q.nq;
         s.nk = q.nk;
-        const int heads = unit / q.row_units;
+        const int heads = q.row_units == 1 ? unit : unit / q.row_units;
         s.hkv = heads * a.head_group + head0;
         s.node0 = (unit - heads * q.row_units) * (kTiles * tile_nodes);
         s.ct = q.ct;
@@ -565,13 +564,14 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       if (k == 0 && lane == 0) {
         // what the merge has to know, once the loads are on their way
         TreeMergeRec r{};
-        if (s.k0 > 0 && share.owner(u0 + tree_unit_cost(D)) == c - 1) {
+        const Share share(bar->list[0], a.groups);
+        if (s.k0 > 0 && share.owner(u0 + tree_unit_cost(D)) == group - 1) {
           r.rows0 = tile_rows(s, 0);
           r.rows1 = kTiles == 2 ? tile_rows(s, 1) : 0;
           r.node0 = s.tok0 + s.node0;
           r.node_step = tile_nodes;
           r.hkv = s.hkv;
-          r.slot0 = u0 <= share.begin(c - 1) ? 0 : 1;
+          r.slot0 = u0 <= share.begin(group - 1) ? 0 : 1;
           r.last = share.owner(u0 + size - 1) * a.head_group + head0;
         }
         a.merge[blockIdx.x] = r;
@@ -1146,7 +1146,8 @@ cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
   a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kTreeMergeBytes);
   const int d = a.d, keys = d == 256 ? 64 : 128;
   a.tile_rows = tree_tile_rows(a.max_nodes, a.g, d);
-  if ((e = make_map_bf16(&a.tm_q, a.q, d, a.Hq, a.total_q, d, a.q_stride, a.g, a.tile_rows / a.g)) != cudaSuccess) return e;
+  a.tile_nodes = a.tile_rows / a.g;
+  if ((e = make_map_bf16(&a.tm_q, a.q, d, a.Hq, a.total_q, d, a.q_stride, a.g, a.tile_nodes)) != cudaSuccess) return e;
   a.new_box = a.max_nodes < keys ? (a.max_nodes + 7) / 8 * 8 : keys;
   if ((e = make_map_bf16(&a.tm_kn, a.k_new, d, a.Hkv, a.total_q, d, a.k_new_stride, 1, a.new_box)) != cudaSuccess ||
       (e = make_map_bf16(&a.tm_vn, a.v_new, d, a.Hkv, a.total_q, d, a.v_new_stride, 1, a.new_box)) != cudaSuccess)
