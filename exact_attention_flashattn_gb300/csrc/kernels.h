@@ -214,6 +214,25 @@ inline int64_t tree_most_tiles(const TreeArgs& a) {
 // Fills the maps and sizes that follow from the others, launches the attention and the merge.
 cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream);
 
+#ifdef __CUDACC__
+// Launches a kernel whose threads all begin with griddepcontrol.wait: it may be set up while the kernel
+// before it in the stream ends.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+#endif
+
 // ---- paged cache bookkeeping ----
 struct TreeMaskArgs {
   const int32_t* parents;

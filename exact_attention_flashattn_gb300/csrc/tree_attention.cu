@@ -314,31 +314,12 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   const int group = static_cast<int>(blockIdx.x) / a.head_group;  // of CTAs with the same places
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
-  asm volatile("griddepcontrol.launch_dependents;");  // the merge waits for this grid to complete
-
   if (warp == C::kTmaWarp && lane == 0) {
     prefetch_tmap(&a.tm_q);
     prefetch_tmap(&a.tm_k);
     prefetch_tmap(&a.tm_v);
     prefetch_tmap(&a.tm_kn);
     prefetch_tmap(&a.tm_vn);
-  }
-  // ---- the list of tiles: a thread sums the tiles of a run of sequences. Up to 128 sequences the
-  // producer warp does it alone (nobody else needs the list), beyond that the whole block
-  const bool wide = a.num_seqs > 128;
-  const int run = wide ? (a.num_seqs + C::kThreads - 1) / C::kThreads : (a.num_seqs + 31) / 32;
-  const int run0 = min((wide ? tid : lane) * run, a.num_seqs), run1 = min(run0 + run, a.num_seqs);
-  int mine = 0, incl = 0;
-  if (wide || warp == C::kTmaWarp) {
-#pragma unroll 4
-    for (int b = run0; b < run1; ++b) mine += seq_tiles<D, kTiles>(a, b).all(a.head_groups);
-    incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += x;
-    }
-    if (wide && lane == 31) bar->scan[warp] = incl;
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -369,9 +350,31 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     tmem_alloc(&bar->tmem_base, C::kCols);
     tmem_relinquish();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what the stream did before is complete and visible
+
+  // ---- the list of tiles: a thread sums the tiles of a run of sequences. Up to 128 sequences the
+  // producer warp does it alone (nobody else needs the list), beyond that the whole block
+  const bool wide = a.num_seqs > 128;
+  const int run = wide ? (a.num_seqs + C::kThreads - 1) / C::kThreads : (a.num_seqs + 31) / 32;
+  const int run0 = min((wide ? tid : lane) * run, a.num_seqs), run1 = min(run0 + run, a.num_seqs);
+  int mine = 0, incl = 0;
+  if (wide || warp == C::kTmaWarp) {
+#pragma unroll 4
+    for (int b = run0; b < run1; ++b) mine += seq_tiles<D, kTiles>(a, b).all(a.head_groups);
+    incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += x;
+    }
+    if (wide && lane == 31) bar->scan[warp] = incl;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // the merge may be set up from now on; it waits for this grid to complete. Not before this CTA has its tensor
+  // memory: a dependent kernel's CTA that held some beside it would wait for this grid
+  asm volatile("griddepcontrol.launch_dependents;");
   int my_begin = 0, my_end = 0;  // the group's places
   if (wide || warp == C::kTmaWarp) {
     int T = __shfl_sync(0xffffffffu, incl, 31), before = incl - mine;
@@ -1115,23 +1118,14 @@ cudaError_t launch(const TreeArgs& a, int dev, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev < 64) set.fetch_or(1ull << dev);
   }
-  tree_kernel<D, kTiles><<<a.groups * a.head_group, C::kThreads, C::kSmem, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_dependent(tree_kernel<D, kTiles>, dim3(a.groups * a.head_group), C::kThreads, C::kSmem, stream, a);
+  if (e != cudaSuccess) return e;
   count_launch();
   if (a.groups == 1) return cudaSuccess;
-  cudaLaunchConfig_t cfg = {};
   const int quarters = a.tile_rows / 32;
-  cfg.gridDim = dim3(a.merges, quarters * kTiles, D / (4 * kMergeQuads));
-  cfg.blockDim = dim3(a.merge_warps * 32);
-  cfg.dynamicSmemBytes = merge_smem(a.merge_warps);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, tree_merge_kernel, static_cast<const float*>(a.partial), static_cast<const TreeMergeRec*>(a.merge), a.o,
-                         a.lse, D, quarters, kTiles, a.g, a.Hq, a.head_group, a.groups * a.head_group);
+  e = launch_dependent(tree_merge_kernel, dim3(a.merges, quarters * kTiles, D / (4 * kMergeQuads)), a.merge_warps * 32,
+                       merge_smem(a.merge_warps), stream, a.partial, a.merge, a.o, a.lse, D, quarters, kTiles, a.g, a.Hq,
+                       a.head_group, a.groups * a.head_group);
   if (e == cudaSuccess) count_launch();
   return e;
 }
