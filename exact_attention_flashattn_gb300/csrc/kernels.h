@@ -215,8 +215,8 @@ inline int64_t tree_most_tiles(const TreeArgs& a) {
 cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream);
 
 #ifdef __CUDACC__
-// Launches a kernel whose threads all begin with griddepcontrol.wait: it may be set up while the kernel
-// before it in the stream ends.
+// Launches a kernel whose threads all pass griddepcontrol.wait before they touch memory: it may be set up
+// while the kernel before it in the stream ends.
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg = {};

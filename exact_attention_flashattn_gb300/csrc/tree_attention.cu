@@ -346,11 +346,13 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     bar->abort = 0;
     fence_mbar_init();
   }
+  // What the stream did before is complete and visible from here on. No tensor memory is held while
+  // waiting: a CTA of the kernel before, beside this one, may have yet to take its own.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == C::kMmaWarp) {
     tmem_alloc(&bar->tmem_base, C::kCols);
     tmem_relinquish();
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // what the stream did before is complete and visible
 
   // ---- the list of tiles: a thread sums the tiles of a run of sequences. Up to 128 sequences the
   // producer warp does it alone (nobody else needs the list), beyond that the whole block
@@ -372,8 +374,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // the merge may be set up from now on; it waits for this grid to complete. Not before this CTA has its tensor
-  // memory: a dependent kernel's CTA that held some beside it would wait for this grid
+  // the merge may be set up from now on; it waits for this grid to complete (not before this CTA has its
+  // tensor memory, for the same reason)
   asm volatile("griddepcontrol.launch_dependents;");
   int my_begin = 0, my_end = 0;  // the group's places
   if (wide || warp == C::kTmaWarp) {

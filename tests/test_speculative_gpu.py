@@ -702,3 +702,107 @@ def test_a_serving_run(page, fp8):
                 dst[b, :, :len(x)] = x.double().cpu().numpy().transpose(1, 0, 2)
         ref, _ = oracle.decode(q.double().cpu().numpy(), kc, vc, nk.cpu().numpy(), method="naive")
     assert np.abs(o.double().cpu().numpy() - ref).max() <= 2e-2  # the decode's own bound
+
+
+@pytest.mark.parametrize("how", ["eager", "graph"])
+def test_back_to_back_chain(how):
+    """Each kernel reads what the one before it wrote, with nothing in between: the packed prefill's output
+    is the trees' queries, their output the rows that are appended, and a decode reads the pages. The same
+    calls with a synchronisation behind each give the values."""
+    Hq, Hkv, d, page, B = 16, 4, 128, 16, 3
+    q_lens, k_lens, nodes, nk = [300, 7, 40], [300, 900, 40], [30, 7, 40], [1000, 17, 300]
+    g = gen(77)
+    q = randn((sum(q_lens), Hq, d), g)
+    k, v = randn((sum(k_lens), Hkv, d), g), randn((sum(k_lens), Hkv, d), g)
+    cu_q, cu_k, cu_n = sums(q_lens), sums(k_lens), sums(nodes)
+    total = sum(nodes)
+    pages0 = [randn((120, page, Hkv, d), g) for _ in range(2)]
+    kp, vp = (x.clone() for x in pages0)
+    r = np.random.default_rng(3)
+    parents = i32(np.concatenate([[r.integers(-1, i) if i else -1 for i in range(n)] for n in nodes]).tolist())
+    have = [(n + page - 1) // page for n in nk]
+    table0 = torch.full((B, 70), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(have):
+        table0[b, :n] = torch.arange(at, at + n, device="cuda")
+        at += n
+    table = table0.clone()
+    free, count, n_new = torch.arange(at, 120, dtype=torch.int32, device="cuda"), i32([120 - at]), i32(nodes)
+    lens, held = i32(nk), i32(have)
+    ws = torch.empty(bw.tree_workspace_size(B, max(nodes), Hq, Hkv, d), dtype=torch.uint8, device="cuda")
+
+    def chain(between):
+        kp.copy_(pages0[0]), vp.copy_(pages0[1]), table.copy_(table0)
+        between()
+        o, _ = bw.attn_varlen(q, k, v, cu_q, cu_k, max(q_lens), max(k_lens), causal=True)
+        between()
+        nk1, _, cu, slots, left = bw.kv_plan_paged(lens, n_new, table, held, free, count, page, total)
+        between()
+        mask, _ = bw.attn_tree_mask(parents, cu, max(nodes), nk=lens)
+        between()
+        qt = o[:total]
+        o2, lse2 = bw.attn_tree_paged(qt, kp, vp, table, qt[:, :Hkv], qt[:, Hkv:2 * Hkv], lens, cu, mask, max(nodes), workspace=ws)
+        between()
+        bw.kv_append_paged(o2[:, :Hkv], o2[:, Hkv:2 * Hkv], slots, kp, vp)
+        between()
+        mask2, pos = bw.attn_tree_mask(parents, cu, max(nodes), nk=nk1)
+        between()
+        o3, lse3 = bw.attn_tree_paged(o2, kp, vp, table, o2[:, :Hkv], o2[:, Hkv:2 * Hkv], nk1, cu, mask2, max(nodes), workspace=ws)
+        between()
+        o4, lse4 = bw.attn_decode_paged(o3[:B], kp, vp, table.clamp(min=0), nk1, num_splits=4)
+        return o, o2, lse2, o3, lse3, o4, lse4, kp, vp, table, slots, pos, left
+
+    want = [x.clone() for x in chain(torch.cuda.synchronize)]
+    assert int(want[-1]) >= 0
+    if how == "graph":
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = chain(lambda: None)
+    for _ in range(20):
+        if how == "graph":
+            graph.replay()
+        else:
+            got = chain(lambda: None)
+        for i, (x, w) in enumerate(zip(got, want)):
+            assert torch.equal(x, w), i
+
+
+def test_fork_and_join_in_a_graph():
+    # kernels with dependencies on two streams at once, captured: the append on one, the mask on the other,
+    # both joined ahead of the attention that reads the pages and the mask
+    t = Case(16, 4, 128, 16, [500, 33], [20, 9], "tree", seed=91)
+    n = sum(t.nodes)
+    parents = i32([-1] + [(i - 1) // 2 for i in range(1, 20)] + [-1] + [(i - 1) // 2 for i in range(1, 9)] + [0] * (t.total - n))
+    slots = torch.cat([t.table[0, :2], t.table[1, :2]]).repeat_interleave(7) * 16 + torch.arange(28, device="cuda").to(torch.int32) % 7
+    k0, v0 = t.k.clone(), t.v.clone()
+    ws = torch.empty(bw.tree_workspace_size(2, t.max_nodes, 16, 4, 128), dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(t.q), torch.empty((t.total, 16), device="cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def calls():
+        here = torch.cuda.current_stream()
+        t.k.copy_(k0), t.v.copy_(v0)
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            bw.attn_tree_mask(parents, t.cu, t.max_nodes, mask=t.mask)
+        bw.kv_append_paged(t.k_new, t.v_new, slots, t.k, t.v)
+        here.wait_stream(side)
+        t.run(out=o, lse=lse, workspace=ws)
+
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(main):
+        calls()
+    torch.cuda.synchronize()
+    bits = lambda x: x.view(torch.int16)  # unused rows hold NaN
+    want = o[:n].clone(), lse[:n].clone(), t.k.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        calls()
+    for _ in range(10):
+        o.zero_(), lse.zero_(), t.mask.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o[:n], want[0]) and torch.equal(lse[:n], want[1])
+        assert torch.equal(bits(t.k), bits(want[2]))
