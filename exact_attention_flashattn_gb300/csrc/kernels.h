@@ -140,7 +140,8 @@ constexpr int kTreeRows = 128;
 constexpr int kTreeMaxCtas = 304;    // persistent CTAs, two per SM (tree_max_ctas)
 constexpr int kTreeMergeBytes = 12288;
 // Tiles' time that a unit takes beside its tiles (its own Q, drafts, output; a tile is half the bytes at
-// d = 64). 48 ragged requests at d = 64: 118 us at 0, 107 at 2, 104 at 5; at d = 256: 44.7, 42.6, 44.3.
+// d = 64). 48 ragged requests at d = 64: 82.7 us at 3 and 4, 86.3 at 6 (before the hot loops were taken apart
+// 118 at 0); 30 ragged requests of two row tiles at d = 128: 82.6 us at 1, 78.0 at 2, 80.7 at 3.
 __host__ __device__ constexpr int tree_unit_cost(int d) { return d == 64 ? 4 : 2; }
 // What the merge has to do at the boundary between CTA c - 1 and CTA c, written by CTA c: something
 // if that is the first boundary inside a unit.
