@@ -456,40 +456,36 @@ def attn_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q:
 # index, the current stream is read as its raw handle (a Stream object costs 2 us), and nothing is
 # entered when the tensors' device is current and no stream is named.
 
-_I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
+_I32, _BF16, _F32, _Tensor = torch.int32, torch.bfloat16, torch.float32, torch.Tensor
+# the current device, and its current stream's handle (a Stream object takes 2 us; absent in a CPU-only torch)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _where(dev: int, stream):
-    """The stream handle of a call on device ``dev`` and the context to run it in: None on the current
-    device's current stream. What a call allocates belongs to its stream, so that the memory is not
-    handed to other work while the kernels still run."""
+def _run(fn, dev: int, stream, *args):
+    """``fn`` with the handle of the call's stream: the current one of device ``dev``, or ``stream``. What a
+    call allocates belongs to its stream, so that the memory is not handed to other work while the kernels
+    still run."""
     if stream is None:
-        if dev == torch._C._cuda_getDevice():
-            return torch._C._cuda_getCurrentRawStream(dev), None
+        if dev == _current_device():
+            return fn(_raw_stream(dev), dev, *args)
         stream = torch.cuda.current_stream(dev)
     if stream.device.index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
-    return stream.cuda_stream, torch.cuda.stream(stream)
-
-
-def _run(dev, stream, fn, *args):
-    st, context = _where(dev, stream)
-    if context is None:
-        return fn(st, *args)
-    with context:
-        return fn(st, *args)
+    with torch.cuda.stream(stream):
+        return fn(stream.cuda_stream, dev, *args)
 
 
 def _first(t, name, ndim):
     """The device index of a call's leading tensor."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != ndim:
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dim() != ndim:
         raise ValueError(f"{name} must be a {ndim}-D CUDA tensor")
     return t.get_device()
 
 
 def _like(t, name, dev, dtype, shape=None):
     """A contiguous tensor of that type on the call's device: its address."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
@@ -506,7 +502,7 @@ def _out(t, name, dev, dtype, shape):
 
 def _rows(t, name, dev, shape):
     """bf16 [rows, heads, d] whose rows may lie apart (a slice of a fused projection): the row stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != dev or t.shape != shape:
+    if not isinstance(t, _Tensor) or t.dtype is not _BF16 or t.get_device() != dev or t.shape != shape:
         raise ValueError(f"{name} must be a bf16 tensor {shape} on cuda:{dev}")
     n, h, c = shape
     if t.is_contiguous():
@@ -577,7 +573,7 @@ def attn_tree(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor, k_new
     [total_q, ceil(max_nodes / 64)] int64 (``attn_tree_mask`` makes it) -> (o, lse or None)."""
     dev = _first(q, "q", 3)
     _first(kcache, "kcache", 4)
-    return _run(dev, stream, _tree, dev, q, kcache, vcache, None, k_new, v_new, nk, cu_seqlens_q, mask, int(max_nodes),
+    return _run(_tree, dev, stream, q, kcache, vcache, None, k_new, v_new, nk, cu_seqlens_q, mask, int(max_nodes),
                 scale, workspace, out, lse)
 
 
@@ -590,7 +586,7 @@ def attn_tree_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     dev = _first(q, "q", 3)
     _first(k_pages, "k_pages", 4)
     _first(block_table, "block_table", 2)
-    return _run(dev, stream, _tree, dev, q, k_pages, v_pages, block_table, k_new, v_new, nk, cu_seqlens_q, mask,
+    return _run(_tree, dev, stream, q, k_pages, v_pages, block_table, k_new, v_new, nk, cu_seqlens_q, mask,
                 int(max_nodes), scale, workspace, out, lse)
 
 
@@ -599,7 +595,7 @@ def attn_tree_mask(parents: torch.Tensor, cu_seqlens_q: torch.Tensor, max_nodes:
     """Masks and positions of drafted trees. parents [total_q] int32 (index within the sequence, a root
     outside [0, i)) -> (mask [total_q, ceil(max_nodes / 64)] int64, positions [total_q] int32 = nk + depth)."""
     dev = _first(parents, "parents", 1)
-    return _run(dev, stream, _tree_mask, dev, parents, cu_seqlens_q, int(max_nodes), nk, mask, positions)
+    return _run(_tree_mask, dev, stream, parents, cu_seqlens_q, int(max_nodes), nk, mask, positions)
 
 
 def _tree_mask(st, dev, parents, cu, max_nodes, nk, mask, positions):
@@ -622,7 +618,7 @@ def kv_plan_paged(nk: torch.Tensor, n_new: torch.Tensor, block_table: torch.Tens
     cu_seqlens [B + 1], slots [num_tokens], free_count - pages taken), all int32. A negative last value:
     the stack was short by so many pages, nothing of the plan may be used."""
     dev = _first(block_table, "block_table", 2)
-    return _run(dev, stream, _plan, dev, nk, n_new, block_table, held, free_pages, free_count, int(page_size), int(num_tokens))
+    return _run(_plan, dev, stream, nk, n_new, block_table, held, free_pages, free_count, int(page_size), int(num_tokens))
 
 
 def _plan(st, dev, nk, n_new, table, held, free_pages, free_count, page_size, num_tokens):
@@ -675,7 +671,7 @@ def kv_append_paged(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tenso
     slots and rows out of range are skipped. Returns (k_pages, v_pages), written in place."""
     dev = _first(k_pages, "k_pages", 4)
     _first(k_new, "k_new", 3)
-    return _run(dev, stream, _append, dev, k_new, v_new, slots, k_pages, v_pages, None, None, rows, False)
+    return _run(_append, dev, stream, k_new, v_new, slots, k_pages, v_pages, None, None, rows, False)
 
 
 def kv_append_paged_fp8(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor, k_pages: torch.Tensor,
@@ -684,7 +680,7 @@ def kv_append_paged_fp8(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.T
     """``kv_append_paged`` into pages of E4M3 codes: code = nearest E4M3 value of x / scale[head, channel]."""
     dev = _first(k_pages, "k_pages", 4)
     _first(k_new, "k_new", 3)
-    return _run(dev, stream, _append, dev, k_new, v_new, slots, k_pages, v_pages, k_scale, v_scale, rows, True)
+    return _run(_append, dev, stream, k_new, v_new, slots, k_pages, v_pages, k_scale, v_scale, rows, True)
 
 
 def get_status(stream=None) -> int:
