@@ -143,13 +143,13 @@ constexpr int kTreeMergeBytes = 12288;
 // d = 64). 48 ragged requests at d = 64: 82.7 us at 3 and 4, 86.3 at 6 (before the hot loops were taken apart
 // 118 at 0); 30 ragged requests of two row tiles at d = 128: 82.6 us at 1, 78.0 at 2, 80.7 at 3.
 __host__ __device__ constexpr int tree_unit_cost(int d) { return d == 64 ? 4 : 2; }
-// What the merge has to do at the boundary between CTA c - 1 and CTA c, written by CTA c: something
-// if that is the first boundary inside a unit.
+// What the merge has to do at the boundary between a CTA and the one before it (of its KV head: head_group
+// CTAs before), written by the later: something if that is the first boundary inside a unit.
 struct TreeMergeRec {
   int rows0, rows1;      // rows of the unit's row tiles (rows0 0: nothing to merge)
   int node0, node_step;  // packed row of the tiles' first node: node0 + w node_step
   int hkv;
-  int slot0;             // CTA c - 1 has its part in this slot, the later CTAs in slot 0
+  int slot0;             // the CTA before has its part in this slot, the later ones in slot 0
   int last;              // the last CTA with a part
   int pad;
 };
