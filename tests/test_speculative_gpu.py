@@ -613,6 +613,16 @@ def test_merge_many_units_and_few():
         t.check(*t.run(), what=(Hq, Hkv, d, page))
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,page,nk,nodes", [
+    (16, 16, 128, 16, [300, 4000], [20, 3]), (12, 12, 64, 48, [2000, 0, 700], [9, 1, 30]), (64, 16, 256, 16, [100, 2500], [5, 7]),
+    (36, 9, 64, 16, [900, 33], [40, 2]), (26, 13, 128, 32, [640], [70]), (4, 1, 64, 0, [100, 7], [1024, 1000]),
+    (8, 2, 128, 16, [300], [1024])])
+def test_tree_heads_and_most_nodes(Hq, Hkv, d, page, nk, nodes):
+    # KV heads read side by side in groups of 8, 6, 8, 3 and one by one; and trees of the most nodes
+    c = Case(Hq, Hkv, d, page, nk, nodes, "any", seed=Hq + d)
+    c.check(*c.run(), what=(Hq, Hkv, d, page))
+
+
 # ------------------------------------------------------------------ together
 
 
@@ -806,3 +816,30 @@ def test_fork_and_join_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(o[:n], want[0]) and torch.equal(lse[:n], want[1])
         assert torch.equal(bits(t.k), bits(want[2]))
+
+
+def test_beside_prefill_and_decode_on_other_streams():
+    # three streams at once, each call over and over; the results are those of the calls alone
+    t = Case(32, 8, 128, 16, [3000, 40, 900], [64, 5, 20], "tree", seed=95)
+    small = Case(12, 4, 64, 0, [700, 90], [9, 3], "tree", seed=96)
+    g = gen(97)
+    q, k, v = (randn((2, 8, 1000, 128), g) for _ in range(3))
+    qd, kc, vc = randn((4, 32, 128), g), randn((4, 8, 2000, 128), g), randn((4, 8, 2000, 128), g)
+    nk = i32([2000, 1, 777, 1500])
+    calls = [lambda: t.run()[0][:sum(t.nodes)], lambda: small.run()[0][:sum(small.nodes)], lambda: bw.attn_fwd(q, k, v, causal=True)[0],
+             lambda: bw.attn_decode(qd, kc, vc, nk, num_splits=8)[0]]
+    want = []
+    for c in calls:
+        want.append(c())
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[] for _ in calls]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for s, c, x in zip(streams, calls, got):
+            with torch.cuda.stream(s):
+                x.append(c())
+    torch.cuda.synchronize()
+    for w, x in zip(want, got):
+        assert all(torch.equal(w, y) for y in x)
