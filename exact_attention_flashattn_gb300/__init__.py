@@ -630,7 +630,8 @@ def _plan(st, dev, nk, n_new, table, held, free_pages, free_count, page_size, nu
             _like(free_count, "free_count", dev, _I32))
     if free_count.numel() != 1:
         raise ValueError("free_count must be one value")
-    nk_out, held_out, free_out, cu, slots = [torch.empty(n, dtype=_I32, device=dev) for n in (B, B, free_count.shape, B + 1, num_tokens)]
+    nk_out, held_out, free_out, cu, slots = [torch.empty(n, dtype=_I32, device=dev)
+                                             for n in (B, B, free_count.shape, B + 1, num_tokens)]
     rc = (_lib or lib()).kv_plan_paged(*args, nk_out.data_ptr(), held_out.data_ptr(), cu.data_ptr(), slots.data_ptr(),
                                        free_out.data_ptr(), B, page_size, max_pages, free_pages.numel(), num_tokens, st)
     if rc:

@@ -303,7 +303,8 @@ __device__ __noinline__ MaskedTile masked_tile(uint32_t tS, uint32_t tP, int lef
 }
 
 template <int D, int kTiles>
-__global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCtasPerSm) tree_kernel(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCtasPerSm)
+    tree_kernel(const __grid_constant__ TreeArgs a) {
   using C = Cfg<D, kTiles>;
   constexpr int kStreams = C::kStreams, kKeys = C::kKeys, kStages = C::kStages, kVSlots = (kStages + 1) / 2;
   extern __shared__ uint8_t smem_raw[];
@@ -990,8 +991,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
 constexpr int kMergeWarps = 8;
 constexpr int kMergeQuads = 8;  // channels of a block, in fours
 constexpr uint32_t merge_smem(int warps) { return warps * (kMergeQuads * 33 * 16 + 32 * 8); }
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const float* partial, const TreeMergeRec* merge, uint16_t* out,
-                                                                       float* lse, int D, int quarters, int tiles, int g, int Hq, int head_group, int ctas) {
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    tree_merge_kernel(const float* partial, const TreeMergeRec* merge, uint16_t* out, float* lse, int D, int quarters, int tiles, int g,
+                      int Hq, int head_group, int ctas) {
   const int warps = blockDim.x / 32;
   extern __shared__ float4 sm_merge[];
   auto sm_o = reinterpret_cast<float4 (*)[kMergeQuads][33]>(sm_merge);  // 33: the joining threads' columns fall on different banks
