@@ -1,5 +1,7 @@
 // Paged KV cache bookkeeping on the GPU: ancestor masks of drafted token trees, block tables and
 // slot maps from request lengths, and K/V rows written into the pages (bf16 or E4M3 codes).
+#include <atomic>
+
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -221,19 +223,16 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
 // A copy of row_elems elements from row rows[i] (or i) of k_new and v_new to row slots[i] of the
 // pool; slots or rows outside their range are skipped. A thread moves 16 bytes of a row.
 //
-// A thread keeps its channels (kVec of them, 16 bytes of output) and takes rows a grid apart, kRows
-// at a time: their slots first, then their data, so that its loads overlap. With E4M3 pages the
-// reciprocals of the channels' scales stay in registers (reading and inverting the scales for every
-// element took 47 us on 20001 rows of 8 x 128, dividing each element exactly 36 us, a bracket around
-// each 22 us, 5.5 TB/s; without the check 20.5 us). The bytes bound the copy: 32768 rows of 8 x 128 in
-// 42 us, 6.4 TB/s.
+// A thread keeps its channels (kVec of them, 16 bytes of output) and takes rows a grid apart, kRows to a
+// batch. Slots are looked up two batches ahead and rows copied into shared memory one ahead, so the
+// memory is busy while a batch is converted and stored. With E4M3 pages the reciprocals of the channels'
+// scales stay in registers (reading and inverting the scales for every element took 47 us on 20001 rows of
+// 8 x 128, dividing each element exactly 36 us, a bracket around each, with the rows in registers, 23.3, as
+// here 21.9 us, 5.6 TB/s). The bytes bound the copy: 32768 rows of 8 x 128 in 40.9 us, 6.6 TB/s (rows in
+// registers 42.5).
 constexpr int kAppendThreads = 256;
-
-__device__ __forceinline__ uint4 load_once(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
+constexpr int append_rows(bool fp8) { return fp8 ? 4 : 2; }
+constexpr int append_smem(bool fp8) { return 2 * append_rows(fp8) * (fp8 ? 2 : 1) * kAppendThreads * 16; }
 
 // The E4M3 code nearest to x / s (ties to even, magnitudes past 448 to 448, NaN to NaN). Rounding is
 // monotonic, so where x r_lo and x r_hi, which bracket x / s, have the same code it is the quotient's:
@@ -273,48 +272,67 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
   wait_for_stream();
   constexpr int kVec = kFp8 ? 16 : 8;
   constexpr int kLoads = kVec / 8;
-  constexpr int kRows = kFp8 ? 6 : 4;
+  constexpr int kRows = append_rows(kFp8);
   const bool is_v = blockIdx.y == 1;
   const uint16_t* src = is_v ? a.v_new : a.k_new;
   uint8_t* dst = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages);
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
   const int per_row = a.row_elems / kVec;
-  const int me = blockIdx.x * kAppendThreads + threadIdx.x;
-  if (me >= threads) return;  // `threads` is a multiple of per_row
+  const int me = blockIdx.x * kAppendThreads + threadIdx.x, lane = threadIdx.x & 31;
+  if (me - lane >= threads) return;  // a warp without rows
+  const bool idle = me >= threads;   // `threads` is a multiple of per_row
   const int c = me % per_row, step = threads / per_row;
   const float* scale = (is_v ? a.v_scale : a.k_scale) + kVec * c;
-  struct Rows {
-    int slot[kRows];
-    uint4 u[kRows][kLoads];
+  // two halves of a ring in shared memory: [2][kRows][warps][kLoads x 32] pieces of 16 bytes. A warp copies its
+  // pieces in the order of their addresses (E4M3: a lane's two pieces are the copies of two other lanes; each
+  // lane copying its own, every sector crossed from L2 twice: 32 us)
+  extern __shared__ uint4 sm_rows[];
+  auto place = [&](int half, int r) { return sm_rows + ((half * kRows + r) * kAppendThreads + (threadIdx.x - lane)) * kLoads; };
+  struct Ids {
+    int slot[kRows], row[kRows];
   };
   const int64_t stride_i = static_cast<int64_t>(step) * kRows;
-  auto fetch = [&](Rows& w, int64_t i0) {
-    int row[kRows];
+  auto look_up = [&](Ids& d, int64_t i0) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int64_t i = i0 + static_cast<int64_t>(r) * step;
-      w.slot[r] = i < a.num_slots ? a.slots[i] : -1;
-      row[r] = static_cast<int>(i);
-      if (a.rows) row[r] = i < a.num_slots ? a.rows[i] : -1;
-      if (w.slot[r] >= a.pool_rows || row[r] < 0 || row[r] >= a.num_rows) w.slot[r] = -1;
+      const bool is = i < a.num_slots && !idle;
+      d.slot[r] = is ? a.slots[i] : -1;
+      d.row[r] = static_cast<int>(i);
+      if (a.rows) d.row[r] = is ? a.rows[i] : -1;
     }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-      if (w.slot[r] >= 0)
-#pragma unroll
-        for (int q = 0; q < kLoads; ++q) w.u[r][q] = load_once(src + row[r] * stride + kVec * c + 8 * q);
   };
-  Bracket inv[kVec];
-  auto store = [&](const Rows& w) {
+  auto fetch = [&](Ids& d, int half) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      if (w.slot[r] < 0) continue;
-      const int64_t at = static_cast<int64_t>(w.slot[r]) * a.row_elems + kVec * c;
+      if (d.slot[r] >= a.pool_rows || d.row[r] < 0 || d.row[r] >= a.num_rows) d.slot[r] = -1;
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) {
+        const int owner = kLoads == 1 ? lane : 16 * q + lane / 2, part = kLoads == 1 ? 0 : lane & 1;
+        const int row = __shfl_sync(0xffffffffu, d.slot[r] >= 0 ? d.row[r] : -1, owner);
+        const int col = (me - lane + owner) % per_row * kVec + 8 * part;
+        if (row >= 0)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(place(half, r) + 32 * q + lane)),
+                       "l"(src + row * stride + col)
+                       : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  Bracket inv[kVec];
+  auto store = [&](const Ids& d, int half) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (d.slot[r] < 0) continue;
+      const int64_t at = static_cast<int64_t>(d.slot[r]) * a.row_elems + kVec * c;
+      uint4 u[kLoads];
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) u[q] = place(half, r)[lane * kLoads + q];
       if constexpr (kFp8) {
         float x[kVec];
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-          const uint4& w4 = w.u[r][e / 8];
+          const uint4& w4 = u[e / 8];
           const uint32_t h = (e / 2) % 4 == 0 ? w4.x : (e / 2) % 4 == 1 ? w4.y : (e / 2) % 4 == 2 ? w4.z : w4.w;
           x[e] = __uint_as_float(e % 2 ? h & 0xffff0000u : h << 16);
         }
@@ -334,13 +352,15 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
         }
         *reinterpret_cast<uint4*>(dst + at) = make_uint4(code[0], code[1], code[2], code[3]);
       } else {
-        *reinterpret_cast<uint4*>(dst + 2 * at) = w.u[r][0];
+        *reinterpret_cast<uint4*>(dst + 2 * at) = u[0];
       }
     }
   };
   int64_t i0 = me / per_row;
-  Rows w;
-  fetch(w, i0);
+  Ids now, next;
+  look_up(now, i0);
+  look_up(next, i0 + stride_i);
+  fetch(now, 0);
   if constexpr (kFp8) {
 #pragma unroll
     for (int e = 0; e < kVec; e += 4) {
@@ -348,11 +368,21 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
       inv[e] = bracket(v.x), inv[e + 1] = bracket(v.y), inv[e + 2] = bracket(v.z), inv[e + 3] = bracket(v.w);
     }
   }
-  for (;;) {
-    store(w);
-    if ((i0 += stride_i) >= a.num_slots) break;
-    fetch(w, i0);
+  // a batch's slots are looked up two batches ahead and its rows copied one ahead
+#pragma unroll 1
+  for (int half = 0;; half ^= 1) {
+    Ids after;
+    look_up(after, i0 + 2 * stride_i);
+    fetch(next, half ^ 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
+    store(now, half);
+    i0 += stride_i;
+    if (__all_sync(0xffffffffu, i0 >= a.num_slots)) break;
+    now = next;
+    next = after;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 }  // namespace
@@ -381,15 +411,25 @@ cudaError_t launch_kv_plan(const PlanArgs& a, cudaStream_t stream) {
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
   const int per_row = a.row_elems / (a.k_scale ? 16 : 8);
   // E4M3: one block an SM for each of K and V, as a thread inverts 16 scales before its rows (20001 rows
-  // of 8 x 128: 23.1 us, four blocks 29.9); a copy has nothing to set up and 32 even out the SMs (32768
-  // rows: 41.9 us, eight 42.5). In whole rows, no more than there are rows.
+  // of 8 x 128: 21.9 us, two blocks 24.4); a copy has nothing to set up and 32 even out the SMs (32768
+  // rows: 40.9 us, 16 41.5). In whole rows, no more than there are rows.
   const int64_t most = static_cast<int64_t>(a.num_slots) * per_row;
   int64_t threads = 152 * (a.k_scale ? 1 : 32) * kAppendThreads / per_row * per_row;
   if (threads == 0) threads = per_row;
   if (threads > most) threads = most;
   const dim3 grid(static_cast<unsigned>((threads + kAppendThreads - 1) / kAppendThreads), 2);
-  return launch_dependent(a.k_scale ? kv_append_kernel<true> : kv_append_kernel<false>, grid, kAppendThreads, 0, stream, a,
-                          static_cast<int>(threads));
+  if (!a.k_scale)
+    return launch_dependent(kv_append_kernel<false>, grid, kAppendThreads, append_smem(false), stream, a, static_cast<int>(threads));
+  // more than 48 KB of shared memory is asked for once per device
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev >= 64 || !(set.load() >> dev & 1))) {
+    e = cudaFuncSetAttribute(kv_append_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, append_smem(true));
+    if (e == cudaSuccess && dev < 64) set.fetch_or(1ull << dev);
+  }
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kv_append_kernel<true>, grid, kAppendThreads, append_smem(true), stream, a, static_cast<int>(threads));
 }
 
 }  // namespace bw
