@@ -9,13 +9,12 @@ namespace bw {
 
 namespace {
 
-// The first statement of every kernel here: the next one in the stream may be set up from now on, and what
-// the stream did before is complete and visible behind it. (Without this, a kernel behind another starts
-// some 2.5 us later: 32768 rows of 8 x 128 appended again and again 44.4 us a call, with it 41.8.)
-__device__ __forceinline__ void wait_for_stream() {
-  asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
+// The first statement of every kernel here, a dependent launch: what the stream did before is complete and
+// visible behind it. (Launched the ordinary way, a kernel behind another starts some 2.5 us later: 32768
+// rows of 8 x 128 appended again and again 44.4 us a call, so 41.8.) The next kernel is set up when this
+// one's blocks end, not when they start: a tree attention's CTAs that came in between them were spread over
+// the SMs in another order, two with the same work on one, and took 84 to 89 us for 48 ragged requests.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---------------------------------------------------------------- tree masks
 //
