@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       mbar_init(&bar->mma_done[i], 1);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&bar->kv_full[i], 1);
+      mbar_init(&bar->kv_full[i], a.block_table ? 1 + C::kHelpers : 1);  // everyone who loads into the slot
       mbar_init(&bar->kv_empty[i], kTiles);  // one commit per stream that reads the slot
       mbar_init(&bar->v_ready[i], 1);
     }
@@ -435,7 +435,11 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   // to issue, and a tile out of 16-row pages is 8 to 16 such copies of K and as many of V, so a helper warp
   // takes a third of both (one warp for K and V held the paged d = 128 cache at 4400 GB/s where a contiguous
   // one ran at 6270). The K and V producers (member 0) announce a tile's bytes; the helper's copies (member
-  // 1) may land before that, but the phase waits for the announcement.
+  // 1) may land before that, but the phase waits for the announcement. The helper arrives for every tile, those
+  // that hold none of its copies too (drafts, pages of 128 rows, short tails): the ring cannot run on past a load
+  // that the helper has not reached, so its waits for slots always mean the use they are for. (Waiting by parity
+  // without arriving, two uses behind it took a free slot for a taken one, and its wait ran out at the list's
+  // end.)
   auto load_tiles = [&](const Seg& s, int kv0, int kv1, int member, int& n, auto before_tile) -> bool {
     const int nctx = min(max(s.ct - s.k0, 0), s.nt);
     int j = 0;
@@ -471,6 +475,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             tma_load_3d_lane(sRing + slot * C::kTileBytes + hfl * (kKeys * 128) + my_piece * 128, kv ? &a.tm_v : &a.tm_k,
                              &bar->kv_full[slot], 64 * hfl, s.hkv, row);
           __syncwarp();
+          if (member > 0 && lane == 0) mbar_arrive(&bar->kv_full[slot]);
         }
       }
     } else {
@@ -491,7 +496,11 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       for (int kv = kv0; kv < kv1; ++kv) {
         const int i = 2 * n + kv, slot = i % kStages;
         if (!wait_slot(i)) return false;
-        if (member > 0) continue;  // drafts are the producers' alone; the helper keeps step
+        if (member > 0) {  // drafts are the producers' alone
+          if (lane == 0) mbar_arrive(&bar->kv_full[slot]);
+          __syncwarp();
+          continue;
+        }
         mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(a.new_box) * 128 * C::kHalves);
         for (int hf = 0; hf < C::kHalves; ++hf)
           tma_load_3d(sRing + slot * C::kTileBytes + hf * (kKeys * 128), kv ? &a.tm_vn : &a.tm_kn, &bar->kv_full[slot], 64 * hf,
@@ -500,10 +509,11 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     }
     return true;
   };
-  // the copies a producer warp issued last, of n tiles in all, have landed: those whose slot no later tile took
+  // the copies a producer warp issued last, of n tiles in all, have landed: those whose slot no later tile took.
+  // Where another warp gave up, a slot's phase may never end: the wait that runs out has been the others' time too
   auto drain = [&](int kv, int n) {
     for (int i = 2 * n - 1; i >= max(0, 2 * n - kStages); --i) {
-      if ((i & 1) == kv) mbar_wait(&bar->kv_full[i % kStages], (i / kStages) & 1, tmo, &no_abort);
+      if ((i & 1) == kv && !mbar_wait(&bar->kv_full[i % kStages], (i / kStages) & 1, tmo, &no_abort)) return;
     }
   };
 

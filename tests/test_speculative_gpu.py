@@ -843,3 +843,20 @@ def test_beside_prefill_and_decode_on_other_streams():
     torch.cuda.synchronize()
     for w, x in zip(want, got):
         assert all(torch.equal(w, y) for y in x)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,page", [(8, 4, 128, 128), (8, 8, 64, 64), (6, 3, 64, 128), (4, 2, 256, 64), (8, 8, 128, 16), (8, 8, 64, 16)])
+def test_tree_tiles_without_copies_for_the_helper(Hq, Hkv, d, page):
+    # one row tile over pages: pages so large that the helping producer warp has no copy, contexts so short that
+    # it has some in few tiles, and drafts, which it never copies, one after another in every CTA's list
+    r = np.random.default_rng(d + page)
+    nk = [int(x) for x in r.choice([0, 1, 15, 17, 33, 100, 130, 2000], 300)]
+    n = [int(x) for x in r.integers(1, 9, 300)]
+    c = Case(Hq, Hkv, d, page, nk, n, "tree", seed=101)
+    o, lse = c.run()
+    c.check(o, lse)
+    want = o[:sum(n)].clone()
+    for _ in range(200):
+        c.run(out=o)
+    assert torch.equal(o[:sum(n)], want)
+    assert bw.get_status() == bw.OK  # no wait ran out
