@@ -464,7 +464,11 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         row_next = pool_row(kt + 1);
         for (int kv = kv0; kv < kv1; ++kv) {
           const int i = 2 * n + kv, slot = i % kStages;
-          if (!wait_slot(i)) return false;
+          if (!wait_slot(i)) {
+            // drain() does not know of the K of this tile that went out just before
+            if (kv > kv0) mbar_wait(&bar->kv_full[(i - 1) % kStages], ((i - 1) / kStages) & 1, tmo, &no_abort);
+            return false;
+          }
           if (member == 0) {
             // pieces past the last key are not copied: their K scores are masked, their V rows zeroed
             const int pieces = min(kKeys / a.piece, (s.nk - kt * kKeys + a.piece - 1) / a.piece);
