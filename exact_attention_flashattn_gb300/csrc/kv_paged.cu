@@ -26,6 +26,7 @@ __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol
 // thread per node, masks and links in shared memory; the new values are read before a barrier and
 // written behind it.
 constexpr int kMaskMaxNodes = kTreeMaxNodes;
+constexpr int mask_smem(int threads, int words) { return threads * (8 * words + 2); }
 
 template <int kWords>  // at least the call's words
 __global__ void __launch_bounds__(kMaskMaxNodes) tree_mask_kernel(const TreeMaskArgs a) {
@@ -384,22 +385,34 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// More than 48 KB of shared memory is asked for once per device (`set`: a bit each), and then the most that any
+// call takes: the limit belongs to the kernel, and a call's own size would lower it between another call's
+// setting and its launch.
+template <typename K>
+cudaError_t allow_smem(K kernel, int most, std::atomic<uint64_t>& set) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev >= 64 || !(set.load() >> dev & 1))) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess && dev < 64) set.fetch_or(1ull << dev);
+  }
+  return e;
+}
+
 }  // namespace
 
 cudaError_t launch_tree_mask(const TreeMaskArgs& a, cudaStream_t stream) {
   const int threads = (a.max_nodes + 31) / 32 * 32;
   auto go = [&](auto kernel, int words) {
-    const size_t smem = static_cast<size_t>(threads) * (words * sizeof(uint64_t) + sizeof(int16_t));
-    if (smem > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-      if (e != cudaSuccess) return e;
-    }
-    return launch_dependent(kernel, dim3(a.num_seqs), threads, smem, stream, a);
+    return launch_dependent(kernel, dim3(a.num_seqs), threads, mask_smem(threads, words), stream, a);
   };
   if (a.words == 1) return go(tree_mask_kernel<1>, 1);
   if (a.words == 2) return go(tree_mask_kernel<2>, 2);
+  static_assert(mask_smem(256, 4) <= 48 * 1024, "without allow_smem");
   if (a.words <= 4) return go(tree_mask_kernel<4>, 4);
-  return go(tree_mask_kernel<16>, 16);
+  static std::atomic<uint64_t> set{0};
+  const cudaError_t e = allow_smem(tree_mask_kernel<16>, mask_smem(kMaskMaxNodes, 16), set);
+  return e == cudaSuccess ? go(tree_mask_kernel<16>, 16) : e;
 }
 
 cudaError_t launch_kv_plan(const PlanArgs& a, cudaStream_t stream) {
@@ -419,14 +432,8 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((threads + kAppendThreads - 1) / kAppendThreads), 2);
   if (!a.k_scale)
     return launch_dependent(kv_append_kernel<false>, grid, kAppendThreads, append_smem(false), stream, a, static_cast<int>(threads));
-  // more than 48 KB of shared memory is asked for once per device
   static std::atomic<uint64_t> set{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && (dev >= 64 || !(set.load() >> dev & 1))) {
-    e = cudaFuncSetAttribute(kv_append_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, append_smem(true));
-    if (e == cudaSuccess && dev < 64) set.fetch_or(1ull << dev);
-  }
+  const cudaError_t e = allow_smem(kv_append_kernel<true>, append_smem(true), set);
   if (e != cudaSuccess) return e;
   return launch_dependent(kv_append_kernel<true>, grid, kAppendThreads, append_smem(true), stream, a, static_cast<int>(threads));
 }

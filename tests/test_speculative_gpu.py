@@ -10,6 +10,7 @@ relative). With A = sum_j p_j |v_j| / l of the element and E the largest error o
 * LSE: E, the sum of n weights in fp32 (n 2^-24), and 2^-21 (1 + |LSE|) for its logarithm and products.
 """
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -860,3 +861,32 @@ def test_tree_tiles_without_copies_for_the_helper(Hq, Hkv, d, page):
         c.run(out=o)
     assert torch.equal(o[:sum(n)], want)
     assert bw.get_status() == bw.OK  # no wait ran out
+
+
+def test_mask_calls_of_several_threads():
+    # each takes another amount of shared memory; the C calls run side by side
+    call, sizes = bw.lib().attn_tree_mask, (1024, 400, 900, 513)
+    start, codes = threading.Barrier(len(sizes)), [set() for _ in sizes]
+    masks, keep, threads = [], [], []
+
+    def work(i, args):
+        start.wait()
+        for _ in range(20000):
+            codes[i].add(call(*args))
+
+    for i, n in enumerate(sizes):
+        parents, cu, stream = i32(range(-1, n - 1)), sums([n]), torch.cuda.Stream()  # one line
+        masks.append(torch.zeros((n, (n + 63) // 64), dtype=torch.int64, device="cuda"))
+        keep.append((parents, cu, stream))
+        args = (parents.data_ptr(), cu.data_ptr(), None, masks[i].data_ptr(), None, 1, n, n, stream.cuda_stream)
+        args = [x if x is None else t(x) for x, t in zip(args, call.argtypes)]
+        threads.append(threading.Thread(target=work, args=(i, args)))
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [{bw.OK}] * len(sizes)
+    for n, m in zip(sizes, masks):
+        assert np.array_equal(m.cpu().numpy(), pack(np.tril(np.ones((n, n), bool)), m.shape[1]))
