@@ -377,6 +377,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncwarp();
     store(now, half);
+    __syncwarp();  // the next turn's copies go over what other lanes have just read
     i0 += stride_i;
     if (__all_sync(0xffffffffu, i0 >= a.num_slots)) break;
     now = next;

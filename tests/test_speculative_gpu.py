@@ -890,3 +890,48 @@ def test_mask_calls_of_several_threads():
     assert codes == [{bw.OK}] * len(sizes)
     for n, m in zip(sizes, masks):
         assert np.array_equal(m.cpu().numpy(), pack(np.tril(np.ones((n, n), bool)), m.shape[1]))
+
+
+def codes_on_gpu(x, scale):
+    """``codes_of`` for many values: the same comparisons, on the GPU."""
+    val = e4m3_values()
+    ax, s = x.double().abs(), scale.double()
+    code = torch.zeros(x.shape, dtype=torch.uint8, device="cuda")
+    for c in range(126):
+        border = (val[c] + val[c + 1]) / 2 * s
+        code += (ax >= border) if c % 2 == 1 else (ax > border)
+    return code | torch.signbit(x).to(torch.uint8) << 7
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Hkv,d,batches,more", [(64, 256, 1, 0), (64, 256, 2, 1), (64, 256, 5, 77), (8, 128, 3, 1001), (3, 64, 4, 13)])
+@pytest.mark.parametrize("how", ["plain", "fused", "gather"])
+def test_append_batch_after_batch(fp8, Hkv, d, batches, more, how):
+    # every thread goes through several batches of rows, the last of them partly filled: a batch is at most
+    # 152 SMs x blocks x 256 threads of 16 output bytes, times its rows
+    batch = 152 * 256 * (4 * 16 if fp8 else 32 * 2 * 8) // (Hkv * d)
+    n, page = batches * batch + more, 16
+    g = gen(n + d)
+    rows_in = n + 50
+    if how == "fused":
+        x = randn((rows_in, 2 + 2 * Hkv, d), g, 3.0)
+        k_new, v_new = x[:, 2:2 + Hkv], x[:, 2 + Hkv:]
+    else:
+        k_new, v_new = randn((rows_in, Hkv, d), g, 3.0), randn((rows_in, Hkv, d), g, 3.0)
+    pages = n // page + 3
+    slots = torch.randperm(pages * page, generator=g, device="cuda")[:n].to(torch.int32)
+    slots[torch.rand(n, generator=g, device="cuda") < 0.05] = -1
+    rows = torch.randint(-20, rows_in + 20, (n,), generator=g, device="cuda").to(torch.int32) if how == "gather" else None
+    src = torch.arange(n, device="cuda") if rows is None else rows.long()
+    ok = (slots >= 0) & (src >= 0) & (src < rows_in)
+    ks, vs = (torch.rand((Hkv, d), generator=g, device="cuda") * 0.02 + 1e-3 for _ in range(2))
+    kp, vp = (torch.full((pages, page, Hkv, d), 7, dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda") for _ in range(2))
+    if fp8:
+        bw.kv_append_paged_fp8(k_new, v_new, slots, kp, vp, ks, vs, rows=rows)
+    else:
+        bw.kv_append_paged(k_new, v_new, slots, kp, vp, rows=rows)
+    for p, new, s in ((kp, k_new, ks), (vp, v_new, vs)):
+        want = torch.full_like(p, 7).view(-1, Hkv, d)
+        r = new[src[ok]]
+        want[slots[ok].long()] = codes_on_gpu(r, s) if fp8 else r
+        assert torch.equal(p.view(-1, Hkv, d), want)
