@@ -121,9 +121,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs a)
 #pragma unroll
     for (int r = 0; r < kPlanRun; ++r) {
       const int64_t keys = static_cast<int64_t>(nk[r]) + add[r];
-      const int want = keys < static_cast<int64_t>(a.max_pages) * a.page_size
-                           ? (static_cast<int>(keys) + a.page_size - 1) / a.page_size
-                           : a.max_pages;
+      const int k32 = static_cast<int>(keys);  // rounded up without a sum that could pass 32 bits
+      const int want = keys < static_cast<int64_t>(a.max_pages) * a.page_size ? k32 / a.page_size + (k32 % a.page_size != 0)
+                                                                              : a.max_pages;
       need[r] = b0 + tid * kPlanRun + r < a.B ? max(want - held[r], 0) : 0;
       tok += add[r];
       page += need[r];

@@ -935,3 +935,12 @@ def test_append_batch_after_batch(fp8, Hkv, d, batches, more, how):
         r = new[src[ok]]
         want[slots[ok].long()] = codes_on_gpu(r, s) if fp8 else r
         assert torch.equal(p.view(-1, Hkv, d), want)
+
+
+def test_plan_keys_near_the_end_of_32_bits():
+    # the widest table of 48-row pages; the last pages of a request that fills it to within some keys
+    P = 48
+    columns = 0x7fffffff // P
+    table = np.full((1, columns), -1, np.int32)
+    for left in (5, 0, -20):  # keys to the table's end
+        plan_check([P * columns - left - 45], [45], table, [columns - 2], [5, 6, 7], 3, P, 50)
