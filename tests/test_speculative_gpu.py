@@ -944,3 +944,39 @@ def test_plan_keys_near_the_end_of_32_bits():
     table = np.full((1, columns), -1, np.int32)
     for left in (5, 0, -20):  # keys to the table's end
         plan_check([P * columns - left - 45], [45], table, [columns - 2], [5, 6, 7], 3, P, 50)
+
+
+@pytest.mark.parametrize("B,P,most", [(2047, 16, 5), (2048, 48, 3), (2049, 16, 4), (4096, 16, 2), (5000, 16, 40), (9000, 128, 30)])
+def test_plan_of_more_requests_than_a_scan(B, P, most):
+    # requests are scanned 2048 at a time: what is carried from scan to scan, a stack and slots that run out
+    # behind the first, and (5000 and 9000 requests) the scans' outputs by several blocks
+    r = np.random.default_rng(B)
+    nk = r.integers(0, 200, B)
+    new = r.integers(0, most + 1, B)
+    new[r.integers(0, B, 3)] = 300
+    held = np.maximum(-(-nk // P) + r.integers(-1, 3, B), 0)
+    need = np.maximum(0, -(-(nk + new) // P) - held)
+    columns = int((held + need).max())
+    pages = r.permutation(int(held.sum() + need.sum()) + 9).astype(np.int32)
+    table = np.full((B, columns), -1, np.int32)
+    inside = np.arange(columns)[None] < held[:, None]
+    table[inside] = pages[:held.sum()]
+    free, tokens = pages[held.sum():].tolist(), int(new.sum())
+    behind = min(B - 1, 2048 + B // 7)  # a request of a later scan, where there is one
+    for count, slots in ((len(free), tokens + 30), (int(need[:behind].sum()), tokens), (len(free), int(new[:behind].sum()) + 1), (0, 17)):
+        plan_check(nk.tolist(), new.tolist(), table, held.tolist(), free, count, P, slots)
+
+
+def test_plan_of_more_tokens_than_threads():
+    # above 152 x 1024 tokens a thread takes several, in several scans
+    r = np.random.default_rng(8)
+    B, P = 2100, 64
+    nk, new = r.integers(0, 100, B), r.integers(0, 200, B)
+    held = -(-nk // P)
+    need = np.maximum(0, -(-(nk + new) // P) - held)
+    tokens = int(new.sum())
+    assert int(new[:2048].sum()) > 152 * 1024
+    table = np.full((B, 8), -1, np.int32)
+    table[np.arange(8)[None] < held[:, None]] = np.arange(held.sum())
+    free = np.arange(held.sum(), (held + need).sum()).tolist()
+    plan_check(nk.tolist(), new.tolist(), table, held.tolist(), free, len(free), P, tokens + 5)
