@@ -20,6 +20,12 @@ bool page_sizes(int page_size, int num_pages) {
   return page_size >= 16 && page_size <= 1024 && page_size % 16 == 0 && num_pages > 0 &&
          static_cast<int64_t>(num_pages) * page_size <= 0x7fffffff;
 }
+// what the tree calls take, and the size of their workspace is given for: sizes in range (else INVALID_ARG) ...
+bool tree_range(int num_seqs, int max_nodes, int Hq, int Hkv, int d) {
+  return num_seqs >= 0 && num_seqs <= 65535 && max_nodes >= 0 && Hq > 0 && Hq <= 65535 && Hkv > 0 && d > 0 && Hq % Hkv == 0;
+}
+// ... that the kernels implement (else UNSUPPORTED)
+bool tree_supported(int max_nodes, int g, int d) { return head_dim(d) && g <= bw::kTreeRows && max_nodes <= bw::kTreeMaxNodes; }
 
 int done(cudaError_t e) {
   if (e != cudaSuccess) {
@@ -34,12 +40,10 @@ int tree_impl(const void* q, const void* k, const void* v, const void* k_new, co
               int num_seqs, int total_q, int max_nodes, int kv_cap, int page_size, int num_pages, int max_pages,
               int Hq, int Hkv, int d, int64_t q_stride, int64_t k_new_stride, int64_t v_new_stride, float scale,
               void* workspace, size_t workspace_bytes, void* stream) {
-  if (num_seqs < 0 || total_q < 0 || max_nodes < 0 || kv_cap < 0 || Hq <= 0 || Hkv <= 0 || d <= 0)
-    return BWATTN_ERR_INVALID_ARG;
-  if (Hq % Hkv != 0 || !(isfinite(scale) && scale > 0.f) || num_seqs > 65535 || Hq > 65535)
+  if (!tree_range(num_seqs, max_nodes, Hq, Hkv, d) || total_q < 0 || kv_cap < 0 || !(isfinite(scale) && scale > 0.f))
     return BWATTN_ERR_INVALID_ARG;
   const int g = Hq / Hkv;
-  if (!head_dim(d) || g > bw::kTreeRows || max_nodes > bw::kTreeMaxNodes) return BWATTN_ERR_UNSUPPORTED;
+  if (!tree_supported(max_nodes, g, d)) return BWATTN_ERR_UNSUPPORTED;
   if (num_seqs == 0 || total_q == 0 || max_nodes == 0) return BWATTN_OK;
   if (!good(q, 16) || !good(k_new, 16) || !good(v_new, 16) || !good(o, 16) || !good_or_null(lse, 4) || !good(nk, 4) ||
       !good(cu_seqlens_q, 4) || !good(mask, 8) || !good(workspace, 16))
@@ -120,7 +124,8 @@ int append_impl(const void* k_new, const void* v_new, const int32_t* slots, cons
 extern "C" {
 
 size_t attn_tree_workspace_size(int num_seqs, int max_nodes, int Hq, int Hkv, int d) {
-  if (num_seqs <= 0 || max_nodes <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || !head_dim(d)) return 0;
+  if (!tree_range(num_seqs, max_nodes, Hq, Hkv, d) || !tree_supported(max_nodes, Hq / Hkv, d) || num_seqs == 0 || max_nodes == 0)
+    return 0;
   return bw::tree_ws_bytes(max_nodes, Hq / Hkv, d);
 }
 

@@ -118,3 +118,15 @@ def test_python_checks():
         bw.kv_plan_paged(t, t, t[None], t, t, t[:1], 16, 4)
     with pytest.raises(ValueError):
         bw.kv_append_paged(new, new, t, c, c)
+
+
+def test_tree_workspace_size_of_refused_sizes(L):
+    # 0 for every size that the calls refuse, at the limits' two sides
+    f = L.attn_tree_workspace_size
+    for n, mn, Hq, Hkv, d in ((2, 1025, 8, 2, 128), (2, 8, 258, 2, 128), (2, 8, 129, 1, 64), (65536, 8, 8, 2, 128), (2, 8, 65536, 8192, 64),
+                              (2, 8, 8, 2, 512), (-1, 8, 8, 2, 64), (2, -1, 8, 2, 64), (2, 8, 0, 2, 64), (2, 8, 8, 0, 64)):
+        assert f(n, mn, Hq, Hkv, d) == 0, (n, mn, Hq, Hkv, d)
+        if min(Hq, Hkv) > 0:
+            assert tree(L, n=n, mn=mn, Hq=Hq, Hkv=Hkv, d=d, qs=Hq * d, ks=Hkv * d, vs=Hkv * d) in (bw.ERR_INVALID_ARG, bw.ERR_UNSUPPORTED)
+    for n, mn, Hq, Hkv, d in ((2, 1024, 8, 2, 128), (2, 8, 256, 2, 128), (65535, 8, 8, 2, 128), (2, 8, 65520, 8190, 64)):
+        assert f(n, mn, Hq, Hkv, d) > 0, (n, mn, Hq, Hkv, d)
