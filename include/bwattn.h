@@ -392,7 +392,8 @@ int kv_plan_paged(const int32_t* nk, const int32_t* n_new, int32_t* block_table,
  *                  E4M3 code nearest to x / scale (ties to the even code; magnitudes past 448, infinities
  *                  among them, become +-448; NaN stays NaN)
  * Slots must differ from one another: of two slots with one value, which row stays is not defined (and
- * may differ within the row). Supported: d in {64, 128, 256}. num_slots = 0 or num_rows = 0 is a no-op.
+ * may differ within the row). k_new and v_new may be rows of the pools themselves if no row that is read
+ * is also written. Supported: d in {64, 128, 256}. num_slots = 0 or num_rows = 0 is a no-op.
  */
 int kv_append_paged(const void* k_new, const void* v_new, const int32_t* slots, const int32_t* rows, void* k_pages,
                     void* v_pages, int num_slots, int num_rows, int page_size, int num_pages, int Hkv, int d,

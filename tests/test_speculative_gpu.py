@@ -980,3 +980,151 @@ def test_plan_of_more_tokens_than_threads():
     table[np.arange(8)[None] < held[:, None]] = np.arange(held.sum())
     free = np.arange(held.sum(), (held + need).sum()).tolist()
     plan_check(nk.tolist(), new.tolist(), table, held.tolist(), free, len(free), P, tokens + 5)
+
+
+def test_tree_without_a_cache():
+    # a cache of no rows (its pointers may be null), whatever the lengths say
+    c = Case(8, 2, 128, 0, [0, 0, 0], [9, 0, 150], "any", seed=111)
+    c.k = c.v = torch.empty((3, 2, 0, 128), dtype=torch.bfloat16, device="cuda")
+    c.nk_t = i32([0, 5, 1 << 30])
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 0), (256, 16)])
+def test_tree_without_nodes(d, page):
+    c = Case(8, 2, d, page, [300, 40], [0, 0], seed=113, bound=40)  # rows, but none of a sequence
+    o = torch.full((c.total, 8, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((c.total, 8), 7.0, device="cuda")
+    c.run(out=o, lse=lse)
+    assert bool((o == 7).all()) and bool((lse == 7).all())
+
+
+def test_tree_cache_past_32_bits():
+    # contiguous caches whose later sequences' elements lie past 2^32
+    B, Hkv, cap, d = 3, 4, 4_500_000, 128
+    c = Case(8, Hkv, d, 0, [200, 0, 333], [10, 2, 40], "tree", seed=115)
+    k, v = (torch.empty((B, Hkv, cap, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert k[:2].numel() > 1 << 32
+    for b, n in enumerate(c.nk):
+        k[b, :, :n], v[b, :, :n] = (x.transpose(0, 1) for x in c.ctx[b])
+    c.k, c.v = k, v
+    c.check(*c.run())
+
+
+def test_tree_most_sequences():
+    # 65535 requests of one node, and as many heads as a call of one request may have
+    B, d, most = 65535, 64, 20
+    g = gen(117)
+    nk = torch.randint(0, most + 1, (B,), generator=g, device="cuda").to(torch.int32)
+    q, k_new, v_new = randn((B, 2, d), g, 2.0), randn((B, 1, d), g), randn((B, 1, d), g)
+    k, v = randn((B, 1, most, d), g), randn((B, 1, most, d), g)
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    mask = torch.ones((B, 1), dtype=torch.int64, device="cuda")
+    o, lse = bw.attn_tree(q, k, v, k_new, v_new, nk, cu, mask, 1)
+    kk, vv = (torch.cat([x[:, 0], y], 1).double() for x, y in ((k, k_new), (v, v_new)))
+    see = torch.arange(most + 1, device="cuda")[None] < nk[:, None]
+    see[:, most] = True
+    s = (q.double() @ kk.transpose(1, 2) / math.sqrt(d)).masked_fill(~see[:, None], -INF)
+    p = torch.softmax(s, -1)
+    E = (d + 8) * 2.0 ** -24 * (q.double().abs() @ kk.abs().transpose(1, 2) / math.sqrt(d)).amax(-1)
+    ref, A = p @ vv, p @ vv.abs()
+    dO = (2.0 ** -8 + 4 * E)[..., None] * A
+    assert bool(((o.double() - ref).abs() <= dO + 2.0 ** -8 * (ref.abs() + dO) + 1e-30).all())
+    z = torch.logsumexp(s, -1)
+    assert bool(((lse.double() - z).abs() <= E + 21 * 2.0 ** -24 + 2.0 ** -21 * (1 + z.abs())).all())
+    c = Case(2048, 512, 64, 16, [70], [3], "tree", seed=118)
+    c.check(*c.run())
+
+
+def test_append_rows_of_the_pool():
+    # rows moved within the pool: none of those read is written
+    g = gen(119)
+    pages, page, Hkv, d = 40, 16, 2, 128
+    kp, vp = randn((pages, page, Hkv, d), g), randn((pages, page, Hkv, d), g)
+    order = torch.randperm(pages * page, generator=g, device="cuda").to(torch.int32)
+    rows, slots = order[:300].contiguous(), order[300:600].contiguous()
+    want = []
+    for p in (kp, vp):
+        w = p.clone().view(-1, Hkv, d)
+        w[slots.long()] = w[rows.long()]
+        want.append(w.view_as(p))
+    bw.kv_append_paged(kp.view(-1, Hkv, d), vp.view(-1, Hkv, d), slots, kp, vp, rows=rows)
+    assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
+
+
+def test_append_to_pages_of_a_float8_type():
+    g = gen(121)
+    k_new, v_new = randn((50, 2, 64), g), randn((50, 2, 64), g)
+    ks, vs = (torch.rand((2, 64), generator=g, device="cuda") * 0.02 + 1e-3 for _ in range(2))
+    kp, vp = (torch.zeros((4, 16, 2, 64), dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+    slots = torch.randperm(64, generator=g, device="cuda")[:50].to(torch.int32)
+    bw.kv_append_paged_fp8(k_new, v_new, slots, kp, vp, ks, vs)
+    for p, x, s in ((kp, k_new, ks), (vp, v_new, vs)):
+        assert torch.equal(p.view(torch.uint8).view(-1, 2, 64)[slots.long()], codes_of(x, s))
+
+
+def test_tree_captured_without_a_workspace():
+    # what a captured call allocates lives in the graph's memory, and two graphs replayed at once have their own
+    cases = [Case(16, 4, 128, 16, [3000, 5], [20, 9], "tree", seed=123), Case(16, 4, 128, 16, [40, 2500], [7, 30], "any", seed=124)]
+    want = [c.run() for c in cases]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c.run())
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(30):
+        for g, s, (o, l) in zip(graphs, streams, outs):
+            with torch.cuda.stream(s):
+                o.zero_(), l.zero_()
+                g.replay()
+    torch.cuda.synchronize()
+    for c, (o, l), (wo, wl) in zip(cases, outs, want):
+        n = sum(c.nodes)
+        assert torch.equal(o[:n], wo[:n]) and torch.equal(l[:n], wl[:n])
+
+
+def test_refusals_of_the_binding():
+    c = Case(8, 2, 128, 16, [40, 3], [5, 2], "tree", seed=127)
+    t = dict(q=c.q, k=c.k, v=c.v, table=c.table, k_new=c.k_new, v_new=c.v_new, nk=c.nk_t, cu=c.cu, mask=c.mask, max_nodes=c.max_nodes)
+    wide = torch.zeros((c.total, 2, 132), dtype=torch.bfloat16, device="cuda")
+
+    def call(**kw):
+        x = {**t, **kw}
+        return bw.attn_tree_paged(x["q"], x["k"], x["v"], x["table"], x["k_new"], x["v_new"], x["nk"], x["cu"], x["mask"],
+                                  x["max_nodes"], **{n: kw[n] for n in ("out", "lse", "workspace") if n in kw})
+    call()
+    for kw in (dict(q=c.q.float()), dict(q=c.q[:, :, ::2]), dict(q=c.q.transpose(0, 1)), dict(k=c.k[:, :, :1]), dict(v=c.v[1:]),
+               dict(k=c.k.half()), dict(k_new=c.k_new[1:]), dict(k_new=wide[:, :, :128]), dict(v_new=c.v_new.cpu()),
+               dict(v_new=c.v_new[:1].expand(c.total, 2, 128)), dict(table=c.table.long()), dict(table=c.table[:, ::2]),
+               dict(nk=c.nk_t[:1]), dict(nk=c.nk_t.long()), dict(cu=c.cu[:2]), dict(mask=c.mask[:-1]), dict(mask=c.mask.to(torch.int32)),
+               dict(max_nodes=65), dict(out=c.q[:-1].clone()), dict(lse=torch.zeros((c.total, 7), device="cuda")),
+               dict(workspace=torch.zeros(1 << 26, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(bw.BwattnError):
+        call(workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    slots = i32(range(c.total))
+    for args in ((c.k_new.float(), c.v_new, slots, c.k, c.v), (c.k_new, c.v_new[:-1], slots, c.k, c.v), (c.k_new, c.v_new, slots.long(), c.k, c.v),
+                 (c.k_new, c.v_new, slots, c.k, c.v[:-1]), (c.k_new, c.v_new, slots, c.k.float(), c.v.float())):
+        with pytest.raises(ValueError):
+            bw.kv_append_paged(*args)
+    with pytest.raises(ValueError):
+        bw.kv_append_paged(c.k_new, c.v_new, slots, c.k, c.v, rows=slots[1:])
+    with pytest.raises(bw.BwattnError):
+        bw.kv_append_paged(c.k_new[1:], c.v_new[1:], slots, c.k, c.v)  # more slots than rows
+    with pytest.raises(ValueError):
+        bw.kv_append_paged_fp8(c.k_new, c.v_new, slots, c.k, c.v, torch.ones((2, 128), device="cuda"), torch.ones((2, 128), device="cuda"))
+    with pytest.raises(ValueError):
+        bw.attn_tree_mask(i32([0]).long(), i32([0, 1]), 1)
+    with pytest.raises(ValueError):
+        bw.attn_tree_mask(i32([0]), i32([0, 1]), 1, nk=i32([1, 2]))
+    with pytest.raises(bw.BwattnError):
+        bw.attn_tree_mask(i32([0]), i32([0, 1]), 1025)
+    for a, b in ((i32([1]), i32([0, 1])), (i32([1, 2]), i32([0]))):
+        with pytest.raises(ValueError):
+            bw.kv_plan_paged(a, b, c.table, i32([1, 1]), i32([3, 4]), i32([2]), 16, 4)
+    with pytest.raises(bw.BwattnError):
+        bw.kv_plan_paged(i32([1, 2]), i32([0, 1]), c.table, i32([1, 1]), i32([3, 4]), i32([2]), 24, 4)
