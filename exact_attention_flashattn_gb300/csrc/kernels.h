@@ -141,7 +141,9 @@ constexpr int kTreeMaxCtas = 304;    // persistent CTAs, two per SM (tree_max_ct
 constexpr int kTreeMergeBytes = 12288;
 // Tiles' time that a unit takes beside its tiles (its own Q, drafts, output; a tile is half the bytes at
 // d = 64). 48 ragged requests at d = 64: 82.7 us at 3 and 4, 86.3 at 6 (before the hot loops were taken apart
-// 118 at 0); 30 ragged requests of two row tiles at d = 128: 82.6 us at 1, 78.0 at 2, 80.7 at 3.
+// 118 at 0); 30 ragged requests of two row tiles at d = 128: 82.6 us at 1, 78.0 at 2, 80.7 at 3. At d = 256 it
+// matters little: at 1, 2, 4 and 6, 4 ragged requests up to 12000 keys took 40.1, 39.7, 39.4 and 40.0 us, 30 up
+// to 6000 over pages 74.2, 74.8, 75.7 and 76.8, 64 of 700 keys 30.6, 29.2, 29.8 and 30.6.
 __host__ __device__ constexpr int tree_unit_cost(int d) { return d == 64 ? 4 : 2; }
 // What the merge has to do at the boundary between a CTA and the one before it (of its KV head: head_group
 // CTAs before), written by the later: something if that is the first boundary inside a unit.

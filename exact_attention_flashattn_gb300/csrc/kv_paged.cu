@@ -9,6 +9,8 @@ namespace bw {
 
 namespace {
 
+constexpr int kSms = 152;  // of a GB300; it only says over how many blocks work is spread
+
 // The first statement of every kernel here, a dependent launch: what the stream did before is complete and
 // visible behind it. (Launched the ordinary way, a kernel behind another starts some 2.5 us later: 32768
 // rows of 8 x 128 appended again and again 44.4 us a call, so 41.8.) The next kernel is set up when this
@@ -417,7 +419,7 @@ cudaError_t launch_tree_mask(const TreeMaskArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_kv_plan(const PlanArgs& a, cudaStream_t stream) {
-  const int blocks = min(152, a.num_tokens / kPlanThreads + 1);
+  const int blocks = min(kSms, a.num_tokens / kPlanThreads + 1);
   return launch_dependent(kv_plan_kernel, dim3(blocks), kPlanThreads, 0, stream, a);
 }
 
@@ -427,7 +429,7 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
   // of 8 x 128: 21.9 us, two blocks 24.4); a copy has nothing to set up and 32 even out the SMs (32768
   // rows: 40.9 us, 16 41.5). In whole rows, no more than there are rows.
   const int64_t most = static_cast<int64_t>(a.num_slots) * per_row;
-  int64_t threads = 152 * (a.k_scale ? 1 : 32) * kAppendThreads / per_row * per_row;
+  int64_t threads = kSms * (a.k_scale ? 1 : 32) * kAppendThreads / per_row * per_row;
   if (threads == 0) threads = per_row;
   if (threads > most) threads = most;
   const dim3 grid(static_cast<unsigned>((threads + kAppendThreads - 1) / kAppendThreads), 2);

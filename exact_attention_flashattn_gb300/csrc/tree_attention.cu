@@ -6,7 +6,7 @@
 //
 // What bounds it: the cache is read once, 4 d bytes per key and KV head, and every key costs 4 d
 // operations per row, a row being one (node, query head) pair of the KV head's group. 128 rows are
-// far on the memory side of this card (128 keys x 128 rows take about 0.35 us of one SM's tensor
+// far on the memory side of this card (at d = 128, 128 keys x 128 rows take 0.67 us of one SM's tensor
 // pipe, their K and V 1.5 us of its share of HBM), 256 rows about level with it. So a tile holds 128
 // rows (whole nodes: kTreeRows / g of them, which the Q copy's box {64, g, nodes} lays out without a
 // gather), and a unit of work is one row tile of one KV head, or two (kTiles == 2) when a sequence
@@ -18,8 +18,7 @@
 // [c T / G, (c + 1) T / G), whatever the lengths (with pages, a group of CTAs, each for another KV head: the
 // list is then of the units of head groups). A unit that lies within one CTA's range is finished there; otherwise each
 // CTA that has a part of it writes its (m, l, o), at most two such parts per CTA, and a second,
-// dependent launch merges them in the order of the keys (no atomics: results do not depend on which
-// CTA ends first).
+// dependent launch merges them in the order of the keys, so results do not depend on which CTA ends first.
 //
 // Inside a CTA a stream has an S and an O in tensor memory, an MMA issuing warp and a softmax warpgroup
 // (thread = row = TMEM lane):
@@ -870,8 +869,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
               if (!vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort))) return false;
               tc_fence_after();
             }
-            // p = 2^(s scale log2e - m) as bf16 pairs into the first half of the S columns; l is the fp32
-            // sum before that rounding
+            // p = 2^(s scale log2e - m) as bf16 pairs into the first half of the S columns. The tensor core
+            // multiplies bf16 V by weights of the same type only: each is off by at most 2^-8 of itself, the
+            // output type's own half step (measured on the listed sizes, 2.3e-3 from 64 bits, fp32 weights
+            // rounded once at the end 1.7e-3). l is the fp32 sum before that rounding
             float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < kKeys / 32; ++c) {

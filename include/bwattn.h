@@ -313,7 +313,9 @@ size_t attn_tree_workspace_size(int num_seqs, int max_nodes, int Hq, int Hkv, in
  *   workspace    : at least attn_tree_workspace_size(...) bytes; contents undefined on exit. Must not
  *                  be shared by calls that may overlap on the GPU
  * Keys and values that a node does not see (context rows at or past nk, drafts its mask leaves out)
- * have no effect on its outputs, whatever they hold (infinities and NaN included). Supported: d in
+ * have no effect on its outputs, whatever they hold (infinities and NaN included). Scores, the sum of the
+ * weights and O are held in fp32; each weight is rounded to bf16 (by at most 2^-8 of itself) for the product
+ * with V, as attn_fwd's are. Supported: d in
  * {64, 128, 256}, Hq / Hkv <= 128, max_nodes <= 1024. Strides are multiples of 8 and at least
  * Hq * d (q) or Hkv * d (k_new, v_new), else INVALID_ARG; other errors as for attn_decode.
  */
