@@ -22,6 +22,8 @@ Calls (see ``include/bwattn.h`` for the full contract):
   ``attn_tree_mask`` (their masks and positions from parent links), ``kv_plan_paged`` (block tables
   and slots from request lengths), ``kv_append_paged`` / ``kv_append_paged_fp8`` (new K/V rows into
   the pages).
+* Around a paged cache's attention: ``attn_qk_norm_rope`` (per-head norm and rotation of q and k),
+  ``attn_chunk_paged`` (new tokens over the pages), ``attn_tree_verify`` (which drafts are kept).
 """
 from __future__ import annotations
 
@@ -36,7 +38,7 @@ __all__ = [
     "attn_fwd", "attn_fwd_host", "attn_decode", "attn_decode_paged", "attn_decode_fp8", "attn_decode_paged_fp8",
     "attn_varlen", "attn_tree", "attn_tree_paged", "attn_tree_mask", "kv_plan_paged", "kv_append_paged",
     "kv_append_paged_fp8", "fwd_host_workspace_size", "decode_workspace_size", "varlen_workspace_size",
-    "tree_workspace_size",
+    "tree_workspace_size", "attn_chunk_paged", "chunk_workspace_size", "attn_qk_norm_rope", "attn_tree_verify",
     "get_status", "clear_status", "set_wait_timeout_ns", "test_wait_timeout", "launch_count", "lib",
     "status_string", "BwattnError", "OK", "ERR_INVALID_ARG", "ERR_UNSUPPORTED", "ERR_CUDA", "ERR_TIMEOUT",
 ]
@@ -105,6 +107,14 @@ def lib() -> ctypes.CDLL:
         L.kv_append_paged.restype = ci
         L.kv_append_paged_fp8.argtypes = [vp] * 8 + [ci] * 6 + [i64] * 2 + [vp]
         L.kv_append_paged_fp8.restype = ci
+        L.attn_chunk_workspace_size.argtypes = [ci] * 5
+        L.attn_chunk_workspace_size.restype = sz
+        L.attn_chunk_paged.argtypes = [vp] * 8 + [ci] * 9 + [i64, ci, cf, vp, sz, vp]
+        L.attn_chunk_paged.restype = ci
+        L.attn_qk_norm_rope.argtypes = [vp] * 9 + [cf] + [ci] * 7 + [i64] * 4 + [vp]
+        L.attn_qk_norm_rope.restype = ci
+        L.attn_tree_verify.argtypes = [vp] * 10 + [ci] * 4 + [i64] * 2 + [vp]
+        L.attn_tree_verify.restype = ci
         L.bwattn_last_cuda_error.argtypes = []
         L.bwattn_last_cuda_error.restype = ci
         L.bwattn_status_string.argtypes = [ci]
@@ -680,6 +690,141 @@ def kv_append_paged_fp8(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.T
     dev = _first(k_pages, "k_pages", 4)
     _first(k_new, "k_new", 3)
     return _run(_append, dev, stream, k_new, v_new, slots, k_pages, v_pages, k_scale, v_scale, rows, True)
+
+
+# ---------------------------------------------------------------- around a paged cache's attention
+
+
+def chunk_workspace_size(num_seqs: int, max_seqlen_q: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(lib().attn_chunk_workspace_size(num_seqs, max_seqlen_q, Hq, Hkv, d))
+
+
+def attn_chunk_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                     nk: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqlen_q: int, causal: bool = True,
+                     scale: float | None = None, workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     lse: torch.Tensor | bool | None = True, stream=None):
+    """New tokens over a paged cache that holds their own keys too. q [total_q, Hq, d] bf16 (rows may lie apart);
+    pages [num_pages, page_size, Hkv, d], block_table [B, max_pages] int32; nk [B] (keys, the new tokens' among
+    them), cu_seqlens_q [B + 1] int32 -> (o, lse or None). ``causal`` False: every token sees all nk keys."""
+    dev = _first(q, "q", 3)
+    _first(k_pages, "k_pages", 4)
+    _first(block_table, "block_table", 2)
+    return _run(_chunk, dev, stream, q, k_pages, v_pages, block_table, nk, cu_seqlens_q, int(max_seqlen_q), bool(causal),
+                scale, workspace, out, lse)
+
+
+def _chunk(st, dev, q, k, v, table, nk, cu, most, causal, scale, workspace, out, lse):
+    tq, Hq, d = q.shape
+    num_pages, page_size, Hkv, dk = k.shape
+    num_seqs, max_pages = table.shape
+    if dk != d:
+        raise ValueError("q and the pages must have the same head dim")
+    tp = _like(table, "block_table", dev, _I32)
+    kp = _like(k, "k_pages", dev, _BF16)
+    vp = _like(v, "v_pages", dev, _BF16, k.shape)
+    qs = _rows(q, "q", dev, q.shape)
+    nkp = _like(nk, "nk", dev, _I32, (num_seqs,))
+    cup = _like(cu, "cu_seqlens_q", dev, _I32, (num_seqs + 1,))
+    out = _out(out, "out", dev, _BF16, q.shape)
+    if lse is True:
+        lse = torch.empty((tq, Hq), dtype=_F32, device=dev)
+    elif not isinstance(lse, _Tensor):
+        lse = None
+    else:
+        _like(lse, "lse", dev, _F32, (tq, Hq))
+    if workspace is None:
+        workspace = torch.empty(max(chunk_workspace_size(num_seqs, most, Hq, Hkv, d), 16), dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    rc = (_lib or lib()).attn_chunk_paged(
+        q.data_ptr(), kp, vp, tp, out.data_ptr(), None if lse is None else lse.data_ptr(), nkp, cup, num_seqs, tq, most,
+        page_size, num_pages, max_pages, Hq, Hkv, d, qs, causal, _scale(scale, d), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), st)
+    if rc:
+        _check(rc, "attn_chunk_paged")
+    return out, lse
+
+
+def attn_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
+                      q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                      axes: torch.Tensor | None = None, interleaved: bool = False, q_out: torch.Tensor | None = None,
+                      k_out: torch.Tensor | None = None, stream=None):
+    """Per-head norm and rotation of q [n, Hq, d] and k [n, Hkv, d] bf16 (rows may lie apart) -> (q_out, k_out), which may
+    be q and k themselves. positions [n] or [num_axes, n] int32; inv_freq [pairs] fp32; axes [pairs] int32, each
+    pair's row of positions; weights [d] bf16 (None: no norm). Pairs are channels (i, i + pairs), or neighbours
+    with ``interleaved``; channels behind them are not rotated."""
+    dev = _first(q, "q", 3)
+    _first(k, "k", 3)
+    return _run(_qk_rope, dev, stream, q, k, positions, inv_freq, q_weight, k_weight, float(eps), axes, bool(interleaved),
+                q_out, k_out)
+
+
+def _qk_rope(st, dev, q, k, positions, freq, q_weight, k_weight, eps, axes, interleaved, q_out, k_out):
+    n, Hq, d = q.shape
+    Hkv = k.shape[1]
+    qs, ks = _rows(q, "q", dev, q.shape), _rows(k, "k", dev, (n, Hkv, d))
+    num_axes = 1 if positions.dim() == 1 else positions.shape[0]
+    pp = _like(positions, "positions", dev, _I32, (n,) if positions.dim() == 1 else (num_axes, n))
+    if freq.dim() != 1:
+        raise ValueError("inv_freq must be 1-D")
+    fp = _like(freq, "inv_freq", dev, _F32)
+    pairs = freq.shape[0]
+    ap = None if axes is None else _like(axes, "axes", dev, _I32, (pairs,))
+    qw = None if q_weight is None else _like(q_weight, "q_weight", dev, _BF16, (d,))
+    kw = None if k_weight is None else _like(k_weight, "k_weight", dev, _BF16, (d,))
+    if q_out is None:
+        q_out, qos = torch.empty((n, Hq, d), dtype=_BF16, device=dev), Hq * d
+    else:
+        qos = _rows(q_out, "q_out", dev, q.shape)
+    if k_out is None:
+        k_out, kos = torch.empty((n, Hkv, d), dtype=_BF16, device=dev), Hkv * d
+    else:
+        kos = _rows(k_out, "k_out", dev, k.shape)
+    rc = (_lib or lib()).attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), pp, ap, fp, qw, kw,
+                                           eps, n, num_axes, pairs, interleaved, Hq, Hkv, d, qs, ks, qos, kos, st)
+    if rc:
+        _check(rc, "attn_qk_norm_rope")
+    return q_out, k_out
+
+
+def attn_tree_verify(tokens: torch.Tensor, parents: torch.Tensor, cu_seqlens_q: torch.Tensor, target_probs: torch.Tensor,
+                     uniforms: torch.Tensor, sample_uniforms: torch.Tensor, max_nodes: int,
+                     draft_probs: torch.Tensor | None = None, stream=None):
+    """Which drafts are kept: tokens, parents [total_q] int32 (node 0 of a request its root), target_probs (and
+    draft_probs, if the drafts were drawn from them) [total_q, vocab] fp32 (rows may lie apart), uniforms [total_q]
+    and sample_uniforms [B] fp32 -> int32 (accepted [total_q]: packed rows of each request's path, then -1; counts
+    [B]; next_tokens [B])."""
+    dev = _first(target_probs, "target_probs", 2)
+    return _run(_verify, dev, stream, tokens, parents, cu_seqlens_q, target_probs, uniforms, sample_uniforms, int(max_nodes),
+                draft_probs)
+
+
+def _prob_rows(t, name, dev, shape):
+    """fp32 [rows, vocab] whose rows may lie apart: the row stride."""
+    if not isinstance(t, _Tensor) or t.dtype is not _F32 or t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name} must be an fp32 tensor {tuple(shape)} on cuda:{dev}")
+    n, c = shape
+    if t.is_contiguous() or n <= 1 and t.stride(1) == 1:
+        return c
+    if t.stride(1) != 1 or t.stride(0) < c:
+        raise ValueError(f"{name}: a row's values must be contiguous, and rows must not overlap")
+    return t.stride(0)
+
+
+def _verify(st, dev, tokens, parents, cu, p, u, w, max_nodes, q):
+    n, vocab = p.shape
+    num_seqs = cu.numel() - 1
+    ps = _prob_rows(p, "target_probs", dev, p.shape)
+    qs = 0 if q is None else _prob_rows(q, "draft_probs", dev, p.shape)
+    args = (_like(tokens, "tokens", dev, _I32, (n,)), _like(parents, "parents", dev, _I32, (n,)),
+            _like(cu, "cu_seqlens_q", dev, _I32), p.data_ptr(), None if q is None else q.data_ptr(),
+            _like(u, "uniforms", dev, _F32, (n,)), _like(w, "sample_uniforms", dev, _F32, (num_seqs,)))
+    accepted, counts, following = [torch.empty(m, dtype=_I32, device=dev) for m in (n, num_seqs, num_seqs)]
+    rc = (_lib or lib()).attn_tree_verify(*args, accepted.data_ptr(), counts.data_ptr(), following.data_ptr(), num_seqs, n,
+                                          max_nodes, vocab, ps, qs, st)
+    if rc:
+        _check(rc, "attn_tree_verify")
+    return accepted, counts, following
 
 
 def get_status(stream=None) -> int:

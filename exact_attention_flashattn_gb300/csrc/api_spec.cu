@@ -4,36 +4,17 @@
 #include <stdint.h>
 
 #include "../../include/bwattn.h"
+#include "checks.h"
 #include "kernels.h"
 
 namespace {
 
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-bool good(const void* p, uintptr_t n) { return p != nullptr && aligned(p, n); }
-bool good_or_null(const void* p, uintptr_t n) { return p == nullptr || aligned(p, n); }
-bool head_dim(int d) { return d == 64 || d == 128 || d == 256; }
-// distance between consecutive rows of `width` elements: 16-byte steps, no overlap, a tensor map's limit
-bool row_stride(int64_t stride, int64_t width) {
-  return stride >= width && stride % 8 == 0 && stride < (static_cast<int64_t>(1) << 38);
-}
-bool page_sizes(int page_size, int num_pages) {
-  return page_size >= 16 && page_size <= 1024 && page_size % 16 == 0 && num_pages > 0 &&
-         static_cast<int64_t>(num_pages) * page_size <= 0x7fffffff;
-}
 // what the tree calls take, and the size of their workspace is given for: sizes in range (else INVALID_ARG) ...
 bool tree_range(int num_seqs, int max_nodes, int Hq, int Hkv, int d) {
   return num_seqs >= 0 && num_seqs <= 65535 && max_nodes >= 0 && Hq > 0 && Hq <= 65535 && Hkv > 0 && d > 0 && Hq % Hkv == 0;
 }
 // ... that the kernels implement (else UNSUPPORTED)
 bool tree_supported(int max_nodes, int g, int d) { return head_dim(d) && g <= bw::kTreeRows && max_nodes <= bw::kTreeMaxNodes; }
-
-int done(cudaError_t e) {
-  if (e != cudaSuccess) {
-    bw::record_cuda_error(e);
-    return BWATTN_ERR_CUDA;
-  }
-  return BWATTN_OK;
-}
 
 int tree_impl(const void* q, const void* k, const void* v, const void* k_new, const void* v_new, void* o, float* lse,
               const int32_t* nk, const int32_t* cu_seqlens_q, const uint64_t* mask, const int32_t* block_table,

@@ -164,7 +164,9 @@ struct TreeArgs {
   const uint16_t* q;      // bf16 bits; node t of the packed batch at q + t * q_stride, heads d apart
   const uint16_t* k;      // cache: contiguous [B, Hkv, cap, d] or pages [num_pages, page_size, Hkv, d]
   const uint16_t* v;
-  const uint16_t* k_new;  // drafted rows, node t at k_new + t * k_new_stride, KV heads d apart
+  const uint16_t* k_new;  // drafted rows, node t at k_new + t * k_new_stride, KV heads d apart; null: a chunk, whose
+                          // keys are in the (paged) cache: its "nodes" are tokens, of which i sees the keys up to and
+                          // with i + nk - nq (causal), or all nk; max_nodes is then the most tokens of a sequence
   const uint16_t* v_new;
   uint16_t* o;            // [total_q, Hq, d]
   float* lse;             // [total_q, Hq] or null
@@ -186,6 +188,7 @@ struct TreeArgs {
   int groups;             // groups of CTAs of the attention kernel
   int merges, merge_warps;  // units that may have to be merged; warps that share out one's parts
   float scale_log2;
+  int causal;             // chunks
   unsigned int* status;
   uint64_t timeout_ns;
 };
@@ -212,7 +215,7 @@ inline int64_t tree_most_units(const TreeArgs& a) {
 inline int64_t tree_most_tiles(const TreeArgs& a) {
   const int keys = a.d == 256 ? 64 : 128;
   return tree_most_units(a) *
-         ((static_cast<int64_t>(a.kv_cap) + keys - 1) / keys + (a.max_nodes + keys - 1) / keys + tree_unit_cost(a.d));
+         ((static_cast<int64_t>(a.kv_cap) + keys - 1) / keys + (a.k_new ? (a.max_nodes + keys - 1) / keys : 1) + tree_unit_cost(a.d));
 }
 // Fills the maps and sizes that follow from the others, launches the attention and the merge.
 cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream);
@@ -278,6 +281,41 @@ struct AppendArgs {
   int row_elems;               // Hkv * d
 };
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
+
+// ---- norm and rotation of queries and keys ----
+struct RopeArgs {
+  const uint16_t* q;  // bf16 bits; row i at q + i * q_stride, heads d apart
+  const uint16_t* k;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  const int32_t* positions;  // [num_axes, num_rows]
+  const int32_t* axes;       // [pairs] or null (axis 0)
+  const float* freq;         // [pairs], radians a position
+  const uint16_t* q_weight;  // [d] or null: no norm
+  const uint16_t* k_weight;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  int num_rows, num_axes, pairs, interleaved, Hq, Hkv, d;
+  float eps;
+};
+cudaError_t launch_qk_rope(const RopeArgs& a, cudaStream_t stream);
+
+// ---- verification of drafted trees ----
+constexpr int kVerifyMaxVocab = 500000;  // a row of ones, in 2^-44ths, stays below 2^63
+struct VerifyArgs {
+  const int32_t* tokens;   // [total_q]
+  const int32_t* parents;  // [total_q]
+  const int32_t* cu_q;     // [num_seqs + 1] (clamped to total_q)
+  const float* p;          // target's probabilities: row i at p + i * p_stride
+  const float* q;          // the drafts' or null
+  const float* u;          // [total_q]
+  const float* w;          // [num_seqs]
+  int32_t* accepted;       // [total_q]
+  int32_t* counts;         // [num_seqs]
+  int32_t* next;           // [num_seqs]
+  int64_t p_stride, q_stride;
+  int num_seqs, total_q, max_nodes, vocab;
+};
+cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t stream);
 
 // Timeout self-test: one CTA waits on a barrier that is never arrived at.
 cudaError_t launch_wait_timeout_probe(uint64_t timeout_ns, unsigned int* status, cudaStream_t stream);

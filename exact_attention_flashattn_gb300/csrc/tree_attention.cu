@@ -99,6 +99,7 @@ struct Seg {
   int k0, nt, ct;   // tiles [k0, k0 + nt) of the unit; its first ct tiles are context
   int slot;         // -1: the whole unit; else which of the CTA's two partial results
   int bad;          // set when a draft's V held an infinity or NaN
+  int shift;        // chunks: node i sees keys up to and with i + shift (nk: the most that a row of the unit sees)
 };
 
 struct Barriers {
@@ -122,19 +123,33 @@ static_assert(sizeof(Barriers) <= kBarBytes, "barrier block");
 
 __device__ __forceinline__ bool vote(bool x) { return __all_sync(0xffffffffu, x); }
 
-// Tiles of one sequence.
-template <int D>
+// Tiles of one sequence. Chunks: the units of its later rows have more of them, and the places of a KV head are
+// summed unit by unit.
+template <int D, bool kChunk>
 struct SeqTiles {
   int tok0, nq, nk;
   int ct, per_unit;  // context tiles, all tiles of a unit
   int row_units;     // units of a KV head
+  int shift;         // chunks: as in Seg
+  int places;        // chunks: of a KV head
   // places of the list; the host bounds their sum
-  __device__ __forceinline__ int all(int head_groups) const { return (per_unit + tree_unit_cost(D)) * row_units * head_groups; }
+  __device__ __forceinline__ int all(int head_groups) const {
+    return kChunk ? places * head_groups : (per_unit + tree_unit_cost(D)) * row_units * head_groups;
+  }
+  // chunks: keys that the last row of unit u sees, and the unit's tiles (one at least: rows without keys are written too)
+  __device__ __forceinline__ int unit_keys(int u, int unit_nodes) const {
+    return min(max(shift + min(nq, (u + 1) * unit_nodes), 0), nk);
+  }
+  template <int kKeys>
+  __device__ __forceinline__ int unit_tiles(int u, int unit_nodes) const {
+    const int n = unit_keys(u, unit_nodes);
+    return max(n / kKeys + (n % kKeys != 0), 1);
+  }
 };
-template <int D, int kTiles>
-__device__ __forceinline__ SeqTiles<D> seq_tiles(const TreeArgs& a, int b) {
+template <int D, int kTiles, bool kChunk>
+__device__ __forceinline__ SeqTiles<D, kChunk> seq_tiles(const TreeArgs& a, int b) {
   constexpr int kKeys = Cfg<D, kTiles>::kKeys;
-  SeqTiles<D> s;
+  SeqTiles<D, kChunk> s;
   s.tok0 = min(max(a.cu_q[b], 0), a.total_q);
   s.nq = min(min(max(a.cu_q[b + 1], s.tok0), a.total_q) - s.tok0, a.max_nodes);
   s.nk = min(max(a.nk[b], 0), a.kv_cap);
@@ -142,6 +157,11 @@ __device__ __forceinline__ SeqTiles<D> seq_tiles(const TreeArgs& a, int b) {
   s.per_unit = s.ct + (s.nq + kKeys - 1) / kKeys;
   const int unit_nodes = kTiles * a.tile_nodes;
   s.row_units = s.nq <= unit_nodes ? s.nq > 0 : (s.nq + unit_nodes - 1) / unit_nodes;  // 0 for a sequence without nodes
+  if constexpr (kChunk) {
+    s.shift = a.causal ? s.nk - s.nq : s.nk - 1;  // (its sum with nq fits: the host sees to that)
+    s.places = s.row_units * tree_unit_cost(D);
+    for (int u = 0; u < s.row_units; ++u) s.places += s.template unit_tiles<kKeys>(u, unit_nodes);
+  }
   return s;
 }
 
@@ -253,13 +273,15 @@ struct Regs {
 struct MaskedTile {
   float m, l, alpha;
 };
-__device__ __noinline__ MaskedTile masked_tile(uint32_t tS, uint32_t tP, int left, const uint64_t* bits, int bit0, float sl2,
+// Chunks: no mask, the row's own first `mine` keys.
+template <bool kChunk>
+__device__ __noinline__ MaskedTile masked_tile(uint32_t tS, uint32_t tP, int left, int mine, const uint64_t* bits, int bit0, float sl2,
                                                float m_ref) {
   const int chunks = (left + 31) / 32;
   auto load = [&](int c, uint32_t (&v)[32]) {
-    const int rest = left - 32 * c, bit = bit0 + 32 * c;
-    uint32_t keep = rest >= 32 ? 0xffffffffu : (1u << rest) - 1u;
-    if (bits) keep &= static_cast<uint32_t>(bits[bit >> 6] >> (bit & 32));
+    const int rest = (kChunk ? mine : left) - 32 * c, bit = bit0 + 32 * c;
+    uint32_t keep = rest >= 32 ? 0xffffffffu : kChunk && rest <= 0 ? 0u : (1u << rest) - 1u;
+    if (!kChunk && bits) keep &= static_cast<uint32_t>(bits[bit >> 6] >> (bit & 32));
     tmem_ld32(tS + 32 * c, v);
     tmem_wait_ld();
     tmem_reg_fence(v);
@@ -301,7 +323,7 @@ __device__ __noinline__ MaskedTile masked_tile(uint32_t tS, uint32_t tP, int lef
   return r;
 }
 
-template <int D, int kTiles>
+template <int D, int kTiles, bool kChunk>
 __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCtasPerSm)
     tree_kernel(const __grid_constant__ TreeArgs a) {
   using C = Cfg<D, kTiles>;
@@ -318,8 +340,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     prefetch_tmap(&a.tm_q);
     prefetch_tmap(&a.tm_k);
     prefetch_tmap(&a.tm_v);
-    prefetch_tmap(&a.tm_kn);
-    prefetch_tmap(&a.tm_vn);
+    if constexpr (!kChunk) {
+      prefetch_tmap(&a.tm_kn);
+      prefetch_tmap(&a.tm_vn);
+    }
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -362,7 +386,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   int mine = 0, incl = 0;
   if (wide || warp == C::kTmaWarp) {
 #pragma unroll 4
-    for (int b = run0; b < run1; ++b) mine += seq_tiles<D, kTiles>(a, b).all(a.head_groups);
+    for (int b = run0; b < run1; ++b) mine += seq_tiles<D, kTiles, kChunk>(a, b).all(a.head_groups);
     incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -391,7 +415,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     if (group < share.G && T > 0) my_begin = share.begin(group), my_end = share.begin(group + 1);
     if (my_begin < my_end && before <= my_begin && my_begin < before + mine) {
       int b = run0;
-      for (int n; my_begin >= before + (n = seq_tiles<D, kTiles>(a, b).all(a.head_groups)); ++b) before += n;
+      for (int n; my_begin >= before + (n = seq_tiles<D, kTiles, kChunk>(a, b).all(a.head_groups)); ++b) before += n;
       bar->list[1] = b;
       bar->list[2] = before;
     }
@@ -418,6 +442,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     if (lane == 0) mbar_arrive(&bar->seg_empty[k % kSegSlots]);
   };
   // rows of the unit's row tile w that exist
+  // chunks: the first tile (of the unit) that some row of it does not see whole
+  auto first_masked = [&](const Seg& s) { return min(max(s.shift + s.node0 + 1, 0), s.nk) / kKeys; };
   auto tile_rows = [&](const Seg& s, int w) { return max(0, min(tile_nodes, s.nq - s.node0 - w * tile_nodes)) * a.g; };
 
   // paged: the copy of a tile (atom copy % kHalves of piece copy / kHalves) that is this lane's; with a
@@ -494,7 +520,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       }
     }
 #pragma unroll 1
-    for (; j < s.nt; ++j, ++n) {
+    for (; !kChunk && j < s.nt; ++j, ++n) {
       if (!before_tile(j)) return false;
       for (int kv = kv0; kv < kv1; ++kv) {
         const int i = 2 * n + kv, slot = i % kStages;
@@ -526,15 +552,54 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     const int head0 = static_cast<int>(blockIdx.x) - group * a.head_group, end = my_end;
     int pos = my_begin, b = pos < end ? bar->list[1] : 0, seq_at = pos < end ? bar->list[2] : 0;
     int nload = 0, nq[2] = {0, 0};  // K tiles, and Q tiles into each buffer
+    // chunks: the sequence, and the unit of it (and of a group of heads) that holds place pos, from place unit_at on
+    SeqTiles<D, kChunk> seq{};
+    int heads = 0, unit = 0, unit_at = 0;
+    if (kChunk && pos < end) {
+      seq = seq_tiles<D, kTiles, kChunk>(a, b);
+      heads = (pos - seq_at) / seq.places;
+      unit_at = seq_at + heads * seq.places;
+    }
     bool ok = true;
     for (int k = 0; ok; ++k) {
       Seg s{};
       int u0 = 0, size = 0;  // the unit's first place, and its places
-      while (pos < end && !s.valid) {
-        SeqTiles<D> q = seq_tiles<D, kTiles>(a, b);
+      while (kChunk && pos < end && !s.valid) {
+        for (;;) {
+          if (pos >= seq_at + seq.all(a.head_groups)) {
+            seq_at += seq.all(a.head_groups);
+            seq = seq_tiles<D, kTiles, kChunk>(a, ++b);
+            heads = unit = 0;
+            unit_at = seq_at;
+            continue;
+          }
+          size = seq.template unit_tiles<kKeys>(unit, kTiles * tile_nodes) + tree_unit_cost(D);
+          if (pos < unit_at + size) break;
+          unit_at += size;
+          if (++unit == seq.row_units) unit = 0, ++heads;
+        }
+        const int at = pos - unit_at, to = min(size, at + end - pos);
+        u0 = unit_at;
+        pos += to - at;
+        s.k0 = max(at - tree_unit_cost(D), 0);
+        s.nt = to - tree_unit_cost(D) - s.k0;
+        if (s.nt <= 0) break;  // the range ends before the unit's first tile
+        s.valid = 1;
+        s.b = b;
+        s.tok0 = seq.tok0;
+        s.nq = seq.nq;
+        s.nk = seq.unit_keys(unit, kTiles * tile_nodes);
+        s.hkv = heads * a.head_group + head0;
+        s.node0 = unit * (kTiles * tile_nodes);
+        s.ct = size - tree_unit_cost(D);
+        s.shift = seq.shift;
+        s.slot = s.nt == s.ct ? -1 : (k == 0 ? 0 : 1);
+      }
+      while (!kChunk && pos < end && !s.valid) {
+        SeqTiles<D, kChunk> q = seq_tiles<D, kTiles, kChunk>(a, b);
         while (pos >= seq_at + q.all(a.head_groups)) {
           seq_at += q.all(a.head_groups);
-          q = seq_tiles<D, kTiles>(a, ++b);
+          q = seq_tiles<D, kTiles, kChunk>(a, ++b);
         }
         size = q.per_unit + tree_unit_cost(D);
         const int local = pos - seq_at, unit = local / size;
@@ -696,7 +761,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       const int nt = s.nt, base = nload;
       nload += 2 * nt;
       // the tiles from `plain` on: the context's last one, if it is not whole, and the drafts
-      const int plain = min(max((s.nk % kKeys ? s.ct - 1 : s.ct) - s.k0, 0), nt);
+      const int plain = min(max((kChunk ? first_masked(s) : s.nk % kKeys ? s.ct - 1 : s.ct) - s.k0, 0), nt);
       const bool turns = kTiles == 2 && !C::kLook && tile_rows(s, 1) > 0;
       if (kTiles == 2 && tile_rows(s, w) == 0) {  // no rows: only gives the slots back
         umma_commit(&bar->q_empty[qb]);
@@ -726,9 +791,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
           // are zeroed, and drafts' infinities and NaN (two row tiles read one V tile: stream 0 looks it
           // over for both)
           const int kt = s.k0 + j;
-          const bool draft = kt >= s.ct;
+          const bool draft = kChunk ? a.causal != 0 : kt >= s.ct;  // keys that some rows see and others do not
           uint64_t* ready = &bar->v_ready[nspecial % kVSlots];
-          valid = min(kKeys, draft ? s.nq - (kt - s.ct) * kKeys : s.nk - kt * kKeys);
+          valid = min(kKeys, !kChunk && draft ? s.nq - (kt - s.ct) * kKeys : s.nk - kt * kKeys);
           if (kTiles == 1 || w == 0) {
             if (clean_v<C::kHalves, kKeys>(sRing + (iv % kStages) * C::kTileBytes, valid, draft, lane) && lane == 0)
               atomicOr(&sp->bad, 1);
@@ -806,9 +871,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       const int some_row = min(max(row, 0), rows - 1);
       const int node = s.node0 + rw * tile_nodes + some_row / a.g;  // within the sequence
       const int head = s.hkv * a.g + some_row % a.g;
-      const uint64_t* bits = a.mask + static_cast<int64_t>(s.tok0 + node) * a.mask_words;
+      const uint64_t* bits = kChunk ? nullptr : a.mask + static_cast<int64_t>(s.tok0 + node) * a.mask_words;
+      const int limit = kChunk ? min(max(s.shift + node + 1, 0), s.nk) : 0;  // keys that this row sees
       // the tiles from `plain` on have keys that some row does not see
-      const int plain = min(max((s.nk % kKeys ? s.ct - 1 : s.ct) - s.k0, 0), s.nt);
+      const int plain = min(max((kChunk ? first_masked(s) : s.nk % kKeys ? s.ct - 1 : s.ct) - s.k0, 0), s.nt);
       float m_ref = -INFINITY, l = 0.f;
       auto tile = [&](int j, auto masked) -> bool {
         const int x = C::kTwoS ? n & 1 : w, phase = (C::kTwoS ? n >> 1 : n) & 1;
@@ -824,9 +890,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
               if (!vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort))) return false;
               tc_fence_after();
             }
-            const bool draft = kt >= s.ct;
+            const bool draft = !kChunk && kt >= s.ct;
             const int left = draft ? s.nq - (kt - s.ct) * kKeys : s.nk - kt * kKeys;
-            const MaskedTile r = masked_tile(tS, tP, min(left, kKeys), draft ? bits : nullptr, (kt - s.ct) * kKeys, sl2, m_ref);
+            const MaskedTile r = masked_tile<kChunk>(tS, tP, min(left, kKeys), limit - kt * kKeys, draft ? bits : nullptr,
+                                                     (kt - s.ct) * kKeys, sl2, m_ref);
             m_ref = r.m;
             l = l * r.alpha + r.l;
             if (j > 0) alpha_o = r.alpha;
@@ -946,9 +1013,20 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]);
           if (bad && row_ok) {
-            // the infinities and NaN among the drafts that this row sees
+            // the infinities and NaN among the drafts (chunks: among the keys of masked tiles) that this row sees
+            if constexpr (kChunk) {
+              const int* table = a.block_table + static_cast<int64_t>(s.b) * a.max_pages;
+              const int d1 = min((s.k0 + s.nt) * kKeys, limit);
+              for (int x = (s.k0 + plain) * kKeys; x < d1; ++x) {
+                const int page = min(max(table[x / a.page_size], 0), a.num_pages - 1);
+                const uint16_t* v = a.v + ((static_cast<int64_t>(page) * a.page_size + x % a.page_size) * a.Hkv + s.hkv) * D + c * 32;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if ((v[e] & 0x7f80) == 0x7f80) o[e] += __uint_as_float(static_cast<uint32_t>(v[e]) << 16);
+              }
+            }
             const int d0 = max(s.k0 - s.ct, 0) * kKeys, d1 = min((s.k0 + s.nt - s.ct) * kKeys, s.nq);
-            for (int x = d0; x < d1; ++x) {
+            for (int x = d0; !kChunk && x < d1; ++x) {
               if (!(bits[x >> 6] >> (x & 63) & 1)) continue;
               const uint16_t* v = a.v_new + (s.tok0 + x) * a.v_new_stride + s.hkv * D + c * 32;
 #pragma unroll
@@ -957,6 +1035,12 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             }
           }
           if (!row_ok) continue;
+          if constexpr (kChunk) {
+            // a unit without keys has no P.V: what stands in tensor memory is not its O
+            if (s.nk == 0)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
           if (s.slot < 0) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -1126,18 +1210,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   }
 }
 
-template <int D, int kTiles>
+template <int D, int kTiles, bool kChunk>
 cudaError_t launch(const TreeArgs& a, int dev, cudaStream_t stream) {
   using C = Cfg<D, kTiles>;
   // once per device (the attribute stays with the device's copy of the kernel)
   static std::atomic<uint64_t> set{0};
   cudaError_t e;
   if (dev >= 64 || !(set.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(tree_kernel<D, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
+    e = cudaFuncSetAttribute(tree_kernel<D, kTiles, kChunk>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
     if (e != cudaSuccess) return e;
     if (dev < 64) set.fetch_or(1ull << dev);
   }
-  e = launch_dependent(tree_kernel<D, kTiles>, dim3(a.groups * a.head_group), C::kThreads, C::kSmem, stream, a);
+  e = launch_dependent(tree_kernel<D, kTiles, kChunk>, dim3(a.groups * a.head_group), C::kThreads, C::kSmem, stream, a);
   if (e != cudaSuccess) return e;
   count_launch();
   if (a.groups == 1) return cudaSuccess;
@@ -1161,9 +1245,10 @@ cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
   a.tile_rows = tree_tile_rows(a.max_nodes, a.g, d);
   a.tile_nodes = a.tile_rows / a.g;
   if ((e = make_map_bf16(&a.tm_q, a.q, d, a.Hq, a.total_q, d, a.q_stride, a.g, a.tile_nodes)) != cudaSuccess) return e;
+  const bool chunk = a.k_new == nullptr;
   a.new_box = a.max_nodes < keys ? (a.max_nodes + 7) / 8 * 8 : keys;
-  if ((e = make_map_bf16(&a.tm_kn, a.k_new, d, a.Hkv, a.total_q, d, a.k_new_stride, 1, a.new_box)) != cudaSuccess ||
-      (e = make_map_bf16(&a.tm_vn, a.v_new, d, a.Hkv, a.total_q, d, a.v_new_stride, 1, a.new_box)) != cudaSuccess)
+  if (!chunk && ((e = make_map_bf16(&a.tm_kn, a.k_new, d, a.Hkv, a.total_q, d, a.k_new_stride, 1, a.new_box)) != cudaSuccess ||
+                 (e = make_map_bf16(&a.tm_vn, a.v_new, d, a.Hkv, a.total_q, d, a.v_new_stride, 1, a.new_box)) != cudaSuccess))
     return e;
   if (a.kv_cap == 0) {
     a.tm_k = a.tm_kn;  // no context tile exists
@@ -1202,9 +1287,13 @@ cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
   a.merges = static_cast<int>(units < boundaries ? units : boundaries);
   a.merge_warps = kMergeWarps;  // a power of two, at least the parts of a unit on average
   while (a.merge_warps > 2 && boundaries / units + 2 <= a.merge_warps / 2) a.merge_warps /= 2;
-  if (d == 64) return tiles == 2 ? launch<64, 2>(a, dev, stream) : launch<64, 1>(a, dev, stream);
-  if (d == 128) return tiles == 2 ? launch<128, 2>(a, dev, stream) : launch<128, 1>(a, dev, stream);
-  return launch<256, 1>(a, dev, stream);
+  auto go = [&](auto is_chunk) {
+    constexpr bool kChunk = decltype(is_chunk)::value;
+    if (d == 64) return tiles == 2 ? launch<64, 2, kChunk>(a, dev, stream) : launch<64, 1, kChunk>(a, dev, stream);
+    if (d == 128) return tiles == 2 ? launch<128, 2, kChunk>(a, dev, stream) : launch<128, 1, kChunk>(a, dev, stream);
+    return launch<256, 1, kChunk>(a, dev, stream);
+  };
+  return chunk ? go(std::true_type()) : go(std::false_type());
 }
 
 }  // namespace bw

@@ -406,6 +406,103 @@ int kv_append_paged_fp8(const void* k_new, const void* v_new, const int32_t* slo
                         int num_rows, int page_size, int num_pages, int Hkv, int d, int64_t k_new_stride,
                         int64_t v_new_stride, void* stream);
 
+/* ---- around a paged cache's attention: chunks, norm and rotation, verification ---- */
+
+/*
+ * attn_chunk_workspace_size: bytes of workspace attn_chunk_paged needs, from the host-side bounds it is
+ * given (0 for sizes it refuses).
+ */
+size_t attn_chunk_workspace_size(int num_seqs, int max_seqlen_q, int Hq, int Hkv, int d);
+
+/*
+ * attn_chunk_paged: attention of new tokens over a paged cache that holds their own keys and values too (a
+ * chunk of a prompt behind what is cached already, a decode step, or both mixed in a batch). ("Attention
+ * Computation in Practice", section 5, kernel class 3 over "PagedAttention's kernel difference".)
+ *
+ *   q, o         : [total_q, Hq, d] bf16, sequence s owns rows cu_seqlens_q[s] .. cu_seqlens_q[s+1]-1;
+ *                  consecutive rows of q lie q_stride elements apart (heads d apart; o is contiguous)
+ *   k_pages,
+ *   v_pages, block_table : the cache in the layouts of attn_decode_paged
+ *   nk           : [num_seqs] int32 DEVICE array, keys per sequence in the cache, those of the new tokens
+ *                  among them, 0 <= nk[s] <= max_pages_per_seq * page_size
+ *   cu_seqlens_q : [num_seqs + 1] int32 DEVICE array, non-decreasing, [0] = 0; rows of q behind
+ *                  cu_seqlens_q[num_seqs] belong to no sequence, their o and lse are left as they were
+ *   total_q      : host-side row count of q
+ *   max_seqlen_q : host-side upper bound of the new tokens of a sequence; a longer sequence is not
+ *                  processed correctly
+ *   causal       : 1 = causal aligned to each sequence's end; 0 = every token sees all nk keys (an encoder's
+ *                  states in pages)
+ *   lse          : [total_q, Hq] fp32, may be NULL
+ *   workspace    : at least attn_chunk_workspace_size(...) bytes; contents undefined on exit. Must not be
+ *                  shared by calls that may overlap on the GPU
+ * Keys and values that a token does not see have no effect on its outputs, whatever they hold (infinities
+ * and NaN included). Accuracy as for attn_tree. Supported: d in {64, 128, 256}, Hq / Hkv <= 128. q_stride is a
+ * multiple of 8 and at least Hq * d, else INVALID_ARG; other errors as for attn_decode_paged.
+ */
+int attn_chunk_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* block_table, void* o, float* lse,
+                     const int32_t* nk, const int32_t* cu_seqlens_q, int num_seqs, int total_q, int max_seqlen_q,
+                     int page_size, int num_pages, int max_pages_per_seq, int Hq, int Hkv, int d, int64_t q_stride, int causal,
+                     float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * attn_qk_norm_rope: q and k for attention from a projection's rows: each head normalised, then rotated by
+ * its row's position.
+ *
+ *   q, q_out     : [num_rows, Hq, d] bf16, consecutive rows q_stride / q_out_stride elements apart (heads d apart)
+ *   k, k_out     : [num_rows, Hkv, d] bf16, likewise. q_out = q and k_out = k (with the same strides) work in
+ *                  place; outputs must not overlap inputs otherwise
+ *   q_weight,
+ *   k_weight     : [d] bf16 DEVICE arrays, 16-byte aligned: x_c becomes x_c * weight_c / sqrt(mean(x^2) + eps), the
+ *                  mean over the head's d channels. NULL: x is not normalised
+ *   inv_freq     : [pairs] fp32 DEVICE array, radians per position of each pair of channels, 0 <= pairs <= d / 2
+ *   positions    : [num_axes, num_rows] int32 DEVICE array (any value, negative ones too)
+ *   axes         : [pairs] int32 DEVICE array, which row of positions turns the pair (values are clamped to
+ *                  [0, num_axes)), or NULL: the first
+ *   interleaved  : 0 = pair i is channels (i, i + pairs); 1 = channels (2 i, 2 i + 1). Channels from 2 * pairs on are
+ *                  not rotated
+ * A pair (a, b) becomes (a cos t - b sin t, a sin t + b cos t), t = position * inv_freq as real numbers: the angle
+ * is reduced to a turn before it is rounded, so far positions lose nothing. fp32 arithmetic, one rounding
+ * to bf16. Supported: d in {64, 128, 256}. Strides are multiples of 8 and at least a row, else INVALID_ARG, as is a
+ * negative or infinite eps.
+ */
+int attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions, const int32_t* axes,
+                      const float* inv_freq, const void* q_weight, const void* k_weight, float eps, int num_rows,
+                      int num_axes, int pairs, int interleaved, int Hq, int Hkv, int d, int64_t q_stride, int64_t k_stride,
+                      int64_t q_out_stride, int64_t k_out_stride, void* stream);
+
+/*
+ * attn_tree_verify: which drafts of each request's tree are kept, and the token behind them, distributed as
+ * tokens drawn one by one from the target's probabilities. Node 0 of a request is its root, the token decided
+ * last, which is always kept (a request's other roots are never reached).
+ *
+ *   tokens, parents : [total_q] int32, the nodes' tokens and parent links (as for attn_tree_mask). Nodes
+ *                  whose token is outside [0, vocab) are passed over
+ *   cu_seqlens_q : as for attn_tree
+ *   target_probs : [total_q, vocab] fp32, rows target_stride elements apart: row i is the target's distribution
+ *                  of the token behind node i. Values outside [0, 1] count as the nearer end, NaN as 0
+ *   draft_probs  : the distributions that the children of node i were drawn from, independently and in their
+ *                  order, likewise in row i; or NULL: the drafts were not drawn (the most probable tokens, say)
+ *   uniforms     : [total_q] fp32 in [0, 1), the number that decides on node i
+ *   sample_uniforms : [num_seqs] fp32 in [0, 1), for the token behind the path
+ *   accepted     : [total_q] int32, written: accepted[cu_seqlens_q[s] + j] is the packed row of the j-th node of the
+ *                  kept path of request s, root first; -1 behind the path and in rows that belong to no request
+ *                  (with kv_plan_paged's slots: the `rows` of kv_append_paged)
+ *   counts       : [num_seqs] int32, written: nodes of the path (0 for a request without nodes)
+ *   next_tokens  : [num_seqs] int32, written: the token behind the path (-1 for a request without nodes, and
+ *                  where the target's row has no probabilities at all)
+ * From the root on, with p (q) the last kept node's row and r = p, S = 1, A = 0: its children are tried in the order of
+ * their rows. With draft_probs, child i of token t is kept iff u_i S q(t) < r(t), else A grows by S, r becomes
+ * max(p - A q, 0) and S its sum. Without, it is kept iff u_i S < r(t), else S falls by r(t) (not below 0) and r(t)
+ * becomes 0. Behind the last kept node comes the first token whose running sum of r exceeds w times r's sum (of
+ * p's, where r is all 0), w < 1 the request's sample_uniform. Sums are taken of values rounded to
+ * 2^-44, in integers: the same whatever the launch. Supported: vocab <= 500000, max_nodes <= 1024 (further nodes
+ * of a request are not tried). Strides at least vocab; outputs in an input's place: INVALID_ARG.
+ */
+int attn_tree_verify(const int32_t* tokens, const int32_t* parents, const int32_t* cu_seqlens_q, const float* target_probs,
+                     const float* draft_probs, const float* uniforms, const float* sample_uniforms, int32_t* accepted,
+                     int32_t* counts, int32_t* next_tokens, int num_seqs, int total_q, int max_nodes, int vocab,
+                     int64_t target_stride, int64_t draft_stride, void* stream);
+
 /* ---- status and diagnostics ---- */
 
 /* The cudaError_t of the last failing CUDA call made by this thread inside the library (0 if none). */
