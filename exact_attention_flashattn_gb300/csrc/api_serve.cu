@@ -137,8 +137,8 @@ int attn_tree_verify(const int32_t* tokens, const int32_t* parents, const int32_
   for (const void* y : out)
     for (const void* x : in)
       if (x && x == y) return BWATTN_ERR_INVALID_ARG;
-  const bw::VerifyArgs a{tokens, parents, cu_seqlens_q, target_probs, draft_probs, uniforms, sample_uniforms, accepted, counts,
-                         next_tokens, target_stride, draft_stride, num_seqs, total_q, max_nodes, vocab};
+  bw::VerifyArgs a{tokens, parents, cu_seqlens_q, target_probs, draft_probs, uniforms, sample_uniforms, accepted, counts,
+                         next_tokens, target_stride, draft_stride, num_seqs, total_q, max_nodes, vocab, nullptr, 0};
   const cudaError_t e = bw::launch_tree_verify(a, static_cast<cudaStream_t>(stream));
   if (e == cudaSuccess) bw::count_launch();
   return done(e);

@@ -314,8 +314,10 @@ struct VerifyArgs {
   int32_t* next;           // [num_seqs]
   int64_t p_stride, q_stride;
   int num_seqs, total_q, max_nodes, vocab;
+  unsigned int* status;
+  uint64_t timeout_ns;
 };
-cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t stream);
+cudaError_t launch_tree_verify(VerifyArgs& a, cudaStream_t stream);
 
 // Timeout self-test: one CTA waits on a barrier that is never arrived at.
 cudaError_t launch_wait_timeout_probe(uint64_t timeout_ns, unsigned int* status, cudaStream_t stream);

@@ -4,10 +4,15 @@
 // pairs (c, c + pairs) or, interleaved, (2 c, 2 c + 1); the position comes from the pair's axis (time, height,
 // width). Channels behind the pairs are normalised only. 32 bits in between, rounded to bf16 once.
 //
-// What bounds it: every value is read and written once, 4 bytes each. A warp takes whole rows, some heads of
-// one at a time: d / 16 lanes a head, each with two pieces of 8 channels that hold both halves of its pairs,
-// so rotating needs no exchange.
+// What bounds it: every value is read and written once, 4 bytes each, and few instructions may be spent on them.
+// A warp takes whole rows, some heads a turn: d / 16 lanes a head, each with two pieces of 8 channels that hold both
+// halves of its pairs, so rotating needs no exchange. Weights, cosines and sines are multiplied once a row: an
+// output is r (x C + other S), with r the head's 1 / sqrt and `other` the pair's other channel, in packed pairs of
+// 32 bits. The coming turns' values are copied to shared memory meanwhile. 16384 rows of 32 + 8 heads of 128: 55.7 us,
+// 6.0 TB/s (weights and rotation apart, in single values: 78 us and 2400 instructions a row; a row shared by a
+// block's warps, with a barrier a row: 59.6; five blocks an SM in 96 registers: 59.7).
 #include "kernels.h"
+#include "packed.cuh"
 #include "ptx.cuh"
 
 namespace bw {
@@ -19,12 +24,23 @@ constexpr int kRopeThreads = 128;
 
 enum RopeMode { kHalves, kAdjacent, kHalvesAny };  // kHalvesAny: pairs no multiple of 8
 
-// A rotation's angle in turns is position * frequency / 2 pi modulo 1: with the frequency as a fraction of 2^64
-// the product of integers wraps to just that, however far the position. The frequency's own rounding, 2^-53 of
-// it, is off by less than the angle's rounding to 32 bits up to positions of 2^28 or so.
+// A rotation's angle in turns is position * frequency / 2 pi modulo 1: with frequency / 2 pi as a fraction of 2^64
+// the product of integers wraps to just that, however far the position. The frequency's 24 bits times 1 / 2 pi
+// in 2^-64ths, shifted by its exponent: off by 2^-39 of itself and 2^-64 of a turn at most.
 __device__ __forceinline__ uint64_t turn_of(float freq) {
-  const double t = static_cast<double>(freq) * 0.15915494309189535;  // 1 / 2 pi
-  return __double2ull_rd((t - floor(t)) * 0x1p64);
+  constexpr uint64_t kInvTwoPi = 0x28be60db9391054aull;  // 1 / 2 pi, in 2^-64ths
+  const uint32_t bits = __float_as_uint(freq), e = bits >> 23 & 255;
+  const uint64_t m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
+  const int down = 150 - static_cast<int>(e ? e : 1);  // freq = m 2^-down
+  const uint64_t lo = m * kInvTwoPi, hi = __umul64hi(m, kInvTwoPi);
+  uint64_t t;
+  if (down <= 0)
+    t = -down < 64 ? lo << -down : 0;
+  else if (down < 64)
+    t = lo >> down | hi << (64 - down);
+  else
+    t = down < 128 ? hi >> (down - 64) : 0;
+  return bits >> 31 ? 0 - t : t;
 }
 __device__ __forceinline__ float2 cos_sin(int position, uint64_t turn) {
   const uint64_t x = static_cast<uint64_t>(static_cast<int64_t>(position)) * turn;
@@ -33,151 +49,179 @@ __device__ __forceinline__ float2 cos_sin(int position, uint64_t turn) {
   return make_float2(c, s);
 }
 
-__device__ __forceinline__ void unpack(const uint4& u, float* x) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[2 * e] = __uint_as_float(w[e] << 16);
-    x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ uint4 pack(const float* x) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-}
+__device__ __forceinline__ pair_t unpack(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+__device__ __forceinline__ uint32_t pack(pair_t x) { return pack_bf16x2(first(x), second(x)); }
+__device__ __forceinline__ float bf16(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+
+// A warp takes a row's heads (or one of `gridDim.y` parts of them), kHeads a turn, and then another row's.
+constexpr int kRing = 4;        // turns that a warp has under way
+constexpr int kRopeBlocks = 4;  // an SM
 
 template <int D, int kMode>
-__global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeArgs a, int parts, int per_part) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) qk_rope_kernel(const RopeArgs a, int per_part) {
   constexpr int kLanes = D / 16, kHeads = 32 / kLanes;  // lanes a head, heads a turn
-  constexpr int kPairs = D / 2, kMine = kPairs / 32;    // table entries, a lane's
-  constexpr int kWarps = kRopeThreads / 32;
-  __shared__ float2 sm_table[kWarps][kPairs];
-  __shared__ float sm_x[kMode == kHalvesAny ? kWarps : 1][kMode == kHalvesAny ? kHeads : 1][kMode == kHalvesAny ? D : 1];
+  constexpr int kWarps = kRopeThreads / 32, kMine = D / 64;  // kMine: a lane's pairs
+  __shared__ __align__(16) float sm_coef[kWarps][2][2][D];  // C and S of q's channels and of k's
+  __shared__ __align__(16) float sm_x[kMode == kHalvesAny ? kWarps : 1][kMode == kHalvesAny ? kHeads : 1][kMode == kHalvesAny ? D : 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t = lane % kLanes, group = lane / kLanes;
-  float2* table = sm_table[warp];
-  // what a lane keeps over its rows: the turns of its table entries, the weights of its channels
-  uint64_t turn[kMine];
-  int axis[kMine];
+  // turns: of q's heads first, then of k's; the part's
+  const int q_turns = (a.Hq + kHeads - 1) / kHeads, turns = q_turns + (a.Hkv + kHeads - 1) / kHeads;
+  const int turn0 = static_cast<int>(blockIdx.y) * per_part, turn1 = min(turn0 + per_part, turns);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  if (row >= a.num_rows) return;
+  // the two pieces: both halves of 8 pairs, or neighbours among the channels that are not turned
+  const int half = a.pairs / 8;
+  const bool turned = kMode != kHalves || t < half;
+  const int pa = turned ? t : 2 * t, pb = kMode != kHalves ? t + kLanes : turned ? t + half : 2 * t + 1;
+  // The coming turns' values are copied to shared memory, over the ends of rows; a lane reads what it copied itself.
+  extern __shared__ uint4 sm_raw[];
+  uint4* ring = sm_raw + warp * (kRing * 64) + lane;
+  int64_t f_row = row;
+  int f_turn = turn0, f_slot = 0;
+  auto fetch = [&]() {
+    const bool is_k = f_turn >= q_turns;
+    const int head = (is_k ? f_turn - q_turns : f_turn) * kHeads + group;
+    if (f_row < a.num_rows && head < (is_k ? a.Hkv : a.Hq)) {
+      const uint4* src = reinterpret_cast<const uint4*>((is_k ? a.k + f_row * a.k_stride : a.q + f_row * a.q_stride) + head * D);
+      uint4* dst = ring + f_slot * 64;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src + pa) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst + 32)), "l"(src + pb) : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    f_slot = f_slot + 1 == kRing ? 0 : f_slot + 1;
+    if (++f_turn == turn1) f_turn = turn0, f_row += step;
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) fetch();
+  // a lane's pairs: their channels, the channels' weights, the turns a position, the next row's position
+  int axis_row[kMine] = {}, pos[kMine];
+  uint64_t my_turn[kMine];
+  auto position = [&](int i, int64_t r) {
+    return 32 * i + lane < a.pairs && r < a.num_rows ? a.positions[static_cast<int64_t>(axis_row[i]) * a.num_rows + r] : 0;
+  };
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
-    const int pair = 32 * i + lane;
-    turn[i] = pair < a.pairs ? turn_of(a.freq[pair]) : 0;
-    axis[i] = pair < a.pairs && a.axes ? min(max(a.axes[pair], 0), a.num_axes - 1) : 0;
+    const int p = 32 * i + lane;
+    my_turn[i] = p < a.pairs ? turn_of(a.freq[p]) : 0;
+    axis_row[i] = p < a.pairs && a.axes ? min(max(a.axes[p], 0), a.num_axes - 1) : 0;
+    pos[i] = position(i, row);
   }
-  // the two pieces: both halves of 8 pairs, or neighbours among the channels that are not turned
-  const int p8 = a.pairs / 8;
-  const int pa = kMode == kHalves ? (t < p8 ? t : 2 * t) : t;
-  const int pb = kMode == kHalves ? (t < p8 ? t + p8 : 2 * t + 1) : t + kLanes;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  uint4 wq[2] = {zero, zero}, wk[2] = {zero, zero};
-  if (a.q_weight) {
-    wq[0] = reinterpret_cast<const uint4*>(a.q_weight)[pa];
-    wq[1] = reinterpret_cast<const uint4*>(a.q_weight)[pb];
-  }
-  if (a.k_weight) {
-    wk[0] = reinterpret_cast<const uint4*>(a.k_weight)[pa];
-    wk[1] = reinterpret_cast<const uint4*>(a.k_weight)[pb];
-  }
-  const int heads = a.Hq + a.Hkv;
-  const int64_t items = static_cast<int64_t>(a.num_rows) * parts;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp; item < items; item += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t row = item / parts;
-    const int h0 = static_cast<int>(item - row * parts) * per_part, h1 = min(h0 + per_part, heads);
-    __syncwarp();  // the last row's table has been read
+  for (int c = 2 * a.pairs + lane; c < D; c += 32) {  // channels that are not turned
 #pragma unroll
-    for (int i = 0; i < kMine; ++i)
-      // a pair that is not turned: (1, 0)
-      table[32 * i + lane] = 32 * i + lane < a.pairs
-                                 ? cos_sin(a.positions[static_cast<int64_t>(axis[i]) * a.num_rows + row], turn[i])
-                                 : make_float2(1.f, 0.f);
-    __syncwarp();
-    float2 cs[8];
-    if constexpr (kMode != kHalvesAny) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) cs[e] = table[kMode == kHalves ? 8 * t + e : 4 * (e < 4 ? pa : pb) + (e & 3)];
+    for (int k = 0; k < 2; ++k) {
+      const uint16_t* weight = k ? a.k_weight : a.q_weight;
+      sm_coef[warp][k][0][c] = weight ? bf16(weight[c]) : 1.f;
+      sm_coef[warp][k][1][c] = 0.f;
     }
-#pragma unroll 2
-    for (int h = h0; h < h1; h += kHeads) {
-      const int head = h + group;
-      const bool is = head < h1, is_k = head >= a.Hq;
-      const uint16_t* src = is_k ? a.k + row * a.k_stride + (head - a.Hq) * D : a.q + row * a.q_stride + head * D;
-      uint4 u[2] = {zero, zero};
-      if (is) {
-        u[0] = reinterpret_cast<const uint4*>(src)[pa];
-        u[1] = reinterpret_cast<const uint4*>(src)[pb];
-      }
-      float x[16];
-      unpack(u[0], x);
-      unpack(u[1], x + 8);
-      const bool norm = is_k ? a.k_weight != nullptr : a.q_weight != nullptr;
-      float ss = 0.f;
+  }
+  int slot = 0;
+#pragma unroll 1
+  for (; row < a.num_rows; row += step) {
+    __syncwarp();  // the last row's coefficients have been read
 #pragma unroll
-      for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+    for (int i = 0; i < kMine; ++i) {
+      const int p = 32 * i + lane;
+      if (p < a.pairs) {
+        const float2 v = cos_sin(pos[i], my_turn[i]);
+        const int c0 = kMode == kAdjacent ? 2 * p : p, c1 = kMode == kAdjacent ? 2 * p + 1 : p + a.pairs;
 #pragma unroll
-      for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-      if (norm) {
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
-        float w[16];
-        unpack(is_k ? wk[0] : wq[0], w);
-        unpack(is_k ? wk[1] : wq[1], w + 8);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = x[e] * r * w[e];
-      }
-      float y[16];
-      if constexpr (kMode == kHalves) {
-        const bool turned = t < p8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          y[e] = turned ? x[e] * cs[e].x - x[e + 8] * cs[e].y : x[e];
-          y[e + 8] = turned ? x[e] * cs[e].y + x[e + 8] * cs[e].x : x[e + 8];
+        for (int k = 0; k < 2; ++k) {
+          const uint16_t* weight = k ? a.k_weight : a.q_weight;
+          const float w0 = weight ? bf16(weight[c0]) : 1.f, w1 = weight ? bf16(weight[c1]) : 1.f;
+          sm_coef[warp][k][0][c0] = v.x * w0, sm_coef[warp][k][1][c0] = -v.y * w1;
+          sm_coef[warp][k][0][c1] = v.x * w1, sm_coef[warp][k][1][c1] = v.y * w0;
         }
-      } else if constexpr (kMode == kAdjacent) {
+      }
+      pos[i] = position(i, row + step);
+    }
+    __syncwarp();
+    pair_t C[8], S[8];
+#pragma unroll 1
+    for (int turn = turn0; turn < turn1; ++turn) {
+      const bool is_k = turn >= q_turns;
+      if (turn == turn0 || turn == q_turns) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const bool turned = 4 * (e < 4 ? pa : pb) + (e & 3) < a.pairs;
-          y[2 * e] = turned ? x[2 * e] * cs[e].x - x[2 * e + 1] * cs[e].y : x[2 * e];
-          y[2 * e + 1] = turned ? x[2 * e] * cs[e].y + x[2 * e + 1] * cs[e].x : x[2 * e + 1];
+        for (int i = 0; i < 4; ++i) {
+          const int c = 8 * (i < 2 ? pa : pb) + 4 * (i & 1);
+          const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&sm_coef[warp][is_k][0][c]);
+          const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(&sm_coef[warp][is_k][1][c]);
+          C[2 * i] = x.x, C[2 * i + 1] = x.y, S[2 * i] = y.x, S[2 * i + 1] = y.y;
         }
-      } else {
+      }
+      fetch();
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+      pair_t x[8], other[8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 raw = ring[slot * 64 + 32 * i];
+        x[4 * i] = unpack(raw.x), x[4 * i + 1] = unpack(raw.y);
+        x[4 * i + 2] = unpack(raw.z), x[4 * i + 3] = unpack(raw.w);
+      }
+      slot = slot + 1 == kRing ? 0 : slot + 1;
+      if constexpr (kMode == kHalvesAny) {
         float* sx = sm_x[warp][group];
         __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sx[8 * (e < 8 ? pa : pb) + (e & 7)] = x[e];
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float2*>(sx + 8 * (i < 4 ? pa : pb) + 2 * (i & 3)) = make_float2(first(x[i]), second(x[i]));
         __syncwarp();
+        auto partner = [&](int c) { return c < a.pairs ? sx[c + a.pairs] : c < 2 * a.pairs ? sx[c - a.pairs] : 0.f; };
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int c = 8 * (e < 8 ? pa : pb) + (e & 7);
-          y[e] = x[e];
-          if (c < a.pairs) {
-            y[e] = x[e] * table[c].x - sx[c + a.pairs] * table[c].y;
-          } else if (c < 2 * a.pairs) {
-            y[e] = sx[c - a.pairs] * table[c - a.pairs].y + x[e] * table[c - a.pairs].x;
-          }
+        for (int i = 0; i < 8; ++i) {
+          const int c = 8 * (i < 4 ? pa : pb) + 2 * (i & 3);
+          other[i] = pair(partner(c), partner(c + 1));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) other[i] = kMode == kHalves ? x[i ^ 4] : pair(second(x[i]), first(x[i]));
+        if (2 * a.pairs < D) {
+          // 0 times an infinity or NaN of another channel would reach one that is not turned
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (kMode == kHalves ? !turned : 4 * (i < 4 ? pa : pb) + (i & 3) >= a.pairs) other[i] = 0;
         }
       }
-      if (is) {
-        uint16_t* dst = is_k ? a.k_out + row * a.k_out_stride + (head - a.Hq) * D : a.q_out + row * a.q_out_stride + head * D;
-        reinterpret_cast<uint4*>(dst)[pa] = pack(y);
-        reinterpret_cast<uint4*>(dst)[pb] = pack(y + 8);
+      if (is_k ? a.k_weight : a.q_weight) {
+        pair_t sum = mul(x[0], x[0]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) sum = fma(x[i], x[i], sum);
+        float ss = first(sum) + second(sum);
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        const pair_t rr = pair(r, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = mul(x[i], rr), other[i] = mul(other[i], rr);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = fma(other[i], S[i], mul(x[i], C[i]));
+      const int head = (is_k ? turn - q_turns : turn) * kHeads + group;
+      if (head < (is_k ? a.Hkv : a.Hq)) {
+        uint4* dst = reinterpret_cast<uint4*>((is_k ? a.k_out + row * a.k_out_stride : a.q_out + row * a.q_out_stride) + head * D);
+        dst[pa] = make_uint4(pack(x[0]), pack(x[1]), pack(x[2]), pack(x[3]));
+        dst[pb] = make_uint4(pack(x[4]), pack(x[5]), pack(x[6]), pack(x[7]));
       }
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <int D>
 cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
   constexpr int kHeads = 512 / D, kWarps = kRopeThreads / 32;
-  const int turns = (a.Hq + a.Hkv + kHeads - 1) / kHeads;
+  const int turns = (a.Hq + kHeads - 1) / kHeads + (a.Hkv + kHeads - 1) / kHeads;
   // a row's heads go to several warps where there are too few rows to fill the SMs
-  const int64_t want = static_cast<int64_t>(kSms) * 32;
-  int parts = static_cast<int>(want / a.num_rows < 1 ? 1 : want / a.num_rows);
-  if (parts > turns) parts = turns;
-  const int per_turns = (turns + parts - 1) / parts;
-  parts = (turns + per_turns - 1) / per_turns;
-  const int64_t blocks = (static_cast<int64_t>(a.num_rows) * parts + kWarps - 1) / kWarps;
-  const dim3 grid(static_cast<unsigned>(blocks < kSms * 16 ? blocks : kSms * 16));
-  auto go = [&](auto kernel) { return launch_dependent(kernel, grid, kRopeThreads, 0, stream, a, parts, per_turns * kHeads); };
+  const int64_t most = kSms * kRopeBlocks * kWarps;
+  int parts = static_cast<int>(most / a.num_rows);
+  parts = parts < 1 ? 1 : parts > turns ? turns : parts;
+  const int per_part = (turns + parts - 1) / parts;
+  parts = (turns + per_part - 1) / per_part;
+  const int blocks = (a.num_rows + kWarps - 1) / kWarps, room = kSms * kRopeBlocks / parts;
+  const dim3 grid(blocks < room || room < 1 ? blocks : room, parts);
+  auto go = [&](auto kernel) { return launch_dependent(kernel, grid, kRopeThreads, kWarps * kRing * 1024, stream, a, per_part); };
   if (a.interleaved) return go(qk_rope_kernel<D, kAdjacent>);
   if (a.pairs % 8 == 0) return go(qk_rope_kernel<D, kHalves>);
   return go(qk_rope_kernel<D, kHalvesAny>);

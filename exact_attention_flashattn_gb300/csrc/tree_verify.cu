@@ -14,10 +14,14 @@
 // to a multiple of 2^-44 once (r itself in two floats, whose error is far below), and integers are summed. 64 bits
 // in place of that would be 64 times slower than the loads on this card.
 //
-// What bounds it: one row of p (and of q) a request, V values, and the latency of the walk for few requests.
-// A cluster of CTAs takes a request, each a part of the row; all of them walk the tree alike, from values
-// gathered at once, and exchange their sums through distributed shared memory.
+// What bounds it: one row of p (and of q) a request, V values, and for few requests the latency of what follows one
+// another: lengths, links and tokens, their probabilities, the walk, the row, its sums, the border. A cluster of CTAs
+// takes a request, each a part of the row; all of them walk the tree alike and send one another their sums. 64 trees
+// over 131072 tokens: 11.3 us, 3.0 TB/s, of which the row takes 6 (with cluster barriers around the sums, a second
+// pass over a warp's run for the border and the walk in 64 bits: 25 us). A request whose drafts are refused one by
+// one takes a sum each, 6 us over 151007 tokens, which 40 drawn trees' 33 us end with.
 #include "kernels.h"
+#include "packed.cuh"
 #include "ptx.cuh"
 
 namespace bw {
@@ -27,29 +31,47 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxNodes = kTreeMaxNodes;
-constexpr int kBatch = 8;  // vectors of a row that a lane has under way
+constexpr int ctas(bool drawn) { return drawn ? 3 : 4; }  // an SM
+constexpr int kBatch = 4;  // pieces of a row that a lane has under way
 
 // Values in [0, 1] (NaN and negative ones: 0, larger ones: 1).
 __device__ __forceinline__ float unit(float x) { return __saturatef(x); }
 
-// A non-negative value hi + lo, lo far below hi, as a multiple of 2^-44: `big` 2^-22ths, `small` the rest. Adding
-// 3 (1.5 * 2^-21) rounds to a multiple of 2^-22 (2^-44), which then stands in the last bits.
+// A non-negative value x as a multiple of 2^-44: `big` 2^-22ths, `small` the rest. Adding 3 (1.5 * 2^-21) rounds to a
+// multiple of 2^-22 (2^-44), which then stands in the last bits.
 struct Fixed {
   int big, small;
 };
-__device__ __forceinline__ Fixed fixed(float hi, float lo) {
-  const float a = hi + 3.f, rest = (hi - (a - 3.f)) + lo, b = rest + 0x1.8p-21f;
-  return {__float_as_int(a) - __float_as_int(3.f), __float_as_int(b) - __float_as_int(0x1.8p-21f)};
-}
 __device__ __forceinline__ int64_t whole(Fixed f) { return (static_cast<int64_t>(f.big) << 22) + f.small; }
 
-// max(p - A q, 0) with A = a_hi + a_lo
-__device__ __forceinline__ Fixed residual(float p, float q, float a_hi, float a_lo) {
-  const float m = __fmul_rn(a_hi, q), m_lo = fmaf(a_lo, q, fmaf(a_hi, q, -m));  // A q = m + m_lo
-  const float s = __fsub_rn(p, m), back = __fsub_rn(s, p);
-  const float err = __fadd_rn(__fsub_rn(p, __fsub_rn(s, back)), __fsub_rn(-m, back));  // p - m = s + err
-  const float lo = err - m_lo;
-  return s + lo > 0.f ? fixed(s, lo) : Fixed{0, 0};
+// Four values of r = max(p - A q, 0), A = a_hi + a_lo (kDrawn and A not 0), or r = p, each as a multiple of 2^-44
+template <bool kDrawn>
+__device__ __forceinline__ void four(const float (&p)[4], const float (&q)[4], float a_hi, float a_lo, Fixed (&f)[4]) {
+  constexpr float kBig = 3.f, kSmall = 0x1.8p-21f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const pair_t x = pair(unit(p[2 * i]), unit(p[2 * i + 1]));
+    pair_t s = x, lo = 0;
+    if (kDrawn && a_hi != 0.f) {
+      const pair_t y = pair(unit(q[2 * i]), unit(q[2 * i + 1])), hi2 = pair(a_hi, a_hi);
+      const pair_t m = mul(pair(-a_hi, -a_hi), y);                         // A q = -m + m_lo
+      const pair_t m_lo = fma(pair(a_lo, a_lo), y, fma(hi2, y, m));
+      s = add(x, m);
+      const pair_t back = sub(s, x);                                       // x + m = s + what follows, exactly
+      lo = sub(add(sub(x, sub(s, back)), sub(m, back)), m_lo);
+    }
+    const pair_t a = add(s, pair(kBig, kBig)), rest = add(sub(s, add(a, pair(-kBig, -kBig))), lo), b = add(rest, pair(kSmall, kSmall));
+    const bool some0 = !kDrawn || first(s) > -first(lo), some1 = !kDrawn || second(s) > -second(lo);
+    f[2 * i] = Fixed{some0 ? __float_as_int(first(a)) - __float_as_int(kBig) : 0, some0 ? __float_as_int(first(b)) - __float_as_int(kSmall) : 0};
+    f[2 * i + 1] = Fixed{some1 ? __float_as_int(second(a)) - __float_as_int(kBig) : 0,
+                         some1 ? __float_as_int(second(b)) - __float_as_int(kSmall) : 0};
+  }
+}
+__device__ __forceinline__ int64_t fixed(float p) {  // the same of one p
+  const float x[4] = {p, 0.f, 0.f, 0.f};
+  Fixed f[4];
+  four<false>(x, x, 0.f, 0.f, f);
+  return whole(f[0]);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -57,13 +79,21 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+// v to *p of the cluster's CTA `rank`, where its arrival counts as 8 bytes on *bar
+__device__ __forceinline__ void send(int64_t* p, uint64_t* bar, uint32_t rank, int64_t v) {
+  asm volatile(
+      "{\n\t.reg .b32 ra, rb;\n\tmapa.shared::cluster.u32 ra, %0, %2;\n\tmapa.shared::cluster.u32 rb, %1, %2;\n\t"
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [ra], %3, [rb];\n\t}" ::"r"(smem_u32(p)),
+      "r"(smem_u32(bar)), "r"(rank), "l"(v)
+      : "memory");
 }
-__device__ __forceinline__ void store_remote(void* p, uint32_t rank, int64_t v) {
-  asm volatile("{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %0, %1;\n\tst.shared::cluster.b64 [ra], %2;\n\t}" ::"r"(smem_u32(p)),
-               "r"(rank), "l"(v)
-               : "memory");
+// floor(w x) of a number w in [0, 1)
+__device__ __forceinline__ int64_t part_of(float w, int64_t x) {
+  const uint32_t bits = __float_as_uint(w), e = bits >> 23;
+  const uint64_t m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;  // w = m 2^-down, down at least 24
+  const int down = 150 - static_cast<int>(e ? e : 1);
+  const uint64_t lo = m * static_cast<uint64_t>(x), hi = __umul64hi(m, static_cast<uint64_t>(x));
+  return static_cast<int64_t>(down < 64 ? lo >> down | hi << (64 - down) : down < 128 ? hi >> (down - 64) : 0);
 }
 
 // One row (or, with draft probabilities, two) of V values, in pieces of 4 that begin on 16 bytes. The first and
@@ -98,37 +128,52 @@ struct Row {
 __device__ __forceinline__ int run_of(int pieces, int cluster) { return (pieces + 32 * kWarps * cluster - 1) / (32 * kWarps * cluster) * 32; }
 
 template <bool kDrawn>
-__device__ __forceinline__ void load_batch(const Row& row, int piece, int end, float (&p)[kBatch][4], float (&q)[kDrawn ? kBatch : 1][4]) {
+__device__ __forceinline__ void load_piece(const Row& row, bool with_q, int piece, int end, float (&p)[4], float (&q)[4]) {
 #pragma unroll
-  for (int i = 0; i < kBatch; ++i, piece += 32) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) p[i][e] = 0.f;
-    if constexpr (kDrawn)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) q[i][e] = 0.f;
-    if (piece < end) {
-      row.load(row.p, piece, true, p[i]);
-      if constexpr (kDrawn) row.load(row.q, piece, row.q_alike, q[i]);
-    }
+  for (int e = 0; e < 4; ++e) p[e] = q[e] = 0.f;
+  if (piece < end) {
+    row.load(row.p, piece, true, p);
+    if (kDrawn && with_q) row.load(row.q, piece, row.q_alike, q);
   }
 }
 
 enum State { kSum, kReady };  // r has to be summed; the walk is over and r's sums are there
 
+constexpr int kMaxGroups = (kVerifyMaxVocab / 4 + 1 + 32 * kWarps * kMaxCluster - 1) / (32 * kWarps * kMaxCluster);
+
 struct Shared {
-  int64_t part[2][kMaxCluster];  // the CTAs' sums, of two sums in turns
+  uint64_t arrived[2];           // the CTAs' sums, of two sums in turns
+  int64_t part[2][kMaxCluster];
   int64_t warp_sum[kWarps];
+  int64_t group[kWarps][kMaxGroups];  // of 32 pieces each, a warp's run
   int parent[kMaxNodes];  // -1: not to be tried
   int token[kMaxNodes];
   float u[kMaxNodes], p[kMaxNodes], q[kMaxNodes];  // p and q: of the node's token behind its parent
   int path[kMaxNodes];
   int refused[kMaxNodes];  // different tokens refused behind the path's last node
-  int count, num_refused, state;
-  double A;
+  int count, num_refused, state, abort;
+  float a_hi, a_lo;
 };
 
+// The sums over the warp of N values a lane: value i is then in lanes 32 / N i .. 32 / N (i + 1) - 1.
+template <int N>
+__device__ __forceinline__ int64_t sums_of(int64_t (&x)[N], int lane) {
+#pragma unroll
+  for (int n = N, off = 16; n > 1; n /= 2, off /= 2) {
+    const bool upper = lane & off;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const int64_t give = upper ? x[i] : x[i + n / 2], keep = upper ? x[i + n / 2] : x[i];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+    }
+  }
+#pragma unroll
+  for (int off = 16 / N; off > 0; off /= 2) x[0] += __shfl_xor_sync(0xffffffffu, x[0], off);
+  return x[0];
+}
+
 template <bool kDrawn>
-__global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyArgs a, int cluster) {
+__global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(const VerifyArgs a, int cluster) {
   __shared__ Shared sm;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -150,6 +195,14 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyArgs 
     }
     return;
   }
+  if (tid == 0) {
+    mbar_init(&sm.arrived[0], 1);
+    mbar_init(&sm.arrived[1], 1);
+    sm.abort = 0;
+    sm.path[0] = 0;
+    fence_mbar_init();
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // waited for before the first sum is sent
   for (int i = tid; i < n; i += kThreads) {
     const int up = i > 0 ? a.parents[t0 + i] : -1, t = a.tokens[t0 + i];
     const bool real = up >= 0 && up < i && t >= 0 && t < a.vocab;
@@ -159,12 +212,12 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyArgs 
     sm.p[i] = real ? unit(a.p[static_cast<int64_t>(t0 + up) * a.p_stride + t]) : 0.f;
     if (kDrawn) sm.q[i] = real ? unit(a.q[static_cast<int64_t>(t0 + up) * a.q_stride + t]) : 0.f;
   }
-  if (tid == 0) sm.path[0] = 0;
   __syncthreads();
 
   // the walk's state (warp 0, its lanes alike)
   int next = 1, last = 0, count = 1, refused = 0;
   double A = 0.0, S = 1.0;
+  float Af = 0.f, Sf = 1.f;
   bool summed = false;  // the sums below are of r as it is now
   // r's sums: of the CTAs before this one, of all, of this CTA's warps before this one, of this warp
   int64_t before = 0, total = 0, warps_before = 0, mine = 0;
@@ -191,31 +244,35 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyArgs 
         }
         const int c = first + __ffs(hits) - 1;
         next = c + 1;
-        double r = sm.p[c], bar = sm.u[c] * S;
+        // u S q < r in 32 bits, and in 64 only where they may be wrong: 64 take the walk six times as long
+        const float u = sm.u[c], p = sm.p[c], q = kDrawn ? sm.q[c] : 1.f;
         bool again = false;  // the same token was refused before
-        if constexpr (kDrawn) {
-          const double q = sm.q[c];
-          r = fmax(r - A * q, 0.0);
-          bar *= q;
-        } else {
+        if constexpr (!kDrawn) {
           const int t = sm.token[c];
           for (int x = lane; x < refused; x += 32) again |= sm.refused[x] == t;
           again = __any_sync(0xffffffffu, again);
-          if (again) r = 0.0;
         }
-        if (bar < r) {
+        const float bar = u * Sf * q, r = again ? 0.f : kDrawn ? p - Af * q : p;
+        bool keep = bar < r;
+        if (!(fabsf(bar - r) > 0x1p-20f * (fabsf(bar) + p + Af * q))) {
+          const double rd = again ? 0.0 : kDrawn ? fmax(p - A * q, 0.0) : p;
+          keep = u * S * q < rd;
+        }
+        if (keep) {
           last = c;
           if (lane == 0) sm.path[count] = c;
           ++count;
           refused = 0;
-          A = 0.0;
-          S = 1.0;
+          A = 0.0, Af = 0.f;
+          S = 1.0, Sf = 1.f;
           summed = false;
         } else if constexpr (kDrawn) {
           A += S;
+          Af = static_cast<float>(A);
           break;
         } else if (!again) {
-          S = fmax(S - r, 0.0);
+          S = fmax(S - p, 0.0);
+          Sf = static_cast<float>(S);
           if (lane == 0) sm.refused[refused] = sm.token[c];
           ++refused;
           __syncwarp();
@@ -224,7 +281,8 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyArgs 
       if (lane == 0) {
         sm.count = count;
         sm.num_refused = refused;
-        sm.A = A;
+        sm.a_hi = static_cast<float>(A);
+        sm.a_lo = static_cast<float>(A - sm.a_hi);
         sm.state = state;
       }
     }
@@ -233,36 +291,44 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyArgs 
 
     // ---- the sum of r: each warp of the cluster takes a run of pieces
     const Row row(a, t0 + sm.path[sm.count - 1]);
-    const float a_hi = static_cast<float>(sm.A), a_lo = static_cast<float>(sm.A - a_hi);
+    const float a_hi = sm.a_hi, a_lo = sm.a_lo;
     const int run = run_of(row.pieces, cluster), v0 = min((rank * kWarps + warp) * run, row.pieces), v1 = min(v0 + run, row.pieces);
     mine = 0;
+    const bool with_q = a_hi != 0.f;  // A = 0: r is p
+    float p[kBatch][4], q[kBatch][4];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) load_piece<kDrawn>(row, with_q, v0 + 32 * i + lane, v1, p[i], q[i]);
     for (int v = v0; v < v1; v += 32 * kBatch) {
-      float p[kBatch][4], q[kDrawn ? kBatch : 1][4];
-      load_batch<kDrawn>(row, v + lane, v1, p, q);
-      Fixed sum{0, 0};
+      int64_t sum[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const Fixed f = kDrawn ? residual(unit(p[i][e]), unit(q[i][e]), a_hi, a_lo) : fixed(unit(p[i][e]), 0.f);
-          sum.big += f.big;
-          sum.small += f.small;
-        }
-      mine += whole(sum);
+      for (int i = 0; i < kBatch; ++i) {
+        Fixed f[4];
+        four<kDrawn>(p[i], q[i], a_hi, a_lo, f);
+        load_piece<kDrawn>(row, with_q, v + 32 * (i + kBatch) + lane, v1, p[i], q[i]);
+        sum[i] = whole(Fixed{f[0].big + f[1].big + f[2].big + f[3].big, f[0].small + f[1].small + f[2].small + f[3].small});
+      }
+      const int64_t x = sums_of(sum, lane);
+      const int g = (v - v0) / 32 + lane / (32 / kBatch);
+      if (lane % (32 / kBatch) == 0) {
+        if (32 * g < v1 - v0) sm.group[warp][g] = x;
+        mine += x;
+      }
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
     if constexpr (!kDrawn) {
+      __syncwarp();
       for (int x = 0; x < sm.num_refused; ++x) {
         const int t = sm.refused[x], piece = (t + row.skip) / 4;
-        if (piece >= v0 && piece < v1) mine -= whole(fixed(unit(row.p[t]), 0.f));
+        if (piece >= v0 && piece < v1) {
+          const int64_t f = fixed(row.p[t]);
+          mine -= f;
+          if (lane == 0) sm.group[warp][(piece - v0) / 32] -= f;
+        }
       }
     }
     if (lane == 0) sm.warp_sum[warp] = mine;
-    if (turn == 0)
-      cluster_sync();  // every CTA runs, and may be written to
-    else
-      __syncthreads();
+    __syncthreads();
     int64_t cta = 0;
     warps_before = 0;
 #pragma unroll
@@ -270,16 +336,28 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyArgs 
       if (w == warp) warps_before = cta;
       cta += sm.warp_sum[w];
     }
-    // two sums' places in turns: whoever writes one has seen, by the barrier between, that all have read it
-    if (tid < cluster) store_remote(&sm.part[turn & 1][rank], tid, cta);
-    cluster_sync();
+    // Two sums' places and barriers in turns: a CTA sends a sum only when it has all of the one before, for
+    // which every CTA has armed its barrier, and with that has seen the sum before that one.
+    uint64_t* arrived = &sm.arrived[turn & 1];
+    if (turn == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA's barriers are there
+    if (warp == 0) {
+      mbar_arrive_expect_tx(arrived, 8 * cluster);
+      __syncwarp();
+      if (lane < cluster) send(&sm.part[turn & 1][rank], arrived, lane, cta);
+    }
+    const bool ok = mbar_wait(arrived, turn >> 1 & 1, a.timeout_ns, &sm.abort);
+    if (!ok && tid == 0) raise_timeout(&sm.abort, a.status);
+    if (!__syncthreads_and(ok)) return;
     before = total = 0;
     for (int r = 0; r < cluster; ++r) {
       if (r == rank) before = total;
       total += sm.part[turn & 1][r];
     }
     summed = true;
-    S = static_cast<double>(total) * 0x1p-44;
+    if (warp == 0) {
+      S = static_cast<double>(total) * 0x1p-44;
+      Sf = static_cast<float>(S);
+    }
   }
 
   if (rank == 0) {
@@ -290,65 +368,68 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyArgs 
       if (total == 0) a.next[b] = -1;  // p has no probabilities at all
     }
   }
-  // ---- the first value whose running sum exceeds w times the sum: in one warp's run, and there once more
+  // ---- the first value whose running sum exceeds w times the sum: in one warp's run, one of its groups
   const float w = a.w[b];
-  const double bar = static_cast<double>(w >= 0.f ? fminf(w, 1.f - 0x1p-24f) : 0.f) * static_cast<double>(total);
+  const int64_t bar = part_of(w >= 0.f ? fminf(w, 1.f - 0x1p-24f) : 0.f, total);
   int64_t sum = before + warps_before;
-  if (!(static_cast<double>(sum) <= bar && bar < static_cast<double>(sum + mine))) return;
+  if (!(sum <= bar && bar < sum + mine)) return;
   const Row row(a, t0 + sm.path[sm.count - 1]);
-  const float a_hi = static_cast<float>(sm.A), a_lo = static_cast<float>(sm.A - a_hi);
+  const float a_hi = sm.a_hi, a_lo = sm.a_lo;
   const int run = run_of(row.pieces, cluster), v0 = min((rank * kWarps + warp) * run, row.pieces), v1 = min(v0 + run, row.pieces);
-  for (int v = v0; v < v1; v += 32 * kBatch) {
-    float p[kBatch][4], q[kDrawn ? kBatch : 1][4];
-    load_batch<kDrawn>(row, v + lane, v1, p, q);
-#pragma unroll 1
-    for (int i = 0; i < kBatch; ++i) {
-      // (the batch's values are picked by a loop so that its code stands here once)
-      int64_t f[4], all = 0;
+  auto scan = [&](int64_t x) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x = 0.f, y = 0.f;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          if (k == i) {
-            x = p[k][e];
-            if constexpr (kDrawn) y = q[k][e];
-          }
-        f[e] = whole(kDrawn ? residual(unit(x), unit(y), a_hi, a_lo) : fixed(unit(x), 0.f));
-        if constexpr (!kDrawn) {
-          const int t = 4 * (v + 32 * i + lane) - row.skip + e;
-          for (int k = 0; k < sm.num_refused; ++k)
-            if (sm.refused[k] == t) f[e] = 0;
-        }
-        all += f[e];
-      }
-      int64_t upto = all;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, upto, off);
-        if (lane >= off) upto += x;
-      }
-      const unsigned over = __ballot_sync(0xffffffffu, static_cast<double>(sum + upto) > bar);
-      if (over) {
-        if (lane == __ffs(over) - 1) {
-          int64_t x = sum + upto - all;
-          int e = 0;
-          for (; e < 3; ++e) {
-            x += f[e];
-            if (static_cast<double>(x) > bar) break;
-          }
-          a.next[b] = 4 * (v + 32 * i + lane) - row.skip + e;
-        }
-        return;
-      }
-      sum += __shfl_sync(0xffffffffu, upto, 31);
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
     }
+    return x;
+  };
+  int g = 0;
+  for (;; g += 32) {  // (one of the run's groups holds it)
+    const int64_t x = scan(32 * (g + lane) < v1 - v0 ? sm.group[warp][g + lane] : 0);
+    const unsigned over = __ballot_sync(0xffffffffu, sum + x > bar);
+    if (over || 32 * (g + 32) >= v1 - v0) {
+      const int hit = over ? __ffs(over) - 1 : 31;
+      sum += __shfl_sync(0xffffffffu, x, max(hit - 1, 0)) * (hit > 0);
+      g += hit;
+      break;
+    }
+    sum += __shfl_sync(0xffffffffu, x, 31);
+  }
+  float p[4], q[4];
+  load_piece<kDrawn>(row, a_hi != 0.f, v0 + 32 * g + lane, v1, p, q);
+  const int t = 4 * (v0 + 32 * g + lane) - row.skip;
+  Fixed fixed4[4];
+  four<kDrawn>(p, q, a_hi, a_lo, fixed4);
+  int64_t f[4], all = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f[e] = whole(fixed4[e]);
+    if constexpr (!kDrawn)
+      for (int k = 0; k < sm.num_refused; ++k)
+        if (sm.refused[k] == t + e) f[e] = 0;
+    all += f[e];
+  }
+  const int64_t upto = scan(all);
+  const unsigned over = __ballot_sync(0xffffffffu, sum + upto > bar);
+  if (over && lane == __ffs(over) - 1) {
+    int64_t x = sum + upto - all;
+    int e = 0;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      x += f[k];
+      e += x <= bar;
+    }
+    a.next[b] = t + e;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t stream) {
+cudaError_t launch_tree_verify(VerifyArgs& a, cudaStream_t stream) {
+  const cudaError_t e = status_word(&a.status);
+  if (e != cudaSuccess) return e;
+  a.timeout_ns = wait_timeout_ns();
   // CTAs a request: as many as keep a warp busy with some pieces of its row
   int cluster = kMaxCluster;
   while (cluster > 1 && a.vocab < cluster * kWarps * 128) cluster /= 2;
