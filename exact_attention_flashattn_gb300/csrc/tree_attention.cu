@@ -67,7 +67,8 @@ struct Cfg {
   static constexpr int kStages = kCtasPerSm == 2 ? (D == 64 ? 4 : 2) : (D == 64 ? 8 : 5);
   static constexpr uint32_t kRing = kTiles * kQBytes;
   static constexpr uint32_t kBar = kRing + kStages * kTileBytes;
-  static constexpr uint32_t kSmem = kBar + kBarBytes + 1024;  // + alignment slack
+  static constexpr uint32_t kMl = kBar + kBarBytes;  // chunks of two row tiles: stream 1's maxima and sums
+  static constexpr uint32_t kSmem = kMl + (kTiles == 2 ? kTreeRows * 8 : 0) + 1024;  // + alignment slack
   static constexpr int kTmaWarp = 4 * kStreams;  // K tiles, Q and the list of segments
   static constexpr int kMmaWarp = kTmaWarp + 1;
   static constexpr int kTmaVWarp = kMmaWarp + kStreams;
@@ -100,6 +101,7 @@ struct Seg {
   int slot;         // -1: the whole unit; else which of the CTA's two partial results
   int bad;          // set when a draft's V held an infinity or NaN
   int shift;        // chunks: node i sees keys up to and with i + shift (nk: the most that a row of the unit sees)
+  int split;        // chunks: the unit has one row tile, stream 0 takes its even key tiles, stream 1 the odd ones
 };
 
 struct Barriers {
@@ -108,6 +110,7 @@ struct Barriers {
   uint64_t s_free[2];   // kSplitP: the softmax has read S
   uint64_t pv_done[2];  // kLook: the P.V of S buffer (stream) x has completed
   uint64_t turn[2];     // two row tiles at d = 128: P.V turns, 0: stream 0 to 1, 1: back
+  uint64_t ml_full;     // split segments: stream 1's maxima, sums and O are there for stream 0
   uint64_t o_full[2], o_empty[2];
   uint64_t mma_done[2];
   uint64_t kv_full[8], kv_empty[8];
@@ -123,10 +126,19 @@ static_assert(sizeof(Barriers) <= kBarBytes, "barrier block");
 
 __device__ __forceinline__ bool vote(bool x) { return __all_sync(0xffffffffu, x); }
 
+// Places of the list that a tile takes. A batch of chunks mixes units of two row tiles with units of one (decode steps
+// among them, whose tiles are a matter of their bytes): there a tile of two row tiles takes 4 places, of one kSingle.
+template <int D, int kTiles, bool kChunk>
+struct Places {
+  static constexpr int kTile = kChunk && kTiles == 2 ? 4 : 1, kSingle = kTile == 1 ? 1 : D == 64 ? 2 : 3;
+  static constexpr int kCost = tree_unit_cost(D) * kTile;
+};
+
 // Tiles of one sequence. Chunks: the units of its later rows have more of them, and the places of a KV head are
 // summed unit by unit.
-template <int D, bool kChunk>
+template <int D, int kTiles, bool kChunk>
 struct SeqTiles {
+  using P = Places<D, kTiles, kChunk>;
   int tok0, nq, nk;
   int ct, per_unit;  // context tiles, all tiles of a unit
   int row_units;     // units of a KV head
@@ -134,7 +146,7 @@ struct SeqTiles {
   int places;        // chunks: of a KV head
   // places of the list; the host bounds their sum
   __device__ __forceinline__ int all(int head_groups) const {
-    return kChunk ? places * head_groups : (per_unit + tree_unit_cost(D)) * row_units * head_groups;
+    return kChunk ? places * head_groups : (per_unit + P::kCost) * row_units * head_groups;
   }
   // chunks: keys that the last row of unit u sees, and the unit's tiles (one at least: rows without keys are written too)
   __device__ __forceinline__ int unit_keys(int u, int unit_nodes) const {
@@ -145,11 +157,15 @@ struct SeqTiles {
     const int n = unit_keys(u, unit_nodes);
     return max(n / kKeys + (n % kKeys != 0), 1);
   }
+  // chunks: places of a tile of unit u
+  __device__ __forceinline__ int weight(int u, int tile_nodes) const {
+    return nq - u * kTiles * tile_nodes > tile_nodes ? P::kTile : P::kSingle;
+  }
 };
 template <int D, int kTiles, bool kChunk>
-__device__ __forceinline__ SeqTiles<D, kChunk> seq_tiles(const TreeArgs& a, int b) {
+__device__ __forceinline__ SeqTiles<D, kTiles, kChunk> seq_tiles(const TreeArgs& a, int b) {
   constexpr int kKeys = Cfg<D, kTiles>::kKeys;
-  SeqTiles<D, kChunk> s;
+  SeqTiles<D, kTiles, kChunk> s;
   s.tok0 = min(max(a.cu_q[b], 0), a.total_q);
   s.nq = min(min(max(a.cu_q[b + 1], s.tok0), a.total_q) - s.tok0, a.max_nodes);
   s.nk = min(max(a.nk[b], 0), a.kv_cap);
@@ -159,17 +175,17 @@ __device__ __forceinline__ SeqTiles<D, kChunk> seq_tiles(const TreeArgs& a, int 
   s.row_units = s.nq <= unit_nodes ? s.nq > 0 : (s.nq + unit_nodes - 1) / unit_nodes;  // 0 for a sequence without nodes
   if constexpr (kChunk) {
     s.shift = a.causal ? s.nk - s.nq : s.nk - 1;  // (its sum with nq fits: the host sees to that)
-    s.places = s.row_units * tree_unit_cost(D);
-    for (int u = 0; u < s.row_units; ++u) s.places += s.template unit_tiles<kKeys>(u, unit_nodes);
+    s.places = s.row_units * Places<D, kTiles, kChunk>::kCost;
+    for (int u = 0; u < s.row_units; ++u) s.places += s.template unit_tiles<kKeys>(u, unit_nodes) * s.weight(u, a.tile_nodes);
   }
   return s;
 }
 
-// T tiles over at most `most` CTAs, none without a tile: the first T % G CTAs take one more.
+// T places over at most `most` CTAs, none with fewer than a tile's: the first T % G CTAs take one more.
 struct Share {
   int G, per, rem;
-  __device__ __forceinline__ Share(int T, int most) {
-    G = max(min(T, most), 1);
+  __device__ __forceinline__ Share(int T, int most, int tile) {
+    G = max(min(T / tile, most), 1);
     per = T / G;
     rem = T - per * G;
   }
@@ -327,6 +343,7 @@ template <int D, int kTiles, bool kChunk>
 __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCtasPerSm)
     tree_kernel(const __grid_constant__ TreeArgs a) {
   using C = Cfg<D, kTiles>;
+  using P = Places<D, kTiles, kChunk>;
   constexpr int kStreams = C::kStreams, kKeys = C::kKeys, kStages = C::kStages, kVSlots = (kStages + 1) / 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -358,6 +375,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       mbar_init(&bar->o_empty[i], kTreeRows);
       mbar_init(&bar->mma_done[i], 1);
     }
+    mbar_init(&bar->ml_full, kTreeRows);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar->kv_full[i], a.block_table ? 1 + C::kHelpers : 1);  // everyone who loads into the slot
       mbar_init(&bar->kv_empty[i], kTiles);  // one commit per stream that reads the slot
@@ -411,7 +429,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         T += bar->scan[w];
       }
     }
-    const Share share(T, a.groups);
+    const Share share(T, a.groups, P::kTile);
     if (group < share.G && T > 0) my_begin = share.begin(group), my_end = share.begin(group + 1);
     if (my_begin < my_end && before <= my_begin && my_begin < before + mine) {
       int b = run0;
@@ -553,7 +571,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     int pos = my_begin, b = pos < end ? bar->list[1] : 0, seq_at = pos < end ? bar->list[2] : 0;
     int nload = 0, nq[2] = {0, 0};  // K tiles, and Q tiles into each buffer
     // chunks: the sequence, and the unit of it (and of a group of heads) that holds place pos, from place unit_at on
-    SeqTiles<D, kChunk> seq{};
+    SeqTiles<D, kTiles, kChunk> seq{};
     int heads = 0, unit = 0, unit_at = 0;
     if (kChunk && pos < end) {
       seq = seq_tiles<D, kTiles, kChunk>(a, b);
@@ -564,6 +582,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     for (int k = 0; ok; ++k) {
       Seg s{};
       int u0 = 0, size = 0;  // the unit's first place, and its places
+      int tile_places = 1;
       while (kChunk && pos < end && !s.valid) {
         for (;;) {
           if (pos >= seq_at + seq.all(a.head_groups)) {
@@ -573,17 +592,19 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             unit_at = seq_at;
             continue;
           }
-          size = seq.template unit_tiles<kKeys>(unit, kTiles * tile_nodes) + tree_unit_cost(D);
+          tile_places = seq.weight(unit, tile_nodes);
+          size = seq.template unit_tiles<kKeys>(unit, kTiles * tile_nodes) * tile_places + P::kCost;
           if (pos < unit_at + size) break;
           unit_at += size;
           if (++unit == seq.row_units) unit = 0, ++heads;
         }
+        // the tiles whose first place is in the range
         const int at = pos - unit_at, to = min(size, at + end - pos);
         u0 = unit_at;
         pos += to - at;
-        s.k0 = max(at - tree_unit_cost(D), 0);
-        s.nt = to - tree_unit_cost(D) - s.k0;
-        if (s.nt <= 0) break;  // the range ends before the unit's first tile
+        s.k0 = (max(at - P::kCost, 0) + tile_places - 1) / tile_places;
+        s.nt = (max(to - P::kCost, 0) + tile_places - 1) / tile_places - s.k0;
+        if (s.nt <= 0) continue;  // it ends before the unit's first tile, or began inside its last
         s.valid = 1;
         s.b = b;
         s.tok0 = seq.tok0;
@@ -591,12 +612,14 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         s.nk = seq.unit_keys(unit, kTiles * tile_nodes);
         s.hkv = heads * a.head_group + head0;
         s.node0 = unit * (kTiles * tile_nodes);
-        s.ct = size - tree_unit_cost(D);
+        s.ct = (size - P::kCost) / tile_places;
         s.shift = seq.shift;
-        s.slot = s.nt == s.ct ? -1 : (k == 0 ? 0 : 1);
+        // (a CTA has two parts of units at most: of one that began before its range, and of one that ends behind it)
+        s.slot = s.nt == s.ct ? -1 : u0 <= my_begin ? 0 : 1;
+        s.split = kTiles == 2 && s.nt > 1 && tile_rows(s, 1) == 0;
       }
       while (!kChunk && pos < end && !s.valid) {
-        SeqTiles<D, kChunk> q = seq_tiles<D, kTiles, kChunk>(a, b);
+        SeqTiles<D, kTiles, kChunk> q = seq_tiles<D, kTiles, kChunk>(a, b);
         while (pos >= seq_at + q.all(a.head_groups)) {
           seq_at += q.all(a.head_groups);
           q = seq_tiles<D, kTiles, kChunk>(a, ++b);
@@ -636,7 +659,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
           mbar_arrive_expect_tx(&bar->q_full[w], static_cast<uint32_t>(tile_nodes * a.g) * 128 * C::kHalves);
           for (int hf = 0; hf < C::kHalves; ++hf)
             tma_load_3d(sQ + w * C::kQBytes + hf * (kTreeRows * 128) + first_lane * 128, &a.tm_q, &bar->q_full[w], 64 * hf,
-                        s.hkv * a.g, s.tok0 + s.node0 + w * tile_nodes);
+                        s.hkv * a.g, s.tok0 + s.node0 + (kChunk && s.split ? 0 : w * tile_nodes));
           ++nq[w];
         }
         return true;
@@ -648,15 +671,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       if (k == 0 && lane == 0) {
         // what the merge has to know, once the loads are on their way
         TreeMergeRec r{};
-        const Share share(bar->list[0], a.groups);
-        if (s.k0 > 0 && share.owner(u0 + tree_unit_cost(D)) == group - 1) {
+        const Share share(bar->list[0], a.groups, P::kTile);
+        if (s.k0 > 0 && share.owner(u0 + P::kCost) == group - 1) {
           r.rows0 = tile_rows(s, 0);
           r.rows1 = kTiles == 2 ? tile_rows(s, 1) : 0;
           r.node0 = s.tok0 + s.node0;
           r.node_step = tile_nodes;
           r.hkv = s.hkv;
           r.slot0 = u0 <= share.begin(group - 1) ? 0 : 1;
-          r.last = share.owner(u0 + size - 1) * a.head_group + head0;
+          r.last = share.owner(u0 + size - tile_places) * a.head_group + head0;
         }
         a.merge[blockIdx.x] = r;
       }
@@ -763,7 +786,18 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       // the tiles from `plain` on: the context's last one, if it is not whole, and the drafts
       const int plain = min(max((kChunk ? first_masked(s) : s.nk % kKeys ? s.ct - 1 : s.ct) - s.k0, 0), nt);
       const bool turns = kTiles == 2 && !C::kLook && tile_rows(s, 1) > 0;
-      if (kTiles == 2 && tile_rows(s, w) == 0) {  // no rows: only gives the slots back
+      const bool is_split = kChunk && kTiles == 2 && s.split;
+      const int j0 = is_split ? w : 0;  // this stream's first tile
+      // split: a tile of the other stream's, whose slots are given back once they have been filled
+      auto pass_over = [&](int j) -> bool {
+        for (int i = base + 2 * j; i < base + 2 * j + 2; ++i) {
+          if (!wait_load(i)) return false;
+          if (lane == 0) mbar_arrive(&bar->kv_empty[i % kStages]);
+          __syncwarp();
+        }
+        return true;
+      };
+      if (kTiles == 2 && tile_rows(s, w) == 0 && !is_split) {  // no rows: only gives the slots back
         umma_commit(&bar->q_empty[qb]);
         for (int i = base; ok && i < nload; ++i)
           if ((ok = wait_load(i))) umma_commit(&bar->kv_empty[i % kStages]);
@@ -772,13 +806,16 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         release_seg(k);
         continue;
       }
-      if (!(ok = start_s(base))) break;
-      if (nt == 1) umma_commit(&bar->q_empty[qb]);
+      if (j0 > 0 && !(ok = pass_over(0))) break;
+      if (!(ok = start_s(base + 2 * j0))) break;
+      if (is_split ? j0 + 2 >= nt : nt == 1) umma_commit(&bar->q_empty[qb]);
       // one tile; the special ones are apart, as the issuing warp's time per tile bounds two row tiles
-      auto tile = [&](int j, auto special) -> bool {
-        const int ik = base + 2 * j, iv = ik + 1, inext = ik + 2;
+      // (split segments, whose streams take every other tile, too)
+      auto tile = [&](int j, auto special, auto split) -> bool {
+        constexpr int step = split ? 2 : 1;
+        const int ik = base + 2 * j, iv = ik + 1, inext = ik + 2 * step;
         umma_commit(&bar->kv_empty[ik % kStages]);  // S of this tile was issued before
-        const bool more = j + 1 < nt, last_s = j + 2 >= nt;
+        const bool more = j + step < nt, last_s = j + 2 * step >= nt;
         if (C::kLook && more) {
           // S of the next tile goes ahead of this tile's P.V
           if (!start_s(inext)) return false;
@@ -794,15 +831,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
           const bool draft = kChunk ? a.causal != 0 : kt >= s.ct;  // keys that some rows see and others do not
           uint64_t* ready = &bar->v_ready[nspecial % kVSlots];
           valid = min(kKeys, !kChunk && draft ? s.nq - (kt - s.ct) * kKeys : s.nk - kt * kKeys);
-          if (kTiles == 1 || w == 0) {
+          if (kTiles == 1 || w == 0 || split) {
             if (clean_v<C::kHalves, kKeys>(sRing + (iv % kStages) * C::kTileBytes, valid, draft, lane) && lane == 0)
               atomicOr(&sp->bad, 1);
             __syncwarp();
-            if (kTiles == 2 && lane == 0) mbar_arrive(ready);
+            if (kTiles == 2 && !split && lane == 0) mbar_arrive(ready);
           } else if (!vote(mbar_wait(ready, (nspecial / kVSlots) & 1, tmo, abort))) {
             return false;
           }
-          ++nspecial;
+          if (!split) ++nspecial;
         }
         // two row tiles: P.V in turns (0, 1, 0, ...), which keeps the streams out of step, one's softmax
         // beside the other's MMAs
@@ -811,12 +848,18 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                      : nturn > 0 && !vote(mbar_wait(&bar->turn[1], (nturn - 1) & 1, tmo, abort)))
             return false;
         }
-        if (j == 0 && ou > 0 && !vote(mbar_wait(&bar->o_empty[w], (ou - 1) & 1, tmo, abort))) return false;
+        const bool first = split ? j == w : j == 0;
+        if (first && ou > 0 && !vote(mbar_wait(&bar->o_empty[w], (ou - 1) & 1, tmo, abort))) return false;
         if (!vote(mbar_wait(&bar->p_full[buf(np)], use(np) & 1, tmo, abort))) return false;
         tc_fence_after();
-        issue_pv(iv, j > 0, valid, special);
+        issue_pv(iv, !first, valid, special);
+        if constexpr (split) {
+          umma_commit(&bar->kv_empty[iv % kStages]);
+          if (!more) umma_commit(&bar->o_full[w]);
+          if (j + 1 < nt && !pass_over(j + 1)) return false;
+        }
         if (!more) {
-          umma_commit(&bar->o_full[w]);
+          if (!split) umma_commit(&bar->o_full[w]);
           ++ou;
         } else if (!C::kLook) {
           // S of the next tile overwrites P: it follows this P.V in the warp's stream
@@ -828,14 +871,23 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
           if (lane == 0) mbar_arrive(&bar->turn[w]);
           ++nturn;
         }
-        umma_commit(&bar->kv_empty[iv % kStages]);
+        if (!split) umma_commit(&bar->kv_empty[iv % kStages]);
         return true;
       };
-      int j = 0;
+      int j = j0;
+      if (is_split) {
+        if constexpr (kChunk && kTiles == 2) {
 #pragma unroll 1
-      for (; ok && j < plain; ++j) ok = tile(j, std::false_type());
+          for (; ok && j < plain; j += 2) ok = tile(j, std::false_type(), std::true_type());
 #pragma unroll 1
-      for (; ok && j < nt; ++j) ok = tile(j, std::true_type());
+          for (; ok && j < nt; j += 2) ok = tile(j, std::true_type(), std::true_type());
+        }
+      } else {
+#pragma unroll 1
+        for (; ok && j < plain; ++j) ok = tile(j, std::false_type(), std::false_type());
+#pragma unroll 1
+        for (; ok && j < nt; ++j) ok = tile(j, std::true_type(), std::false_type());
+      }
       if (!ok) break;
       release_seg(k);
     }
@@ -851,7 +903,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tO = tbase + lane_base + C::kColO + w * D;
     const float sl2 = a.scale_log2;
-    int n = 0, oused = 0;
+    int n = 0, oused = 0, nsplit = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const Seg* sp = wait_seg(k);
@@ -861,7 +913,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         release_seg(k);
         break;
       }
-      const int rw = kTiles == 2 ? w : 0;  // row tile of this stream
+      const bool is_split = kChunk && kTiles == 2 && s.split;
+      const int rw = kTiles == 2 && !is_split ? w : 0;        // row tile of this stream
       const int rows = tile_rows(s, rw);
       if (rows == 0) {
         release_seg(k);
@@ -876,7 +929,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       // the tiles from `plain` on have keys that some row does not see
       const int plain = min(max((kChunk ? first_masked(s) : s.nk % kKeys ? s.ct - 1 : s.ct) - s.k0, 0), s.nt);
       float m_ref = -INFINITY, l = 0.f;
-      auto tile = [&](int j, auto masked) -> bool {
+      // (split segments: j counts the stream's own tiles, every other one. Their loops are apart, as the common ones take
+      // up to 5 % longer with a choice inside)
+      auto tile = [&](int j, auto masked, auto split) -> bool {
         const int x = C::kTwoS ? n & 1 : w, phase = (C::kTwoS ? n >> 1 : n) & 1;
         const uint32_t tS = tbase + lane_base + C::kColS + x * kKeys;
         const uint32_t tP = C::kSplitP ? tbase + lane_base + C::kColP + w * 64 : tS;
@@ -885,7 +940,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         if (warp_ok) {
           float alpha_o = 1.f;
           if constexpr (masked) {
-            const int kt = s.k0 + j;
+            const int kt = s.k0 + (split ? 2 * j + w : j);
             if (C::kSplitP && n > 0) {
               if (!vote(mbar_wait(&bar->pv_done[x], (n - 1) & 1, tmo, abort))) return false;
               tc_fence_after();
@@ -988,16 +1043,45 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         ++n;
         return true;
       };
-      int j = 0;
+      auto loops = [&](int masked_from, int end, auto split) {
+        int j = 0;
 #pragma unroll 1
-      for (; ok && j < plain; ++j) ok = tile(j, std::false_type());
+        for (; ok && j < masked_from; ++j) ok = tile(j, std::false_type(), split);
 #pragma unroll 1
-      for (; ok && j < s.nt; ++j) ok = tile(j, std::true_type());
+        for (; ok && j < end; ++j) ok = tile(j, std::true_type(), split);
+      };
+      if (is_split) {
+        if constexpr (kChunk && kTiles == 2) loops((plain + 1 - w) / 2, (s.nt + 1 - w) / 2, std::true_type());
+      } else {
+        loops(plain, s.nt, std::false_type());
+      }
       if (!ok) break;
       // ---- the unit's end in this CTA
       if (!(ok = vote(mbar_wait(&bar->o_full[w], oused & 1, tmo, abort)))) break;
       ++oused;
       tc_fence_after();
+      float f0 = 1.f, f1 = 0.f;  // split: the streams' shares of O
+      if (is_split) {
+        // the streams' parts are joined here: stream 0 takes stream 1's O from tensor memory, lane for lane. (What
+        // stream 1 writes for the next split segment comes behind that one's P.V, which waits for o_empty.)
+        float2* ml = reinterpret_cast<float2*>(smem + C::kMl) + ((warp & 3) * 32 + lane);
+        if (w == 1) {
+          *ml = make_float2(m_ref, l);
+          tc_fence_before();
+          mbar_arrive(&bar->ml_full);
+          release_seg(k);
+          continue;
+        }
+        if (!(ok = vote(mbar_wait(&bar->ml_full, nsplit & 1, tmo, abort)))) break;
+        ++nsplit;
+        tc_fence_after();
+        const float2 other = *ml;
+        const float m = fmaxf(m_ref, other.x);
+        f0 = m_ref == -INFINITY ? 0.f : ex2(m_ref - m);
+        f1 = other.x == -INFINITY ? 0.f : ex2(other.x - m);
+        l = l * f0 + other.y * f1;
+        m_ref = m;
+      }
       if (warp_ok) {
         const bool bad = *const_cast<const volatile int*>(&sp->bad) != 0;
         const int64_t orow = static_cast<int64_t>(s.tok0 + node) * a.Hq + head;
@@ -1012,6 +1096,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
           float o[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]);
+          if constexpr (kChunk && kTiles == 2) {
+            if (is_split) {
+              tmem_ld32(tO + D + c * 32, ov);
+              tmem_wait_ld();
+              tmem_reg_fence(ov);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + __uint_as_float(ov[e]) * f1;
+            }
+          }
           if (bad && row_ok) {
             // the infinities and NaN among the drafts (chunks: among the keys of masked tiles) that this row sees
             if constexpr (kChunk) {
@@ -1063,6 +1156,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       }
       tc_fence_before();
       mbar_arrive(&bar->o_empty[w]);
+      if (is_split) mbar_arrive(&bar->o_empty[1]);
       release_seg(k);
     }
     if (!ok && lane == 0) raise_timeout(abort, a.status);
