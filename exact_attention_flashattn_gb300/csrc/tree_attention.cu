@@ -217,16 +217,16 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32
 }
 
 // V tile in shared memory, [atom][kKeys rows][128 bytes]: rows from `valid` to the next 16 become zero, and with
-// `scan` the infinities and NaN of the others (returns whether there were any). A converged warp.
+// `scan` the infinities and NaN of the others from row `from` on (returns whether there were any). A converged warp.
 template <int kHalves, int kKeys>
-__device__ __forceinline__ bool clean_v(uint8_t* tile, int valid, bool scan, int lane) {
+__device__ __forceinline__ bool clean_v(uint8_t* tile, int from, int valid, bool scan, int lane) {
   bool bad = false;
   if (scan) {
     // four pieces of 16 bytes a lane at a time (one by one, 32 drafts at d = 256 took longer than their softmax)
     constexpr int kRun = 4 / kHalves;
     const int end = valid * 128;
 #pragma unroll 1
-    for (int off = lane * 16; off < end; off += 512 * kRun) {
+    for (int off = from * 128 + lane * 16; off < end; off += 512 * kRun) {
       uint4 v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -460,8 +460,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     if (lane == 0) mbar_arrive(&bar->seg_empty[k % kSegSlots]);
   };
   // rows of the unit's row tile w that exist
-  // chunks: the first tile (of the unit) that some row of it does not see whole
-  auto first_masked = [&](const Seg& s) { return min(max(s.shift + s.node0 + 1, 0), s.nk) / kKeys; };
+  // chunks: keys that every row of the unit sees, and its first tile that some row does not see whole
+  auto all_see = [&](const Seg& s) { return min(max(s.shift + s.node0 + 1, 0), s.nk); };
+  auto first_masked = [&](const Seg& s) { return all_see(s) / kKeys; };
   auto tile_rows = [&](const Seg& s, int w) { return max(0, min(tile_nodes, s.nq - s.node0 - w * tile_nodes)) * a.g; };
 
   // paged: the copy of a tile (atom copy % kHalves of piece copy / kHalves) that is this lane's; with a
@@ -832,7 +833,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
           uint64_t* ready = &bar->v_ready[nspecial % kVSlots];
           valid = min(kKeys, !kChunk && draft ? s.nq - (kt - s.ct) * kKeys : s.nk - kt * kKeys);
           if (kTiles == 1 || w == 0 || split) {
-            if (clean_v<C::kHalves, kKeys>(sRing + (iv % kStages) * C::kTileBytes, valid, draft, lane) && lane == 0)
+            // (chunks: the keys that the unit's first token sees are seen by all)
+            const int from = kChunk ? max(all_see(s) - kt * kKeys, 0) : 0;
+            if (clean_v<C::kHalves, kKeys>(sRing + (iv % kStages) * C::kTileBytes, from, valid, draft, lane) && lane == 0)
               atomicOr(&sp->bad, 1);
             __syncwarp();
             if (kTiles == 2 && !split && lane == 0) mbar_arrive(ready);
@@ -1110,7 +1113,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             if constexpr (kChunk) {
               const int* table = a.block_table + static_cast<int64_t>(s.b) * a.max_pages;
               const int d1 = min((s.k0 + s.nt) * kKeys, limit);
-              for (int x = (s.k0 + plain) * kKeys; x < d1; ++x) {
+              for (int x = max(s.k0 * kKeys, all_see(s)); x < d1; ++x) {
                 const int page = min(max(table[x / a.page_size], 0), a.num_pages - 1);
                 const uint16_t* v = a.v + ((static_cast<int64_t>(page) * a.page_size + x % a.page_size) * a.Hkv + s.hkv) * D + c * 32;
 #pragma unroll
