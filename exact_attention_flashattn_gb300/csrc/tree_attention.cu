@@ -87,6 +87,7 @@ struct Cfg {
   static constexpr uint32_t kColS = D == 256 ? 256 : 0;                            // + kKeys a stream (or buffer)
   static constexpr uint32_t kColO = D == 256 ? 0 : 128 * kStreams;                 // + D a stream
   static constexpr uint32_t kColP = 128 * kStreams + D * kStreams;                 // kSplitP: + 64 a stream
+  static constexpr uint32_t kColQ = 384;                                           // d = 256, chunks: Q, 128 columns
   static_assert(kSmem <= (kCtasPerSm == 2 ? 115712 : 232448), "shared memory");
   static_assert(kTiles == 1 || D <= 128, "tiles");
 };
@@ -110,6 +111,7 @@ struct Barriers {
   uint64_t s_free[2];   // kSplitP: the softmax has read S
   uint64_t pv_done[2];  // kLook: the P.V of S buffer (stream) x has completed
   uint64_t turn[2];     // two row tiles at d = 128: P.V turns, 0: stream 0 to 1, 1: back
+  uint64_t qt_full;     // chunks at d = 256: Q is in tensor memory
   uint64_t ml_full;     // split segments: stream 1's maxima, sums and O are there for stream 0
   uint64_t o_full[2], o_empty[2];
   uint64_t mma_done[2];
@@ -344,6 +346,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     tree_kernel(const __grid_constant__ TreeArgs a) {
   using C = Cfg<D, kTiles>;
   using P = Places<D, kTiles, kChunk>;
+  // Chunks at d = 256, which are bound by their products: the softmax threads copy Q into tensor memory, where S reads
+  // only K's 2 KB a step from shared memory, not Q's 4 KB too (2 x 8192 tokens, 16/4 heads: 977 us with Q read there).
+  constexpr bool kQt = kChunk && D == 256;
   constexpr int kStreams = C::kStreams, kKeys = C::kKeys, kStages = C::kStages, kVSlots = (kStages + 1) / 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -375,6 +380,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       mbar_init(&bar->o_empty[i], kTreeRows);
       mbar_init(&bar->mma_done[i], 1);
     }
+    mbar_init(&bar->qt_full, kTreeRows);
     mbar_init(&bar->ml_full, kTreeRows);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar->kv_full[i], a.block_table ? 1 + C::kHelpers : 1);  // everyone who loads into the slot
@@ -738,6 +744,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       const uint32_t tS = tbase + C::kColS + buf(ns) * kKeys;
       if constexpr (D == 128) {
         umma_ss_k128(tS, q_lo, hi, kl, hi, idesc_qk, 0);
+      } else if constexpr (kQt) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          umma_ts(tS, tbase + C::kColQ + 8 * x, kl + x / 4 * (kKeys * 128 / 16) + 2 * (x % 4), hi, idesc_qk, x > 0);
       } else {
 #pragma unroll
         for (int hf = 0; hf < C::kHalves; ++hf)
@@ -780,8 +790,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         release_seg(k);
         break;
       }
-      if (!(ok = vote(mbar_wait(&bar->q_full[qb], k & 1, tmo, abort)))) break;
+      if (!(ok = vote(mbar_wait(kQt ? &bar->qt_full : &bar->q_full[qb], k & 1, tmo, abort)))) break;
       tc_fence_after();
+      if (kQt && lane == 0) mbar_arrive(&bar->q_empty[0]);  // copied out of shared memory
       const int nt = s.nt, base = nload;
       nload += 2 * nt;
       // the tiles from `plain` on: the context's last one, if it is not whole, and the drafts
@@ -809,7 +820,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       }
       if (j0 > 0 && !(ok = pass_over(0))) break;
       if (!(ok = start_s(base + 2 * j0))) break;
-      if (is_split ? j0 + 2 >= nt : nt == 1) umma_commit(&bar->q_empty[qb]);
+      if (!kQt && (is_split ? j0 + 2 >= nt : nt == 1)) umma_commit(&bar->q_empty[qb]);
       // one tile; the special ones are apart, as the issuing warp's time per tile bounds two row tiles
       // (split segments, whose streams take every other tile, too)
       auto tile = [&](int j, auto special, auto split) -> bool {
@@ -820,7 +831,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         if (C::kLook && more) {
           // S of the next tile goes ahead of this tile's P.V
           if (!start_s(inext)) return false;
-          if (last_s) umma_commit(&bar->q_empty[qb]);
+          if (!kQt && last_s) umma_commit(&bar->q_empty[qb]);
         }
         if (!wait_load(iv)) return false;
         int valid = kKeys;  // keys of the tile that count
@@ -867,7 +878,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         } else if (!C::kLook) {
           // S of the next tile overwrites P: it follows this P.V in the warp's stream
           if (!start_s(inext)) return false;
-          if (last_s) umma_commit(&bar->q_empty[qb]);
+          if (!kQt && last_s) umma_commit(&bar->q_empty[qb]);
         }
         if (turns) {
           __syncwarp();
@@ -908,6 +919,26 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     const float sl2 = a.scale_log2;
     int n = 0, oused = 0, nsplit = 0;
     bool ok = true;
+    // Q of the k-th segment from shared memory (128-byte swizzle) into tensor memory, a thread's row each; every S of the
+    // segment before is complete
+    auto copy_q = [&](int k) -> bool {
+      if (!vote(mbar_wait(&bar->q_full[0], k & 1, tmo, abort))) return false;
+      const int r = (warp & 3) * 32 + lane;
+#pragma unroll 1
+      for (int hf = 0; hf < C::kHalves; ++hf) {
+        uint32_t v[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(sQ + hf * (kTreeRows * 128) + r * 128 + ((c ^ (r & 7)) << 4));
+          v[4 * c] = x.x, v[4 * c + 1] = x.y, v[4 * c + 2] = x.z, v[4 * c + 3] = x.w;
+        }
+        tmem_st32(tbase + lane_base + C::kColQ + 32 * hf, v);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&bar->qt_full);
+      return true;
+    };
     for (int k = 0; ok; ++k) {
       const Seg* sp = wait_seg(k);
       if (!(ok = sp != nullptr)) break;
@@ -916,6 +947,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         release_seg(k);
         break;
       }
+      if (kQt && k == 0 && !(ok = copy_q(0))) break;
       const bool is_split = kChunk && kTiles == 2 && s.split;
       const int rw = kTiles == 2 && !is_split ? w : 0;        // row tile of this stream
       const int rows = tile_rows(s, rw);
@@ -1059,6 +1091,11 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         loops(plain, s.nt, std::false_type());
       }
       if (!ok) break;
+      if constexpr (kQt) {
+        // the next segment's first scores are computed while this one's end is written
+        const Seg* next = wait_seg(k + 1);
+        if (!(ok = next != nullptr) || (next->valid && !(ok = copy_q(k + 1)))) break;
+      }
       // ---- the unit's end in this CTA
       if (!(ok = vote(mbar_wait(&bar->o_full[w], oused & 1, tmo, abort)))) break;
       ++oused;
