@@ -789,14 +789,15 @@ def _qk_rope(st, dev, q, k, positions, freq, q_weight, k_weight, eps, axes, inte
 
 def attn_tree_verify(tokens: torch.Tensor, parents: torch.Tensor, cu_seqlens_q: torch.Tensor, target_probs: torch.Tensor,
                      uniforms: torch.Tensor, sample_uniforms: torch.Tensor, max_nodes: int,
-                     draft_probs: torch.Tensor | None = None, stream=None):
+                     draft_probs: torch.Tensor | None = None, accepted: torch.Tensor | None = None,
+                     counts: torch.Tensor | None = None, next_tokens: torch.Tensor | None = None, stream=None):
     """Which drafts are kept: tokens, parents [total_q] int32 (node 0 of a request its root), target_probs (and
     draft_probs, if the drafts were drawn from them) [total_q, vocab] fp32 (rows may lie apart), uniforms [total_q]
     and sample_uniforms [B] fp32 -> int32 (accepted [total_q]: packed rows of each request's path, then -1; counts
-    [B]; next_tokens [B])."""
+    [B]; next_tokens [B]), new or the caller's."""
     dev = _first(target_probs, "target_probs", 2)
     return _run(_verify, dev, stream, tokens, parents, cu_seqlens_q, target_probs, uniforms, sample_uniforms, int(max_nodes),
-                draft_probs)
+                draft_probs, accepted, counts, next_tokens)
 
 
 def _prob_rows(t, name, dev, shape):
@@ -811,7 +812,7 @@ def _prob_rows(t, name, dev, shape):
     return t.stride(0)
 
 
-def _verify(st, dev, tokens, parents, cu, p, u, w, max_nodes, q):
+def _verify(st, dev, tokens, parents, cu, p, u, w, max_nodes, q, accepted, counts, following):
     n, vocab = p.shape
     num_seqs = cu.numel() - 1
     ps = _prob_rows(p, "target_probs", dev, p.shape)
@@ -820,7 +821,9 @@ def _verify(st, dev, tokens, parents, cu, p, u, w, max_nodes, q):
             _like(cu, "cu_seqlens_q", dev, _I32), p.data_ptr(), None if q is None else q.data_ptr(),
             _like(u, "uniforms", dev, _F32, (n,)), _like(w, "sample_uniforms", dev, _F32, (num_seqs,)))
     # (after an empty() with a device's index a launch takes the host 1.5 us more than after an empty_like())
-    accepted, counts, following = torch.empty_like(tokens), torch.empty_like(w, dtype=_I32), torch.empty_like(w, dtype=_I32)
+    accepted = torch.empty_like(tokens) if accepted is None else _out(accepted, "accepted", dev, _I32, (n,))
+    counts = torch.empty_like(w, dtype=_I32) if counts is None else _out(counts, "counts", dev, _I32, (num_seqs,))
+    following = torch.empty_like(w, dtype=_I32) if following is None else _out(following, "next_tokens", dev, _I32, (num_seqs,))
     rc = (_lib or lib()).attn_tree_verify(*args, accepted.data_ptr(), counts.data_ptr(), following.data_ptr(), num_seqs, n,
                                           max_nodes, vocab, ps, qs, st)
     if rc:

@@ -19,7 +19,9 @@
 // takes a request, each a part of the row; all of them walk the tree alike and send one another their sums. 64 trees
 // over 131072 tokens: 11.3 us, 3.0 TB/s, of which the row takes 6 (with cluster barriers around the sums, a second
 // pass over a warp's run for the border and the walk in 64 bits: 25 us). A request whose drafts are refused one by
-// one takes a sum each, 6 us over 151007 tokens, which 40 drawn trees' 33 us end with.
+// one takes a sum each, 6 us over 151007 tokens (117 instructions for 32 x 4 values, two warps a scheduler), which 40
+// drawn trees' 30.5 us end with. Not faster: 512 threads a CTA, rows through a deeper ring in shared memory, a
+// cluster spread over the SMs.
 #include "kernels.h"
 #include "packed.cuh"
 #include "ptx.cuh"
@@ -31,7 +33,9 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxNodes = kTreeMaxNodes;
-constexpr int ctas(bool drawn) { return drawn ? 3 : 4; }  // an SM
+// An SM: four CTAs of 64 registers, so that 64 requests are under way at once; with draft probabilities two of 112 (40
+// trees 30.5 us, three of 80 registers 33.0, four with spills 40.6).
+constexpr int ctas(bool drawn) { return drawn ? 2 : 4; }
 constexpr int kBatch = 4;  // pieces of a row that a lane has under way
 
 // Values in [0, 1] (NaN and negative ones: 0, larger ones: 1).
