@@ -65,8 +65,9 @@ int attn_chunk_paged(const void* q, const void* k_pages, const void* v_pages, co
   a.num_pages = num_pages;
   a.causal = causal;
   a.scale_log2 = scale * bw::kLog2e;
-  // a tile takes up to 4 places of the list
-  if (4 * bw::tree_most_tiles(a) > 0x7fffffff || static_cast<int64_t>(a.kv_cap) + a.max_nodes > 0x7fffffff) return BWATTN_ERR_UNSUPPORTED;
+  // a tile takes up to 4 places of the list, which the heads of a group share
+  if (4 * bw::tree_most_tiles(a) / bw::tree_head_group(Hkv, 8) > 0x7fffffff || static_cast<int64_t>(a.kv_cap) + a.max_nodes > 0x7fffffff)
+    return BWATTN_ERR_UNSUPPORTED;
   return done(bw::launch_tree(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 

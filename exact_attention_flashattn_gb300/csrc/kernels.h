@@ -217,6 +217,13 @@ inline int64_t tree_most_tiles(const TreeArgs& a) {
   return tree_most_units(a) *
          ((static_cast<int64_t>(a.kv_cap) + keys - 1) / keys + (a.k_new ? (a.max_nodes + keys - 1) / keys : 1) + tree_unit_cost(a.d));
 }
+// KV heads of a paged cache that a group of CTAs takes side by side, each CTA one (they share the list of places).
+inline int tree_head_group(int Hkv, int ctas) {
+  int group = 1;
+  for (int n = 2; n <= 8 && n <= ctas; ++n)
+    if (Hkv % n == 0) group = n;
+  return group;
+}
 // Fills the maps and sizes that follow from the others, launches the attention and the merge.
 cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream);
 

@@ -1410,10 +1410,7 @@ cudaError_t launch_tree(TreeArgs& a, void* workspace, cudaStream_t stream) {
   // a page holds the rows of all KV heads side by side: CTAs that read the same keys of different heads at
   // the same time share the pages of HBM that these lie in (16 x 32768 keys, d = 64, 16-token pages: 179 us,
   // each head on its own 202)
-  a.head_group = 1;
-  if (a.block_table)
-    for (int n = 2; n <= 8 && n <= ctas; ++n)
-      if (a.Hkv % n == 0) a.head_group = n;
+  a.head_group = a.block_table ? tree_head_group(a.Hkv, ctas) : 1;
   a.head_groups = a.Hkv / a.head_group;
   a.groups = ctas / a.head_group;
   if (a.groups > most / a.head_group) a.groups = static_cast<int>(most / a.head_group);

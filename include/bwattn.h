@@ -436,8 +436,9 @@ size_t attn_chunk_workspace_size(int num_seqs, int max_seqlen_q, int Hq, int Hkv
  *   workspace    : at least attn_chunk_workspace_size(...) bytes; contents undefined on exit. Must not be
  *                  shared by calls that may overlap on the GPU
  * Keys and values that a token does not see have no effect on its outputs, whatever they hold (infinities
- * and NaN included). Accuracy as for attn_tree. Supported: d in {64, 128, 256}, Hq / Hkv <= 128. q_stride is a
- * multiple of 8 and at least Hq * d, else INVALID_ARG; other errors as for attn_decode_paged.
+ * and NaN included). Accuracy as for attn_tree. Supported: d in {64, 128, 256}, Hq / Hkv <= 128, and sizes whose key
+ * tiles, over all rows at the tables' capacity, stay within 31 bits (131072 tokens of 32/8 heads over tables of a million
+ * keys does). q_stride is a multiple of 8 and at least Hq * d, else INVALID_ARG; other errors as for attn_decode_paged.
  */
 int attn_chunk_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* block_table, void* o, float* lse,
                      const int32_t* nk, const int32_t* cu_seqlens_q, int num_seqs, int total_q, int max_seqlen_q,

@@ -461,6 +461,9 @@ CHUNKS = [
     (8, 2, 128, 16, [5, 0, 3, 200], [9, 4, 200, 300]),  # fewer keys than new tokens: rows without any
     (2, 1, 64, 16, [0, 0], [3, 200]),
     (2, 1, 256, 16, [0, 1], [3, 130]),
+    (128, 1, 256, 32, [300, 40], [30, 1]),
+    (8, 2, 128, 16, [5000, 900, 3000, 700], [1, 200, 2, 1]),  # decode steps among chunks, units of many CTAs
+    (12, 4, 64, 16, [7000, 350, 129, 40], [1, 350, 2, 40]),
 ]
 
 
@@ -515,6 +518,96 @@ def test_chunk_infinities_in_later_values():
                     assert torch.equal(x[:, :, others], y[:, :, others]) and torch.equal(x[:first], y[:first])
         assert bool(torch.isinf(got[50:70, 2:, 5]).all()) and bool(torch.isnan(got[70:100, 2:, 5]).all())
         assert bool(torch.isnan(got[140:250, 2:, 5]).all())
+
+
+def test_chunk_scale_and_caller_buffers():
+    c = Chunk(8, 2, 128, 16, [300, 77], [40, 77], seed=3, pad=0)
+    ref, z = c.run(scale=0.5 / math.sqrt(128))
+    half = Chunk(8, 2, 128, 16, [300, 77], [40, 77], seed=3, pad=0)
+    half.q = (c.q.float() * 0.5).to(torch.bfloat16)  # exact
+    ws = torch.empty(bw.chunk_workspace_size(2, 77, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    o, lse = half.run(workspace=ws)
+    assert torch.equal(o, ref) and torch.equal(lse, z)
+    half.check(o, lse)
+
+
+def test_chunk_pool_past_32_bits():
+    # pages beyond 2^32 bytes and 2^31 elements of the pool
+    Hkv, d, page = 8, 128, 64
+    pool = (1 << 31) // (page * Hkv * d) + 40
+    c = Chunk(16, Hkv, d, page, [500, 90], [120, 90], seed=5)
+    k, v = (torch.empty((pool, page, Hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    m = c.k.shape[0]
+    k[pool - m:], v[pool - m:] = c.k, c.v
+    table = torch.where(c.table < m, c.table + (pool - m), c.table)
+    v[table[0, 499 // page].long(), 499 % page, 3, 7] = INF  # the last token's value, looked up through the table
+    o, lse = bw.attn_chunk_paged(c.q, k, v, table, c.nk_t, c.cu, c.most)
+    assert bool(torch.isinf(o[119, 6:8, 7]).all())
+    o[119, 6:8, 7] = 0
+    c.keys[0][1][499, 3, 7] = 0
+    ref, lse_ref = c.run()
+    assert torch.equal(lse[:210], lse_ref[:210])
+    ref[119, 6:8, 7] = 0
+    assert torch.equal(o[:210], ref[:210])
+
+
+def test_chunk_thousands_of_sequences():
+    r = np.random.default_rng(1)
+    nq = [1] * 3000
+    nk = [int(x) for x in r.integers(1, 40, 3000)]
+    c = Chunk(4, 1, 64, 16, nk, nq, seed=1)
+    o, lse = c.run()
+    some = [int(x) for x in r.integers(0, 3000, 40)] + [0, 2999]
+    for b in some:
+        k, v = (x[:, 0].double() for x in c.keys[b])
+        p = torch.softmax(c.q[b].double() @ k.T / 8, 1)
+        A = p @ v.abs()
+        E = (64 + 8) * 2.0 ** -24 * float((c.q[b].double().abs() @ k.abs().T / 8).max())
+        dO = (2.0 ** -8 + 4 * E) * A
+        assert bool(((o[b].double() - p @ v).abs() <= dO + 2.0 ** -8 * ((p @ v).abs() + dO) + 1e-30).all())
+
+
+def test_rope_far_apart_rows_and_odd_frequencies():
+    # rows whose offsets pass 2^31 elements
+    big = torch.empty((1 << 32) + (1 << 13), dtype=torch.bfloat16, device="cuda")
+    g = gen(8)
+    q = big.as_strided((3, 4, 128), (1 << 31, 128, 1))
+    q.copy_(randn((3, 4, 128), g))
+    k, w = randn((3, 2, 128), g), randn((128,), g)
+    pos, f = i32([3, 70000, -5]), torch.rand(64, device="cuda")
+    a = bw.attn_qk_norm_rope(q, k, pos, f, w, w)
+    b = bw.attn_qk_norm_rope(q.contiguous(), k, pos, f, w, w)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # a negative frequency turns the other way; 0 and the smallest not at all
+    f = torch.tensor([0.7, 1e-45, 0.0, 1e-30] * 16, device="cuda")
+    plus, minus = bw.attn_qk_norm_rope(k, k.clone(), pos, f), bw.attn_qk_norm_rope(k, k.clone(), -pos, -f)
+    assert torch.equal(plus[0], minus[0]) and torch.equal(plus[0][:, :, 1::4], k[:, :, 1::4]) and torch.equal(plus[0][:, :, 2::4], k[:, :, 2::4])
+
+
+def test_verify_rows_far_apart_and_caller_buffers():
+    V, n = 1000, 6
+    big = torch.empty(5 * (1 << 29) + V, device="cuda")
+    g = gen(6)
+    p = big.as_strided((n, V), (1 << 29, 1))
+    p.copy_(probs(n, V, g))
+    q = torch.softmax(torch.log(p) + torch.randn((n, V), generator=g, device="cuda"), 1)
+    parents = trees([2, 4], "tree", np.random.default_rng(0))
+    tokens = drafted(parents, [2, 4], q, g)
+    u, w = torch.rand(n, generator=g, device="cuda") * 0.1, torch.rand(2, generator=g, device="cuda")
+    for drawn in (None, q):
+        check_verify(tokens, i32(parents), [2, 4], p, drawn, u, w)
+    outs = dict(accepted=i32([7] * n), counts=i32([7, 7]), next_tokens=i32([7, 7]))
+    got = bw.attn_tree_verify(tokens, i32(parents), sums([2, 4]), p, u, w, 4, **outs)
+    assert got[0] is outs["accepted"] and got[1] is outs["counts"] and got[2] is outs["next_tokens"]
+    want = bw.attn_tree_verify(tokens, i32(parents), sums([2, 4]), p, u, w, 4)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # no node may be tried: not even the roots are
+    acc, counts, nxt = bw.attn_tree_verify(tokens, i32(parents), sums([2, 4]), p, u, w, 0)
+    assert acc.tolist() == [-1] * n and counts.tolist() == [0, 0] and nxt.tolist() == [-1, -1]
+    with pytest.raises(ValueError):
+        bw.attn_tree_verify(tokens, i32(parents), sums([2, 4]), p, u, w, 4, counts=i32([1]))
+    with pytest.raises(bw.BwattnError):
+        bw.attn_tree_verify(tokens, i32(parents), sums([2, 4]), p, u, w, 4, accepted=tokens)
 
 
 def test_chunk_equals_tree_and_decode():
