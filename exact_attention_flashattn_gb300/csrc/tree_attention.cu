@@ -102,6 +102,8 @@ struct Seg {
   int slot;         // -1: the whole unit; else which of the CTA's two partial results
   int bad;          // set when a draft's V held an infinity or NaN
   int shift;        // chunks: node i sees keys up to and with i + shift (nk: the most that a row of the unit sees)
+  int first;        // chunks: of the segment's tiles that all rows see whole, the one that is taken first (then the
+                    // ones behind it, then those before)
   int split;        // chunks: the unit has one row tile, stream 0 takes its even key tiles, stream 1 the odd ones
 };
 
@@ -496,40 +498,51 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     if (a.block_table) {
       const int copy = share_copy(member), hfl = copy % C::kHalves, my_piece = (copy / C::kHalves) * a.piece;
       const int* table = a.block_table + static_cast<int64_t>(s.b) * a.max_pages;
-      const int first = s.k0 * kKeys + my_piece, pages_on = kKeys / a.page_size, rows_on = kKeys % a.page_size;
-      int page = first / a.page_size, at = first - page * a.page_size;
+      const int pages_on = kKeys / a.page_size, rows_on = kKeys % a.page_size;
+      int page, at;
       // the pool row of this lane's piece in the next tile, looked up one tile ahead
       auto pool_row = [&](int kt) -> int {
         if (my_piece >= kKeys || kt >= s.ct || kt * kKeys + my_piece >= s.nk) return -1;
         // a bad entry reads a wrong page, never outside the pool
         return min(max(table[page], 0), a.num_pages - 1) * a.page_size + at;
       };
-      int row_next = pool_row(s.k0);
+      // chunks: the tiles that all rows see whole may begin with another than the first; then those before it follow,
+      // then the others
+      const int turn = kChunk ? s.first : 0, plain = turn > 0 ? min(max(first_masked(s) - s.k0, 0), s.nt) : nctx;
+      int kt = s.k0 + turn, run_end = s.k0 + plain;
 #pragma unroll 1
-      for (; j < nctx; ++j, ++n) {
-        if (!before_tile(j)) return false;
-        const int kt = s.k0 + j, row = row_next;
-        page += pages_on;
-        if ((at += rows_on) >= a.page_size) at -= a.page_size, ++page;
-        row_next = pool_row(kt + 1);
-        for (int kv = kv0; kv < kv1; ++kv) {
-          const int i = 2 * n + kv, slot = i % kStages;
-          if (!wait_slot(i)) {
-            // drain() does not know of the K of this tile that went out just before
-            if (kv > kv0) mbar_wait(&bar->kv_full[(i - 1) % kStages], ((i - 1) / kStages) & 1, tmo, &no_abort);
-            return false;
-          }
-          if (member == 0) {
-            // pieces past the last key are not copied: their K scores are masked, their V rows zeroed
-            const int pieces = min(kKeys / a.piece, (s.nk - kt * kKeys + a.piece - 1) / a.piece);
-            mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(pieces * a.piece) * 128 * C::kHalves);
+      for (int run = 0; run < (turn > 0 ? 3 : 1); ++run) {
+        if (run == 1) kt = s.k0, run_end = s.k0 + turn;
+        if (run == 2) kt = s.k0 + plain, run_end = s.k0 + nctx;
+        const int first = kt * kKeys + my_piece;
+        page = first / a.page_size, at = first - page * a.page_size;
+        int row_next = pool_row(kt);
+#pragma unroll 1
+        for (; kt < run_end; ++kt, ++j, ++n) {
+          if (!before_tile(j)) return false;
+          const int row = row_next;
+          page += pages_on;
+          if ((at += rows_on) >= a.page_size) at -= a.page_size, ++page;
+          row_next = pool_row(kt + 1);
+          for (int kv = kv0; kv < kv1; ++kv) {
+            const int i = 2 * n + kv, slot = i % kStages;
+            if (!wait_slot(i)) {
+              // drain() does not know of the K of this tile that went out just before
+              if (kv > kv0) mbar_wait(&bar->kv_full[(i - 1) % kStages], ((i - 1) / kStages) & 1, tmo, &no_abort);
+              return false;
+            }
+            if (member == 0) {
+              // pieces past the last key are not copied: their K scores are masked, their V rows zeroed
+              const int pieces = min(kKeys / a.piece, (s.nk - kt * kKeys + a.piece - 1) / a.piece);
+              mbar_arrive_expect_tx(&bar->kv_full[slot], static_cast<uint32_t>(pieces * a.piece) * 128 * C::kHalves);
+              __syncwarp();
+            }
+            if (row >= 0)
+              tma_load_3d_lane(sRing + slot * C::kTileBytes + hfl * (kKeys * 128) + my_piece * 128, kv ? &a.tm_v : &a.tm_k,
+                               &bar->kv_full[slot], 64 * hfl, s.hkv, row);
             __syncwarp();
+            if (member > 0 && lane == 0) mbar_arrive(&bar->kv_full[slot]);
           }
-          if (row >= 0)
-            tma_load_3d_lane(sRing + slot * C::kTileBytes + hfl * (kKeys * 128) + my_piece * 128, kv ? &a.tm_v : &a.tm_k,
-                             &bar->kv_full[slot], 64 * hfl, s.hkv, row);
-          __syncwarp();
-          if (member > 0 && lane == 0) mbar_arrive(&bar->kv_full[slot]);
         }
       }
     } else {
@@ -580,6 +593,12 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     // chunks: the sequence, and the unit of it (and of a group of heads) that holds place pos, from place unit_at on
     SeqTiles<D, kTiles, kChunk> seq{};
     int heads = 0, unit = 0, unit_at = 0;
+    // Units of a sequence read the same keys, each CTA its run of them. A CTA begins a run with the tile whose number is
+    // that of the tiles it has taken, modulo its share: CTAs then read a tile of keys at about the same time, wherever
+    // in their units their shares begin, and HBM once for all of them (512 tokens behind 65024, 32/8 heads of 128: 2.15
+    // GB of HBM reads in the runs' own order).
+    const int share_tiles = max((my_end - my_begin) / P::kTile, 1);
+    int taken = 0;
     if (kChunk && pos < end) {
       seq = seq_tiles<D, kTiles, kChunk>(a, b);
       heads = (pos - seq_at) / seq.places;
@@ -624,6 +643,12 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         // (a CTA has two parts of units at most: of one that began before its range, and of one that ends behind it)
         s.slot = s.nt == s.ct ? -1 : u0 <= my_begin ? 0 : 1;
         s.split = kTiles == 2 && s.nt > 1 && tile_rows(s, 1) == 0;
+        if (seq.row_units > 1) {
+          s.first = (taken - s.k0) % share_tiles;
+          if (s.first < 0) s.first += share_tiles;
+          if (s.first >= min(max(first_masked(s) - s.k0, 0), s.nt)) s.first = 0;
+        }
+        taken += s.nt;
       }
       while (!kChunk && pos < end && !s.valid) {
         SeqTiles<D, kTiles, kChunk> q = seq_tiles<D, kTiles, kChunk>(a, b);
