@@ -121,7 +121,7 @@ struct Barriers {
   uint64_t v_ready[8];  // two row tiles: stream 0 has looked over the V tile, in turn for those that need it
   uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
   Seg seg[kSegSlots];
-  int scan[16];
+  int scan[16], largest[16];
   int list[3];  // tiles of all sequences; the sequence of the CTA's first tile; tiles before it
   uint32_t tmem_base;
   int abort;
@@ -148,6 +148,7 @@ struct SeqTiles {
   int row_units;     // units of a KV head
   int shift;         // chunks: as in Seg
   int places;        // chunks: of a KV head
+  int largest;       // chunks: places of the largest unit
   // places of the list; the host bounds their sum
   __device__ __forceinline__ int all(int head_groups) const {
     return kChunk ? places * head_groups : (per_unit + P::kCost) * row_units * head_groups;
@@ -180,7 +181,12 @@ __device__ __forceinline__ SeqTiles<D, kTiles, kChunk> seq_tiles(const TreeArgs&
   if constexpr (kChunk) {
     s.shift = a.causal ? s.nk - s.nq : s.nk - 1;  // (its sum with nq fits: the host sees to that)
     s.places = s.row_units * Places<D, kTiles, kChunk>::kCost;
-    for (int u = 0; u < s.row_units; ++u) s.places += s.template unit_tiles<kKeys>(u, unit_nodes) * s.weight(u, a.tile_nodes);
+    s.largest = 0;
+    for (int u = 0; u < s.row_units; ++u) {
+      const int n = s.template unit_tiles<kKeys>(u, unit_nodes) * s.weight(u, a.tile_nodes);
+      s.places += n;
+      s.largest = max(s.largest, n + Places<D, kTiles, kChunk>::kCost);
+    }
   }
   return s;
 }
@@ -409,17 +415,22 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   const bool wide = a.num_seqs > 128;
   const int run = wide ? (a.num_seqs + C::kThreads - 1) / C::kThreads : (a.num_seqs + 31) / 32;
   const int run0 = min((wide ? tid : lane) * run, a.num_seqs), run1 = min(run0 + run, a.num_seqs);
-  int mine = 0, incl = 0;
+  int mine = 0, incl = 0, largest = 0;
   if (wide || warp == C::kTmaWarp) {
 #pragma unroll 4
-    for (int b = run0; b < run1; ++b) mine += seq_tiles<D, kTiles, kChunk>(a, b).all(a.head_groups);
+    for (int b = run0; b < run1; ++b) {
+      const auto q = seq_tiles<D, kTiles, kChunk>(a, b);
+      mine += q.all(a.head_groups);
+      if constexpr (kChunk) largest = max(largest, q.largest);
+    }
+    if constexpr (kChunk) largest = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(largest)));
     incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += x;
     }
-    if (wide && lane == 31) bar->scan[warp] = incl;
+    if (wide && lane == 31) bar->scan[warp] = incl, bar->largest[warp] = largest;
   }
   tc_fence_before();
   __syncthreads();
@@ -428,6 +439,11 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   // tensor memory, for the same reason)
   asm volatile("griddepcontrol.launch_dependents;");
   int my_begin = 0, my_end = 0;  // the group's places
+  // Chunks: a unit that several CTAs share costs them their parts and the merge, about what 8 tiles take (16 at d = 256).
+  // Where the largest unit is no longer than that, and a share that is smaller than it, the CTA in whose share a unit
+  // begins takes it whole: 32 requests of 500 keys and one token, d = 128, 25.4 -> 20.3 us, 4 of 1000 and 128 tokens 33.8
+  // -> 30.5, 8 of 600 and 200 at d = 256 46.9 -> 41.0. With 12 tiles 4 of 1000 keys and 64 tokens took 28.7 us, not 24.3.
+  bool whole_units = false;
   if (wide || warp == C::kTmaWarp) {
     int T = __shfl_sync(0xffffffffu, incl, 31), before = incl - mine;
     if (wide) {
@@ -435,10 +451,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       for (int w = 0; w < C::kWarps; ++w) {
         if (w == warp) before += T;
         T += bar->scan[w];
+        if (kChunk) largest = max(largest, bar->largest[w]);
       }
     }
     const Share share(T, a.groups, P::kTile);
     if (group < share.G && T > 0) my_begin = share.begin(group), my_end = share.begin(group + 1);
+    if constexpr (kChunk) {
+      constexpr int kMerge = (D == 256 ? 16 : 8) * P::kTile;  // what the parts and the merge take, in places
+      whole_units = largest <= kMerge + (share.per < largest ? share.per : 0);
+    }
     if (my_begin < my_end && before <= my_begin && my_begin < before + mine) {
       int b = run0;
       for (int n; my_begin >= before + (n = seq_tiles<D, kTiles, kChunk>(a, b).all(a.head_groups)); ++b) before += n;
@@ -624,8 +645,12 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
           unit_at += size;
           if (++unit == seq.row_units) unit = 0, ++heads;
         }
+        if (whole_units && pos > unit_at) {  // it began before the range
+          pos = unit_at + size;
+          continue;
+        }
         // the tiles whose first place is in the range
-        const int at = pos - unit_at, to = min(size, at + end - pos);
+        const int at = pos - unit_at, to = whole_units ? size : min(size, at + end - pos);
         u0 = unit_at;
         pos += to - at;
         s.k0 = (max(at - P::kCost, 0) + tile_places - 1) / tile_places;
