@@ -226,52 +226,66 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32
       : "memory");
 }
 
-// V tile in shared memory, [atom][kKeys rows][128 bytes]: rows from `valid` to the next 16 become zero, and with
-// `scan` the infinities and NaN of the others from row `from` on (returns whether there were any). A converged warp.
+// The infinities and NaN in rows `from` to `valid` of a V tile in shared memory, [atom][kKeys rows][128 bytes], become
+// zero. A converged warp.
 template <int kHalves, int kKeys>
-__device__ __forceinline__ bool clean_v(uint8_t* tile, int from, int valid, bool scan, int lane) {
-  bool bad = false;
-  if (scan) {
-    // four pieces of 16 bytes a lane at a time (one by one, 32 drafts at d = 256 took longer than their softmax)
-    constexpr int kRun = 4 / kHalves;
-    const int end = valid * 128;
+__device__ __forceinline__ void zero_bad(uint8_t* tile, int from, int valid, int lane) {
 #pragma unroll 1
-    for (int off = from * 128 + lane * 16; off < end; off += 512 * kRun) {
-      uint4 v[4];
+  for (int hf = 0; hf < kHalves; ++hf) {
+#pragma unroll 1
+    for (int off = from * 128 + lane * 16; off < valid * 128; off += 512) {
+      uint4* at = reinterpret_cast<uint4*>(tile + hf * (kKeys * 128) + off);
+      const uint4 v = *at;
+      uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int at = off + 512 * (i / kHalves);
-        v[i] = at < end ? *reinterpret_cast<const uint4*>(tile + i % kHalves * (kKeys * 128) + at) : make_uint4(0u, 0u, 0u, 0u);
+      for (int e = 0; e < 4; ++e) {
+        if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+        if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        bool hit = false;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if ((w[e] & 0x7f80u) == 0x7f80u) {
-            w[e] &= 0xffff0000u;
-            hit = true;
-          }
-          if ((w[e] & 0x7f800000u) == 0x7f800000u) {
-            w[e] &= 0xffffu;
-            hit = true;
-          }
-        }
-        if (hit)
-          *reinterpret_cast<uint4*>(tile + i % kHalves * (kKeys * 128) + off + 512 * (i / kHalves)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
-        bad |= hit;
-      }
+      *at = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
+}
+// The same, and whether there were any. Values are looked over by products with 0, whose sum is 0 or NaN, eight pieces
+// of 16 bytes a lane at a time: the last P.V of a unit waits for it (with compares, four pieces at a time, 128 rows at
+// d = 128 took 3 us). Out of line, as in the issuing warp's loop it cost every tile 1 to 2 %.
+template <int kHalves, int kKeys>
+__device__ __noinline__ bool scan_v(uint8_t* tile, int from, int valid, int lane) {
+  constexpr int kRun = 8 / kHalves;
+  const int end = valid * 128;
+  uint32_t sum[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+  for (int off = from * 128 + lane * 16; off < end; off += 512 * kRun) {
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = off + 512 * (i / kHalves);
+      v[i] = at < end ? *reinterpret_cast<const uint4*>(tile + i % kHalves * (kKeys * 128) + at) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[0]) : "r"(v[i].x), "r"(0u));
+      asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[1]) : "r"(v[i].y), "r"(0u));
+      asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[2]) : "r"(v[i].z), "r"(0u));
+      asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[3]) : "r"(v[i].w), "r"(0u));
+    }
+  }
+  const bool bad = __any_sync(0xffffffffu, ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) != 0);
+  if (bad) zero_bad<kHalves, kKeys>(tile, from, valid, lane);
+  return bad;
+}
+// V tile in shared memory: rows from `valid` to the next 16 become zero, and with `scan` the infinities and NaN of the
+// others from row `from` on (returns whether there were any). A converged warp.
+template <int kHalves, int kKeys>
+__device__ __forceinline__ bool clean_v(uint8_t* tile, int from, int valid, bool scan, int lane) {
+  const bool bad = scan && scan_v<kHalves, kKeys>(tile, from, valid, lane);
 #pragma unroll
   for (int hf = 0; hf < kHalves; ++hf)
     for (int off = valid * 128 + lane * 16; off < (valid + 15) / 16 * 2048; off += 512)
       *reinterpret_cast<uint4*>(tile + hf * (kKeys * 128) + off) = make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the tensor pipe reads the tile
   __syncwarp();
-  return __any_sync(0xffffffffu, bad);
+  return bad;
 }
 
 // Registers: a softmax thread holds a row's 128 scores, the other four warps little; at d = 256 a row has 64
@@ -347,6 +361,41 @@ __device__ __noinline__ MaskedTile masked_tile(uint32_t tS, uint32_t tP, int lef
   }
   r.l = l0 + l1;
   return r;
+}
+
+// Chunks: a warp's rows of O, in tensor memory from column tO on, times inv to rows `row` of `out` (-1: none). Rows are
+// written four lanes to one, 64 bytes of it: each four lanes exchange their rows' pieces, and piece x of row k of the
+// four goes to lane x's k-th store. (A lane's own row in pieces of 16 bytes, a store touches 32 rows, and a unit's end
+// took 3 us.) Out of line, as its registers would make the loops over tiles spill.
+template <int D>
+__device__ __noinline__ void write_rows(uint32_t tO, float inv, int64_t row, uint16_t* out, int lane) {
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t o[32];
+    tmem_ld32(tO + c * 32, o);
+    tmem_wait_ld();
+    tmem_reg_fence(o);
+    auto two = [&](int e) { return pack_bf16x2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv); };
+    uint4 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = make_uint4(two(8 * q), two(8 * q + 2), two(8 * q + 4), two(8 * q + 6));
+    auto exchange = [&](uint4& low, uint4& high, int bit) {
+      const bool upper = lane & bit;
+      const uint4 give = upper ? low : high;
+      const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, bit), __shfl_xor_sync(0xffffffffu, give.y, bit),
+                                   __shfl_xor_sync(0xffffffffu, give.z, bit), __shfl_xor_sync(0xffffffffu, give.w, bit));
+      (upper ? low : high) = got;
+    };
+    exchange(v[0], v[1], 1);
+    exchange(v[2], v[3], 1);
+    exchange(v[0], v[2], 2);
+    exchange(v[1], v[3], 2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t to = __shfl_sync(0xffffffffu, row, (lane & ~3) + k);
+      if (to >= 0) *reinterpret_cast<uint4*>(out + to * D + c * 32 + 8 * (lane & 3)) = v[k];
+    }
+  }
 }
 
 template <int D, int kTiles, bool kChunk>
@@ -1177,68 +1226,72 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         const int64_t orow = static_cast<int64_t>(s.tok0 + node) * a.Hq + head;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         float* part = a.partial + ((static_cast<int64_t>(blockIdx.x) * 2 + max(s.slot, 0)) * kTiles + rw) * (kTreeRows * (D + 2));
+        if (kChunk && s.slot < 0 && !bad && !is_split && s.nk > 0) {
+          write_rows<D>(tO, inv, row_ok ? orow : -1, a.o, lane);
+        } else {
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t ov[32];
-          tmem_ld32(tO + c * 32, ov);
-          tmem_wait_ld();
-          tmem_reg_fence(ov);
-          float o[32];
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tmem_ld32(tO + c * 32, ov);
+            tmem_wait_ld();
+            tmem_reg_fence(ov);
+            float o[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]);
-          if constexpr (kChunk && kTiles == 2) {
-            if (is_split) {
-              tmem_ld32(tO + D + c * 32, ov);
-              tmem_wait_ld();
-              tmem_reg_fence(ov);
+            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]);
+            if constexpr (kChunk && kTiles == 2) {
+              if (is_split) {
+                tmem_ld32(tO + D + c * 32, ov);
+                tmem_wait_ld();
+                tmem_reg_fence(ov);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + __uint_as_float(ov[e]) * f1;
+                for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + __uint_as_float(ov[e]) * f1;
+              }
             }
-          }
-          if (bad && row_ok) {
-            // the infinities and NaN among the drafts (chunks: among the keys of masked tiles) that this row sees
-            if constexpr (kChunk) {
-              const int* table = a.block_table + static_cast<int64_t>(s.b) * a.max_pages;
-              const int d1 = min((s.k0 + s.nt) * kKeys, limit);
-              for (int x = max(s.k0 * kKeys, all_see(s)); x < d1; ++x) {
-                const int page = min(max(table[x / a.page_size], 0), a.num_pages - 1);
-                const uint16_t* v = a.v + ((static_cast<int64_t>(page) * a.page_size + x % a.page_size) * a.Hkv + s.hkv) * D + c * 32;
+            if (bad && row_ok) {
+              // the infinities and NaN among the drafts (chunks: among the keys of masked tiles) that this row sees
+              if constexpr (kChunk) {
+                const int* table = a.block_table + static_cast<int64_t>(s.b) * a.max_pages;
+                const int d1 = min((s.k0 + s.nt) * kKeys, limit);
+                for (int x = max(s.k0 * kKeys, all_see(s)); x < d1; ++x) {
+                  const int page = min(max(table[x / a.page_size], 0), a.num_pages - 1);
+                  const uint16_t* v = a.v + ((static_cast<int64_t>(page) * a.page_size + x % a.page_size) * a.Hkv + s.hkv) * D + c * 32;
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if ((v[e] & 0x7f80) == 0x7f80) o[e] += __uint_as_float(static_cast<uint32_t>(v[e]) << 16);
+                }
+              }
+              const int d0 = max(s.k0 - s.ct, 0) * kKeys, d1 = min((s.k0 + s.nt - s.ct) * kKeys, s.nq);
+              for (int x = d0; !kChunk && x < d1; ++x) {
+                if (!(bits[x >> 6] >> (x & 63) & 1)) continue;
+                const uint16_t* v = a.v_new + (s.tok0 + x) * a.v_new_stride + s.hkv * D + c * 32;
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
                   if ((v[e] & 0x7f80) == 0x7f80) o[e] += __uint_as_float(static_cast<uint32_t>(v[e]) << 16);
               }
             }
-            const int d0 = max(s.k0 - s.ct, 0) * kKeys, d1 = min((s.k0 + s.nt - s.ct) * kKeys, s.nq);
-            for (int x = d0; !kChunk && x < d1; ++x) {
-              if (!(bits[x >> 6] >> (x & 63) & 1)) continue;
-              const uint16_t* v = a.v_new + (s.tok0 + x) * a.v_new_stride + s.hkv * D + c * 32;
+            if constexpr (kChunk) {
+              // a unit without keys has no P.V: what stands in tensor memory is not its O
+              if (s.nk == 0)
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if ((v[e] & 0x7f80) == 0x7f80) o[e] += __uint_as_float(static_cast<uint32_t>(v[e]) << 16);
+                for (int e = 0; e < 32; ++e) o[e] = 0.f;
             }
-          }
-          if (!row_ok) continue;
-          if constexpr (kChunk) {
-            // a unit without keys has no P.V: what stands in tensor memory is not its O
-            if (s.nk == 0)
+            if (!row_ok) continue;
+            if (s.slot < 0) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0.f;
-          }
-          if (s.slot < 0) {
+              for (int q = 0; q < 4; ++q) {
+                uint4 v;
+                v.x = pack_bf16x2(o[8 * q] * inv, o[8 * q + 1] * inv);
+                v.y = pack_bf16x2(o[8 * q + 2] * inv, o[8 * q + 3] * inv);
+                v.z = pack_bf16x2(o[8 * q + 4] * inv, o[8 * q + 5] * inv);
+                v.w = pack_bf16x2(o[8 * q + 6] * inv, o[8 * q + 7] * inv);
+                *reinterpret_cast<uint4*>(a.o + orow * D + c * 32 + 8 * q) = v;
+              }
+            } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint4 v;
-              v.x = pack_bf16x2(o[8 * q] * inv, o[8 * q + 1] * inv);
-              v.y = pack_bf16x2(o[8 * q + 2] * inv, o[8 * q + 3] * inv);
-              v.z = pack_bf16x2(o[8 * q + 4] * inv, o[8 * q + 5] * inv);
-              v.w = pack_bf16x2(o[8 * q + 6] * inv, o[8 * q + 7] * inv);
-              *reinterpret_cast<uint4*>(a.o + orow * D + c * 32 + 8 * q) = v;
+              for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<float4*>(part + ((c * 8 + q) * kTreeRows + row) * 4) =
+                    make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
             }
-          } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              *reinterpret_cast<float4*>(part + ((c * 8 + q) * kTreeRows + row) * 4) =
-                  make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           }
         }
         if (row_ok && s.slot < 0 && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
