@@ -8,8 +8,8 @@
 // A warp takes whole rows, some heads a turn: d / 16 lanes a head, each with two pieces of 8 channels that hold both
 // halves of its pairs, so rotating needs no exchange. Weights, cosines and sines are multiplied once a row: an
 // output is r (x C + other S), with r the head's 1 / sqrt and `other` the pair's other channel, in packed pairs of
-// 32 bits. The coming turns' values are copied to shared memory meanwhile. 16384 rows of 32 + 8 heads of 128: 55.7 us,
-// 6.0 TB/s (weights and rotation apart, in single values: 78 us and 2400 instructions a row; a row shared by a
+// 32 bits. The coming turns' values are copied to shared memory meanwhile. 16384 rows of 32 + 8 heads of 128: 53.8 us,
+// 6.2 TB/s (weights and rotation apart, in single values: 78 us and 2400 instructions a row; a row shared by a
 // block's warps, with a barrier a row: 59.6; five blocks an SM in 96 registers: 59.7).
 #include "kernels.h"
 #include "packed.cuh"
@@ -54,7 +54,7 @@ __device__ __forceinline__ uint32_t pack(pair_t x) { return pack_bf16x2(first(x)
 __device__ __forceinline__ float bf16(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
 
 // A warp takes a row's heads (or one of `gridDim.y` parts of them), kHeads a turn, and then another row's.
-constexpr int kRing = 4;        // turns that a warp has under way
+constexpr int kRing = 3;        // turns that a warp has under way (16384 rows of 32 + 8 heads of 128: 53.8 us, 4 55.1, 6 57.1)
 constexpr int kRopeBlocks = 4;  // an SM
 
 template <int D, int kMode>

@@ -121,7 +121,7 @@ struct Barriers {
   uint64_t v_ready[8];  // two row tiles: stream 0 has looked over the V tile, in turn for those that need it
   uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
   Seg seg[kSegSlots];
-  int scan[16], largest[16];
+  int scan[16], largest[16], smallest[16];
   int list[3];  // tiles of all sequences; the sequence of the CTA's first tile; tiles before it
   uint32_t tmem_base;
   int abort;
@@ -131,10 +131,13 @@ static_assert(sizeof(Barriers) <= kBarBytes, "barrier block");
 __device__ __forceinline__ bool vote(bool x) { return __all_sync(0xffffffffu, x); }
 
 // Places of the list that a tile takes. A batch of chunks mixes units of two row tiles with units of one (decode steps
-// among them, whose tiles are a matter of their bytes): there a tile of two row tiles takes 4 places, of one kSingle.
+// among them, whose tiles are a matter of their bytes): there a tile of two row tiles takes 4 places, of one 3, or at d =
+// 64 with copies of more than 16 rows 2 (40 requests of up to 9000 keys, 60 % of them decode steps, 24/8 heads of 64:
+// 64-token pages 205 us with 2 and 217 with 3, 48-token ones, which take copies of 16 rows, 228 and 218; 32/8 heads of
+// 128, 16-token pages, up to 30000 keys: 723 with 3, 876 with 2 before both streams took such tiles).
 template <int D, int kTiles, bool kChunk>
 struct Places {
-  static constexpr int kTile = kChunk && kTiles == 2 ? 4 : 1, kSingle = kTile == 1 ? 1 : D == 64 ? 2 : 3;
+  static constexpr int kTile = kChunk && kTiles == 2 ? 4 : 1;
   static constexpr int kCost = tree_unit_cost(D) * kTile;
 };
 
@@ -148,7 +151,8 @@ struct SeqTiles {
   int row_units;     // units of a KV head
   int shift;         // chunks: as in Seg
   int places;        // chunks: of a KV head
-  int largest;       // chunks: places of the largest unit
+  int largest, smallest;  // chunks: places of the largest and the smallest unit
+  int single;        // chunks: places of a tile of one row tile
   // places of the list; the host bounds their sum
   __device__ __forceinline__ int all(int head_groups) const {
     return kChunk ? places * head_groups : (per_unit + P::kCost) * row_units * head_groups;
@@ -164,7 +168,7 @@ struct SeqTiles {
   }
   // chunks: places of a tile of unit u
   __device__ __forceinline__ int weight(int u, int tile_nodes) const {
-    return nq - u * kTiles * tile_nodes > tile_nodes ? P::kTile : P::kSingle;
+    return nq - u * kTiles * tile_nodes > tile_nodes ? P::kTile : single;
   }
 };
 template <int D, int kTiles, bool kChunk>
@@ -181,11 +185,13 @@ __device__ __forceinline__ SeqTiles<D, kTiles, kChunk> seq_tiles(const TreeArgs&
   if constexpr (kChunk) {
     s.shift = a.causal ? s.nk - s.nq : s.nk - 1;  // (its sum with nq fits: the host sees to that)
     s.places = s.row_units * Places<D, kTiles, kChunk>::kCost;
-    s.largest = 0;
+    s.single = Places<D, kTiles, kChunk>::kTile == 1 ? 1 : D == 64 && a.piece > 16 ? 2 : 3;
+    s.largest = 0, s.smallest = 0x7fffffff;
     for (int u = 0; u < s.row_units; ++u) {
       const int n = s.template unit_tiles<kKeys>(u, unit_nodes) * s.weight(u, a.tile_nodes);
       s.places += n;
       s.largest = max(s.largest, n + Places<D, kTiles, kChunk>::kCost);
+      s.smallest = min(s.smallest, n + Places<D, kTiles, kChunk>::kCost);
     }
   }
   return s;
@@ -464,22 +470,25 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   const bool wide = a.num_seqs > 128;
   const int run = wide ? (a.num_seqs + C::kThreads - 1) / C::kThreads : (a.num_seqs + 31) / 32;
   const int run0 = min((wide ? tid : lane) * run, a.num_seqs), run1 = min(run0 + run, a.num_seqs);
-  int mine = 0, incl = 0, largest = 0;
+  int mine = 0, incl = 0, largest = 0, smallest = 0x7fffffff;
   if (wide || warp == C::kTmaWarp) {
 #pragma unroll 4
     for (int b = run0; b < run1; ++b) {
       const auto q = seq_tiles<D, kTiles, kChunk>(a, b);
       mine += q.all(a.head_groups);
-      if constexpr (kChunk) largest = max(largest, q.largest);
+      if constexpr (kChunk) largest = max(largest, q.largest), smallest = min(smallest, q.smallest);
     }
-    if constexpr (kChunk) largest = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(largest)));
+    if constexpr (kChunk) {
+      largest = __reduce_max_sync(0xffffffffu, largest);
+      smallest = __reduce_min_sync(0xffffffffu, smallest);
+    }
     incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += x;
     }
-    if (wide && lane == 31) bar->scan[warp] = incl, bar->largest[warp] = largest;
+    if (wide && lane == 31) bar->scan[warp] = incl, bar->largest[warp] = largest, bar->smallest[warp] = smallest;
   }
   tc_fence_before();
   __syncthreads();
@@ -489,8 +498,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   asm volatile("griddepcontrol.launch_dependents;");
   int my_begin = 0, my_end = 0;  // the group's places
   // Chunks: a unit that several CTAs share costs them their parts and the merge, about what 8 tiles take (16 at d = 256).
-  // Where the largest unit is no longer than that, and a share that is smaller than it, the CTA in whose share a unit
-  // begins takes it whole: 32 requests of 500 keys and one token, d = 128, 25.4 -> 20.3 us, 4 of 1000 and 128 tokens 33.8
+  // Where the largest unit is no longer than that and a share together (or, where several units may begin in a share,
+  // than that alone), the CTA in whose share a unit begins takes it whole: 32 requests of 500 keys and one token, d = 128, 25.4 -> 20.3 us, 4 of 1000 and 128 tokens 33.8
   // -> 30.5, 8 of 600 and 200 at d = 256 46.9 -> 41.0. With 12 tiles 4 of 1000 keys and 64 tokens took 28.7 us, not 24.3.
   bool whole_units = false;
   if (wide || warp == C::kTmaWarp) {
@@ -500,14 +509,14 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       for (int w = 0; w < C::kWarps; ++w) {
         if (w == warp) before += T;
         T += bar->scan[w];
-        if (kChunk) largest = max(largest, bar->largest[w]);
+        if (kChunk) largest = max(largest, bar->largest[w]), smallest = min(smallest, bar->smallest[w]);
       }
     }
     const Share share(T, a.groups, P::kTile);
     if (group < share.G && T > 0) my_begin = share.begin(group), my_end = share.begin(group + 1);
     if constexpr (kChunk) {
       constexpr int kMerge = (D == 256 ? 16 : 8) * P::kTile;  // what the parts and the merge take, in places
-      whole_units = largest <= kMerge + (share.per < largest ? share.per : 0);
+      whole_units = largest <= kMerge + (share.per <= smallest ? share.per : 0);
     }
     if (my_begin < my_end && before <= my_begin && my_begin < before + mine) {
       int b = run0;
