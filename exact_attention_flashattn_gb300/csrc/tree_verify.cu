@@ -17,11 +17,13 @@
 // What bounds it: one row of p (and of q) a request, V values, and for few requests the latency of what follows one
 // another: lengths, links and tokens, their probabilities, the walk, the row, its sums, the border. A cluster of CTAs
 // takes a request, each a part of the row; all of them walk the tree alike and send one another their sums. 64 trees
-// over 131072 tokens: 11.3 us, 3.0 TB/s, of which the row takes 6 (with cluster barriers around the sums, a second
+// over 131072 tokens: 11.0 us, 3.0 TB/s, of which the row takes 6 (with cluster barriers around the sums, a second
 // pass over a warp's run for the border and the walk in 64 bits: 25 us). A request whose drafts are refused one by
-// one takes a sum each, 6 us over 151007 tokens (117 instructions for 32 x 4 values, two warps a scheduler), which 40
-// drawn trees' 30.5 us end with. Not faster: 512 threads a CTA, rows through a deeper ring in shared memory, a
-// cluster spread over the SMs.
+// one takes a sum each, 5 us over 151007 tokens (2.1 of them the walk and the exchange; the rest the latency of the
+// values' arithmetic at two warps a scheduler), which 40 drawn trees' 26.8 us end with. Not faster: 512 threads a CTA,
+// rows through a deeper ring in shared memory, a cluster spread over the SMs, rows read to and fro.
+#include <type_traits>
+
 #include "kernels.h"
 #include "packed.cuh"
 #include "ptx.cuh"
@@ -33,30 +35,35 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxNodes = kTreeMaxNodes;
-// An SM: four CTAs of 64 registers, so that 64 requests are under way at once; with draft probabilities two of 112 (40
-// trees 30.5 us, three of 80 registers 33.0, four with spills 40.6).
+// An SM: four CTAs of 64 registers, so that 64 requests are under way at once; with draft probabilities two of 103 (40
+// trees over 151007 tokens: three of 80 registers take 1.08 times as long, four, with spills, 1.33).
 constexpr int ctas(bool drawn) { return drawn ? 2 : 4; }
-constexpr int kBatch = 4;  // pieces of a row that a lane has under way
+constexpr int kBatch = 4;  // pieces of a row that a lane has under way (40 drawn trees: 26.8 us, with 6 29.2, 8 29.6)
 
 // Values in [0, 1] (NaN and negative ones: 0, larger ones: 1).
 __device__ __forceinline__ float unit(float x) { return __saturatef(x); }
 
 // A non-negative value x as a multiple of 2^-44: `big` 2^-22ths, `small` the rest. Adding 3 (1.5 * 2^-21) rounds to a
-// multiple of 2^-22 (2^-44), which then stands in the last bits.
+// multiple of 2^-22 (2^-44), which then stands in the last bits: `big` and `small` are those bits, 3's (1.5 * 2^-21's)
+// still in them, and count from kBigBits and kSmallBits.
+constexpr float kBig = 3.f, kSmall = 0x1.8p-21f;
+constexpr uint32_t kBigBits = 0x40400000u, kSmallBits = 0x35400000u;
 struct Fixed {
-  int big, small;
+  uint32_t big, small;
 };
-__device__ __forceinline__ int64_t whole(Fixed f) { return (static_cast<int64_t>(f.big) << 22) + f.small; }
+__device__ __forceinline__ int64_t whole(int big, int small) { return (static_cast<int64_t>(big) << 22) + small; }
+__device__ __forceinline__ int64_t whole(Fixed f) {
+  return whole(static_cast<int>(f.big - kBigBits), static_cast<int>(f.small - kSmallBits));
+}
 
-// Four values of r = max(p - A q, 0), A = a_hi + a_lo (kDrawn and A not 0), or r = p, each as a multiple of 2^-44
+// Four values of r = max(p - A q, 0), A = a_hi + a_lo (kDrawn), or r = p, each as a multiple of 2^-44
 template <bool kDrawn>
 __device__ __forceinline__ void four(const float (&p)[4], const float (&q)[4], float a_hi, float a_lo, Fixed (&f)[4]) {
-  constexpr float kBig = 3.f, kSmall = 0x1.8p-21f;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const pair_t x = pair(unit(p[2 * i]), unit(p[2 * i + 1]));
     pair_t s = x, lo = 0;
-    if (kDrawn && a_hi != 0.f) {
+    if constexpr (kDrawn) {  // (also where A = 0 and q does not count: without a branch 26.8 us, with one 28.3)
       const pair_t y = pair(unit(q[2 * i]), unit(q[2 * i + 1])), hi2 = pair(a_hi, a_hi);
       const pair_t m = mul(pair(-a_hi, -a_hi), y);                         // A q = -m + m_lo
       const pair_t m_lo = fma(pair(a_lo, a_lo), y, fma(hi2, y, m));
@@ -66,9 +73,8 @@ __device__ __forceinline__ void four(const float (&p)[4], const float (&q)[4], f
     }
     const pair_t a = add(s, pair(kBig, kBig)), rest = add(sub(s, add(a, pair(-kBig, -kBig))), lo), b = add(rest, pair(kSmall, kSmall));
     const bool some0 = !kDrawn || first(s) > -first(lo), some1 = !kDrawn || second(s) > -second(lo);
-    f[2 * i] = Fixed{some0 ? __float_as_int(first(a)) - __float_as_int(kBig) : 0, some0 ? __float_as_int(first(b)) - __float_as_int(kSmall) : 0};
-    f[2 * i + 1] = Fixed{some1 ? __float_as_int(second(a)) - __float_as_int(kBig) : 0,
-                         some1 ? __float_as_int(second(b)) - __float_as_int(kSmall) : 0};
+    f[2 * i] = some0 ? Fixed{__float_as_uint(first(a)), __float_as_uint(first(b))} : Fixed{kBigBits, kSmallBits};
+    f[2 * i + 1] = some1 ? Fixed{__float_as_uint(second(a)), __float_as_uint(second(b))} : Fixed{kBigBits, kSmallBits};
   }
 }
 __device__ __forceinline__ int64_t fixed(float p) {  // the same of one p
@@ -128,18 +134,29 @@ struct Row {
   }
 };
 
-// Pieces of a warp's run: whole turns of 32, the runs of a cluster's warps one behind the other.
-__device__ __forceinline__ int run_of(int pieces, int cluster) { return (pieces + 32 * kWarps * cluster - 1) / (32 * kWarps * cluster) * 32; }
-
-template <bool kDrawn>
+// Piece `piece`, or 0 where it is not in front of `end`. kWhole: only pieces that lie in the row from end to end, and
+// of a q whose pieces begin where p's do: one load under a condition, so that a batch's arithmetic is one block of code
+// (40 drawn trees 30.5 -> 26.8 us; without q, where there is little of it, 11.0 us against 11.3 the other way round).
+template <bool kDrawn, bool kWhole>
 __device__ __forceinline__ void load_piece(const Row& row, bool with_q, int piece, int end, float (&p)[4], float (&q)[4]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) p[e] = q[e] = 0.f;
-  if (piece < end) {
+  if constexpr (kWhole) {
+    const int e = 4 * piece - row.skip;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    const bool in = piece < end && e >= 0 && e + 4 <= row.V;
+    if (in) x = *reinterpret_cast<const float4*>(row.p + e);
+    if (kDrawn && in && with_q) y = *reinterpret_cast<const float4*>(row.q + e);
+    p[0] = x.x, p[1] = x.y, p[2] = x.z, p[3] = x.w;
+    if (kDrawn) q[0] = y.x, q[1] = y.y, q[2] = y.z, q[3] = y.w;
+  } else if (piece < end) {
     row.load(row.p, piece, true, p);
     if (kDrawn && with_q) row.load(row.q, piece, row.q_alike, q);
   }
 }
+
+// Pieces of a warp's run: whole turns of 32, the runs of a cluster's warps one behind the other.
+__device__ __forceinline__ int run_of(int pieces, int cluster) { return (pieces + 32 * kWarps * cluster - 1) / (32 * kWarps * cluster) * 32; }
 
 enum State { kSum, kReady };  // r has to be summed; the walk is over and r's sums are there
 
@@ -158,23 +175,6 @@ struct Shared {
   int count, num_refused, state, abort;
   float a_hi, a_lo;
 };
-
-// The sums over the warp of N values a lane: value i is then in lanes 32 / N i .. 32 / N (i + 1) - 1.
-template <int N>
-__device__ __forceinline__ int64_t sums_of(int64_t (&x)[N], int lane) {
-#pragma unroll
-  for (int n = N, off = 16; n > 1; n /= 2, off /= 2) {
-    const bool upper = lane & off;
-#pragma unroll
-    for (int i = 0; i < n / 2; ++i) {
-      const int64_t give = upper ? x[i] : x[i + n / 2], keep = upper ? x[i + n / 2] : x[i];
-      x[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-    }
-  }
-#pragma unroll
-  for (int off = 16 / N; off > 0; off /= 2) x[0] += __shfl_xor_sync(0xffffffffu, x[0], off);
-  return x[0];
-}
 
 template <bool kDrawn>
 __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(const VerifyArgs a, int cluster) {
@@ -299,27 +299,45 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
     const int run = run_of(row.pieces, cluster), v0 = min((rank * kWarps + warp) * run, row.pieces), v1 = min(v0 + run, row.pieces);
     mine = 0;
     const bool with_q = a_hi != 0.f;  // A = 0: r is p
-    float p[kBatch][4], q[kBatch][4];
+    auto sum_run = [&](auto whole_pieces) {
+      constexpr bool kWhole = decltype(whole_pieces)::value;
+      float p[kBatch][4], q[kBatch][4];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) load_piece<kDrawn>(row, with_q, v0 + 32 * i + lane, v1, p[i], q[i]);
-    for (int v = v0; v < v1; v += 32 * kBatch) {
-      int64_t sum[kBatch];
+      for (int i = 0; i < kBatch; ++i) load_piece<kDrawn, kWhole>(row, with_q, v0 + 32 * i + lane, v1, p[i], q[i]);
+      for (int v = v0; v < v1; v += 32 * kBatch) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        Fixed f[4];
-        four<kDrawn>(p[i], q[i], a_hi, a_lo, f);
-        load_piece<kDrawn>(row, with_q, v + 32 * (i + kBatch) + lane, v1, p[i], q[i]);
-        sum[i] = whole(Fixed{f[0].big + f[1].big + f[2].big + f[3].big, f[0].small + f[1].small + f[2].small + f[3].small});
+        for (int i = 0; i < kBatch; ++i) {
+          Fixed f[4];
+          four<kDrawn>(p[i], q[i], a_hi, a_lo, f);
+          load_piece<kDrawn, kWhole>(row, with_q, v + 32 * (i + kBatch) + lane, v1, p[i], q[i]);
+          // (128 values are below 2^30 in either part)
+          const int big = __reduce_add_sync(0xffffffffu, static_cast<int>(f[0].big + f[1].big + f[2].big + f[3].big - 4 * kBigBits));
+          const int small =
+              __reduce_add_sync(0xffffffffu, static_cast<int>(f[0].small + f[1].small + f[2].small + f[3].small - 4 * kSmallBits));
+          const int64_t x = whole(big, small);
+          const int g = (v - v0) / 32 + i;
+          if (lane == 0 && 32 * g < v1 - v0) sm.group[warp][g] = x;
+          mine += x;
+        }
       }
-      const int64_t x = sums_of(sum, lane);
-      const int g = (v - v0) / 32 + lane / (32 / kBatch);
-      if (lane % (32 / kBatch) == 0) {
-        if (32 * g < v1 - v0) sm.group[warp][g] = x;
+    };
+    if (kDrawn && (!with_q || row.q_alike)) {
+      sum_run(std::true_type{});
+      // the pieces that reach past the row, its first and its last
+#pragma unroll 1
+      for (int piece = row.skip ? 0 : row.pieces - 1; piece < row.pieces; piece += max(row.pieces - 1, 1)) {
+        if (piece < v0 || piece >= v1 || (4 * piece >= row.skip && 4 * piece + 4 <= row.V + row.skip)) continue;
+        float p[4], q[4];
+        load_piece<kDrawn, false>(row, with_q, piece, v1, p, q);
+        Fixed f[4];
+        four<kDrawn>(p, q, a_hi, a_lo, f);
+        const int64_t x = whole(f[0]) + whole(f[1]) + whole(f[2]) + whole(f[3]);
+        if (lane == 0) sm.group[warp][(piece - v0) / 32] += x;
         mine += x;
       }
+    } else {
+      sum_run(std::false_type{});
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
     if constexpr (!kDrawn) {
       __syncwarp();
       for (int x = 0; x < sm.num_refused; ++x) {
@@ -350,8 +368,15 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
       if (lane < cluster) send(&sm.part[turn & 1][rank], arrived, lane, cta);
     }
     const bool ok = mbar_wait(arrived, turn >> 1 & 1, a.timeout_ns, &sm.abort);
-    if (!ok && tid == 0) raise_timeout(&sm.abort, a.status);
-    if (!__syncthreads_and(ok)) return;
+    if (!__syncthreads_and(ok)) {
+      // The others may still send to this CTA: it stays until each of them has ended or given up as well, and for a
+      // moment more, in which what they sent arrives.
+      if (tid == 0) raise_timeout(&sm.abort, a.status);
+      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+      const int never = 0;
+      mbar_wait(arrived, turn >> 1 & 1, 1000000, &never);
+      return;
+    }
     before = total = 0;
     for (int r = 0; r < cluster; ++r) {
       if (r == rank) before = total;
@@ -401,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
     sum += __shfl_sync(0xffffffffu, x, 31);
   }
   float p[4], q[4];
-  load_piece<kDrawn>(row, a_hi != 0.f, v0 + 32 * g + lane, v1, p, q);
+  load_piece<kDrawn, false>(row, a_hi != 0.f, v0 + 32 * g + lane, v1, p, q);
   const int t = 4 * (v0 + 32 * g + lane) - row.skip;
   Fixed fixed4[4];
   four<kDrawn>(p, q, a_hi, a_lo, fixed4);
