@@ -39,6 +39,15 @@
 // shared memory before the P.V of the tile; rows that do see those get them back at the end.
 // Every wait is bounded; a timed-out wait sets the device status word, the CTA stops producing
 // output, waits for its own copies and MMAs and frees its TMEM.
+//
+// Chunks (kChunk): the new tokens' own K and V are in the cache too, and the mask is the causal one at the sequence's
+// end, token i of nq seeing keys up to i + nk - nq. A chunk of thousands of tokens has many units, which end at their
+// own last key; the tiles that all of a unit's rows see come first, through the loops without masks, then those on the
+// diagonal. The operations bound it: 2 x 8192 tokens of 32/8 heads of 128 take 715 us, 1540 TFLOP/s (as packed K and V
+// 639), 512 tokens behind 65024 330 us, 1660 TFLOP/s. A batch mixes them with decode steps, of which a unit is one row
+// tile: there both streams take it (even and odd key tiles, joined through tensor memory at its end), as one stream
+// alone reads K and V at half the rate that HBM gives (40 requests, 60 % of them decode steps, 24/8 heads of 64: 238
+// -> 222 us, now 213).
 #include <math.h>
 
 #include <atomic>
@@ -133,7 +142,7 @@ __device__ __forceinline__ bool vote(bool x) { return __all_sync(0xffffffffu, x)
 // Places of the list that a tile takes. A batch of chunks mixes units of two row tiles with units of one (decode steps
 // among them, whose tiles are a matter of their bytes): there a tile of two row tiles takes 4 places, of one 3, or at d =
 // 64 with copies of more than 16 rows 2 (40 requests of up to 9000 keys, 60 % of them decode steps, 24/8 heads of 64:
-// 64-token pages 205 us with 2 and 217 with 3, 48-token ones, which take copies of 16 rows, 228 and 218; 32/8 heads of
+// 64-token pages 206 us with 2 and 217 with 3, 48-token ones, which take copies of 16 rows, 223 and 213; 32/8 heads of
 // 128, 16-token pages, up to 30000 keys: 723 with 3, 876 with 2 before both streams took such tiles).
 template <int D, int kTiles, bool kChunk>
 struct Places {
@@ -499,8 +508,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   int my_begin = 0, my_end = 0;  // the group's places
   // Chunks: a unit that several CTAs share costs them their parts and the merge, about what 8 tiles take (16 at d = 256).
   // Where the largest unit is no longer than that and a share together (or, where several units may begin in a share,
-  // than that alone), the CTA in whose share a unit begins takes it whole: 32 requests of 500 keys and one token, d = 128, 25.4 -> 20.3 us, 4 of 1000 and 128 tokens 33.8
-  // -> 30.5, 8 of 600 and 200 at d = 256 46.9 -> 41.0. With 12 tiles 4 of 1000 keys and 64 tokens took 28.7 us, not 24.3.
+  // than that alone), the CTA in whose share a unit begins takes it whole: 32 requests of 500 keys and one token,
+  // d = 128, 25.4 -> 20.3 us, 4 of 1000 and 128 tokens 33.8 -> 30.5, 8 of 600 and 200 at d = 256 46.9 -> 41.0. With 12
+  // tiles in place of 8, 4 of 1000 keys and 64 tokens took 28.7 us, not 24.3.
   bool whole_units = false;
   if (wide || warp == C::kTmaWarp) {
     int T = __shfl_sync(0xffffffffu, incl, 31), before = incl - mine;
