@@ -133,14 +133,15 @@ int attn_tree_verify(const int32_t* tokens, const int32_t* parents, const int32_
   const int64_t most = static_cast<int64_t>(1) << 38;
   if (target_stride < vocab || target_stride >= most || (draft_probs && (draft_stride < vocab || draft_stride >= most)))
     return BWATTN_ERR_INVALID_ARG;
-  // every CTA of a request reads all of its inputs, so no output may stand in an input's place
+  // every CTA of a request reads all of its inputs, so no output may stand in an input's place, nor in another output's
   const void* in[] = {tokens, parents, cu_seqlens_q, target_probs, draft_probs, uniforms, sample_uniforms};
   const void* out[] = {accepted, counts, next_tokens};
   for (const void* y : out)
     for (const void* x : in)
       if (x && x == y) return BWATTN_ERR_INVALID_ARG;
+  if (accepted == counts || accepted == next_tokens || (counts && counts == next_tokens)) return BWATTN_ERR_INVALID_ARG;
   bw::VerifyArgs a{tokens, parents, cu_seqlens_q, target_probs, draft_probs, uniforms, sample_uniforms, accepted, counts,
-                         next_tokens, target_stride, draft_stride, num_seqs, total_q, max_nodes, vocab, nullptr, 0};
+                   next_tokens, target_stride, draft_stride, num_seqs, total_q, max_nodes, vocab, nullptr, 0};
   const cudaError_t e = bw::launch_tree_verify(a, static_cast<cudaStream_t>(stream));
   if (e == cudaSuccess) bw::count_launch();
   return done(e);

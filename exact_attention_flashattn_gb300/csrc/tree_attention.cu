@@ -556,10 +556,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar->seg_empty[k % kSegSlots]);
   };
-  // rows of the unit's row tile w that exist
   // chunks: keys that every row of the unit sees, and its first tile that some row does not see whole
   auto all_see = [&](const Seg& s) { return min(max(s.shift + s.node0 + 1, 0), s.nk); };
   auto first_masked = [&](const Seg& s) { return all_see(s) / kKeys; };
+  // rows of the unit's row tile w that exist
   auto tile_rows = [&](const Seg& s, int w) { return max(0, min(tile_nodes, s.nq - s.node0 - w * tile_nodes)) * a.g; };
 
   // paged: the copy of a tile (atom copy % kHalves of piece copy / kHalves) that is this lane's; with a

@@ -497,7 +497,7 @@ int attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, co
  * becomes 0. Behind the last kept node comes the first token whose running sum of r exceeds w times r's sum (of
  * p's, where r is all 0), w < 1 the request's sample_uniform. Sums are taken of values rounded to
  * 2^-44, in integers: the same whatever the launch. Supported: vocab <= 500000, max_nodes <= 1024 (further nodes
- * of a request are not tried). Strides at least vocab; outputs in an input's place: INVALID_ARG.
+ * of a request are not tried). Strides at least vocab; outputs in an input's place or in one another's: INVALID_ARG.
  */
 int attn_tree_verify(const int32_t* tokens, const int32_t* parents, const int32_t* cu_seqlens_q, const float* target_probs,
                      const float* draft_probs, const float* uniforms, const float* sample_uniforms, int32_t* accepted,

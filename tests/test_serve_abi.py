@@ -97,6 +97,8 @@ def test_verify_refusals(L):
     for i, out in enumerate(("acc", "cnt", "nxt")):  # an output in an input's place
         for j in range(7):
             assert verify(L, **{out: FAKE * (j + 1)}) == BAD, (out, j)
+    for kw in (dict(acc=FAKE * 9), dict(acc=FAKE * 10), dict(cnt=FAKE * 10)):  # or in another output's
+        assert verify(L, **kw) == BAD, kw
     assert verify(L, n=0, tq=0, tok=None, p=None, acc=None, cnt=None) == bw.OK
 
 
