@@ -62,7 +62,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) qk_rope_kernel(cons
   constexpr int kLanes = D / 16, kHeads = 32 / kLanes;  // lanes a head, heads a turn
   constexpr int kWarps = kRopeThreads / 32, kMine = D / 64;  // kMine: a lane's pairs
   __shared__ __align__(16) float sm_coef[kWarps][2][2][D];  // C and S of q's channels and of k's
-  __shared__ __align__(16) float sm_x[kMode == kHalvesAny ? kWarps : 1][kMode == kHalvesAny ? kHeads : 1][kMode == kHalvesAny ? D : 1];
+  // kHalvesAny: a turn's values; a word between pieces and some between heads, so that a warp's lanes, each at the same
+  // place of its piece, are in 32 banks (16384 rows of 40 heads of 128, 17 pairs: without them 101 us, with them, and
+  // second pieces left alone where they hold no pair, 78)
+  constexpr int kHeadWords = D + D / 8 + (D == 64 ? 28 : D == 128 ? 24 : 16);
+  static_assert(kHeadWords % 32 == 9 * kLanes % 32, "banks");
+  __shared__ float sm_x[kMode == kHalvesAny ? kWarps : 1][kMode == kHalvesAny ? kHeads : 1][kMode == kHalvesAny ? kHeadWords : 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t = lane % kLanes, group = lane / kLanes;
@@ -165,14 +170,30 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) qk_rope_kernel(cons
         float* sx = sm_x[warp][group];
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float2*>(sx + 8 * (i < 4 ? pa : pb) + 2 * (i & 3)) = make_float2(first(x[i]), second(x[i]));
-        __syncwarp();
-        auto partner = [&](int c) { return c < a.pairs ? sx[c + a.pairs] : c < 2 * a.pairs ? sx[c - a.pairs] : 0.f; };
+        for (int i = 0; i < 4; ++i) {
+          float* at = sx + 9 * pa + 2 * i;
+          at[0] = first(x[i]), at[1] = second(x[i]);
+          other[i + 4] = 0;
+        }
+        const bool both = 4 * a.pairs > D;  // else none of the second pieces' channels is turned
+        if (both) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = 8 * (i < 4 ? pa : pb) + 2 * (i & 3);
-          other[i] = pair(partner(c), partner(c + 1));
+          for (int i = 4; i < 8; ++i) {
+            float* at = sx + 9 * pb + 2 * (i - 4);
+            at[0] = first(x[i]), at[1] = second(x[i]);
+          }
+        }
+        __syncwarp();
+        // channel e of piece p: its partner is `pairs` on, or back
+        auto partner = [&](int p, int e) {
+          const int c = 8 * p + e, on = e + a.pairs, back = e - a.pairs;
+          return c < 2 * a.pairs ? sx[9 * p + (c < a.pairs ? on + (on >> 3) : back + (back >> 3))] : 0.f;
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) other[i] = pair(partner(pa, 2 * i), partner(pa, 2 * i + 1));
+        if (both) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) other[i + 4] = pair(partner(pb, 2 * i), partner(pb, 2 * i + 1));
         }
       } else {
 #pragma unroll
