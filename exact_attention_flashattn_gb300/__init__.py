@@ -725,7 +725,7 @@ def _chunk(st, dev, q, k, v, table, nk, cu, most, causal, scale, workspace, out,
     qs = _rows(q, "q", dev, q.shape)
     nkp = _like(nk, "nk", dev, _I32, (num_seqs,))
     cup = _like(cu, "cu_seqlens_q", dev, _I32, (num_seqs + 1,))
-    out = _out(out, "out", dev, _BF16, q.shape)
+    out = torch.empty_like(q) if out is None else _out(out, "out", dev, _BF16, q.shape)
     if lse is True:
         lse = torch.empty((tq, Hq), dtype=_F32, device=dev)
     elif not isinstance(lse, _Tensor):
@@ -772,12 +772,13 @@ def _qk_rope(st, dev, q, k, positions, freq, q_weight, k_weight, eps, axes, inte
     ap = None if axes is None else _like(axes, "axes", dev, _I32, (pairs,))
     qw = None if q_weight is None else _like(q_weight, "q_weight", dev, _BF16, (d,))
     kw = None if k_weight is None else _like(k_weight, "k_weight", dev, _BF16, (d,))
+    # (empty_like() of rows that lie apart is contiguous; two empty() take the host 1.5 us more)
     if q_out is None:
-        q_out, qos = torch.empty((n, Hq, d), dtype=_BF16, device=dev), Hq * d
+        q_out, qos = torch.empty_like(q), Hq * d
     else:
         qos = _rows(q_out, "q_out", dev, q.shape)
     if k_out is None:
-        k_out, kos = torch.empty((n, Hkv, d), dtype=_BF16, device=dev), Hkv * d
+        k_out, kos = torch.empty_like(k), Hkv * d
     else:
         kos = _rows(k_out, "k_out", dev, k.shape)
     rc = (_lib or lib()).attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), pp, ap, fp, qw, kw,
