@@ -35,7 +35,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxNodes = kTreeMaxNodes;
-// An SM: four CTAs of 64 registers, so that 64 requests are under way at once; with draft probabilities two of 103 (40
+// An SM: four CTAs of 64 registers, so that 64 requests are under way at once; with draft probabilities two of 114 (40
 // trees over 151007 tokens: three of 80 registers take 1.08 times as long, four, with spills, 1.33).
 constexpr int ctas(bool drawn) { return drawn ? 2 : 4; }
 constexpr int kBatch = 4;  // pieces of a row that a lane has under way (40 drawn trees: 26.8 us, with 6 29.2, 8 29.6)
@@ -160,7 +160,8 @@ __device__ __forceinline__ int run_of(int pieces, int cluster) { return (pieces 
 
 enum State { kSum, kReady };  // r has to be summed; the walk is over and r's sums are there
 
-constexpr int kMaxGroups = (kVerifyMaxVocab / 4 + 1 + 32 * kWarps * kMaxCluster - 1) / (32 * kWarps * kMaxCluster);
+constexpr int kMaxGroups = 128;  // that a warp's run may have
+static_assert(kVerifyMaxVocab / 4 + 2 <= 32 * kWarps * kMaxCluster * kMaxGroups, "groups");
 
 struct Shared {
   uint64_t arrived[2];           // the CTAs' sums, of two sums in turns
@@ -459,9 +460,14 @@ cudaError_t launch_tree_verify(VerifyArgs& a, cudaStream_t stream) {
   const cudaError_t e = status_word(&a.status);
   if (e != cudaSuccess) return e;
   a.timeout_ns = wait_timeout_ns();
-  // CTAs a request: as many as keep a warp busy with some pieces of its row
+  // CTAs a request: as many as keep a warp busy with some pieces of its row, fewer where there are many requests (what
+  // a CTA does beside its part of the row is the same for all: 300 trees over 65536 tokens, 8 CTAs each 27.5 us, 4 19.6, 2
+  // 16.1, 1 18.1; 100 drawn ones over 131072 36.6, 39.6, 54.1), and enough to have places for the sums of a row's groups
+  constexpr int kMostCtas = 800, kPlaces = 32 * kWarps * kMaxGroups;
+  const int pieces = a.vocab / 4 + 2;  // at most
   int cluster = kMaxCluster;
-  while (cluster > 1 && a.vocab < cluster * kWarps * 128) cluster /= 2;
+  while (cluster > 1 && (a.vocab < cluster * kWarps * 128 || a.num_seqs * cluster > kMostCtas)) cluster /= 2;
+  while (pieces > cluster * kPlaces) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((a.num_seqs > 0 ? a.num_seqs : 1) * cluster));
   cfg.blockDim = dim3(kThreads);

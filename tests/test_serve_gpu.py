@@ -257,6 +257,21 @@ def test_verify_limits():
 
 
 @pytest.mark.parametrize("drawn", [False, True])
+@pytest.mark.parametrize("requests, V", [(130, 9001), (250, 9001), (450, 9001), (900, 9001), (150, 140001), (260, 300001)])
+def test_verify_many_requests(requests, V, drawn):
+    # fewer CTAs a request; rows whose groups need more of them than the requests leave
+    g, r = gen(requests), np.random.default_rng(requests)
+    lengths = [3, 0, 1] + r.integers(0, 4 if V < 10000 else 2, requests - 3).tolist()
+    n = sum(lengths)
+    parents = trees(lengths, "star", r)
+    p = probs(n, V, g)
+    q = torch.softmax(torch.log(p) + 0.7 * torch.randn((n, V), generator=g, device="cuda"), 1)
+    tokens = drafted(parents, lengths, q, g)
+    u, w = torch.rand(n, generator=g, device="cuda"), torch.rand(requests, generator=g, device="cuda")
+    check_verify(tokens, i32(parents), lengths, p, q if drawn else None, u, w)
+
+
+@pytest.mark.parametrize("drawn", [False, True])
 def test_verify_distribution(drawn):
     """The first token behind the root is distributed as p, whatever the drafts: each count of B trials lies within 5
     standard deviations of B p (of 13 tokens and two cases, less than one run in 10^5 would not)."""
