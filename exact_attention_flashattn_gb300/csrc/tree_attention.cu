@@ -175,9 +175,29 @@ struct SeqTiles {
     const int n = unit_keys(u, unit_nodes);
     return max(n / kKeys + (n % kKeys != 0), 1);
   }
-  // chunks: places of a tile of unit u
+  // chunks: places of a tile of unit u, and of the unit
   __device__ __forceinline__ int weight(int u, int tile_nodes) const {
     return nq - u * kTiles * tile_nodes > tile_nodes ? P::kTile : single;
+  }
+  __device__ __forceinline__ int unit_places(int u, int tile_nodes) const {
+    return unit_tiles<Cfg<D, kTiles>::kKeys>(u, kTiles * tile_nodes) * weight(u, tile_nodes) + P::kCost;
+  }
+  // chunks: sums over the units, by a lane, or by a converged warp whose lanes have the same sequence (a lane alone takes
+  // 30 ns a unit: with its sums and its search for a CTA's first unit 3855 tokens of 5 heads of 128, 78 units, took 50.0
+  // us, not 40.8; 16 prompts of 500 tokens, 32/8 heads of 128, 67.9 and 63.2)
+  __device__ __forceinline__ void count(int tile_nodes, int from = 0, int step = 1) {
+    places = largest = 0, smallest = 0x7fffffff;
+#pragma unroll 1
+    for (int u = from; u < row_units; u += step) {
+      const int n = unit_places(u, tile_nodes);
+      places += n, largest = max(largest, n), smallest = min(smallest, n);
+    }
+  }
+  __device__ __forceinline__ void count_warp(int tile_nodes, int lane) {
+    count(tile_nodes, lane, 32);
+    places = __reduce_add_sync(0xffffffffu, places);
+    largest = __reduce_max_sync(0xffffffffu, largest);
+    smallest = __reduce_min_sync(0xffffffffu, smallest);
   }
 };
 template <int D, int kTiles, bool kChunk>
@@ -193,15 +213,7 @@ __device__ __forceinline__ SeqTiles<D, kTiles, kChunk> seq_tiles(const TreeArgs&
   s.row_units = s.nq <= unit_nodes ? s.nq > 0 : (s.nq + unit_nodes - 1) / unit_nodes;  // 0 for a sequence without nodes
   if constexpr (kChunk) {
     s.shift = a.causal ? s.nk - s.nq : s.nk - 1;  // (its sum with nq fits: the host sees to that)
-    s.places = s.row_units * Places<D, kTiles, kChunk>::kCost;
     s.single = Places<D, kTiles, kChunk>::kTile == 1 ? 1 : D == 64 && a.piece > 16 ? 2 : 3;
-    s.largest = 0, s.smallest = 0x7fffffff;
-    for (int u = 0; u < s.row_units; ++u) {
-      const int n = s.template unit_tiles<kKeys>(u, unit_nodes) * s.weight(u, a.tile_nodes);
-      s.places += n;
-      s.largest = max(s.largest, n + Places<D, kTiles, kChunk>::kCost);
-      s.smallest = min(s.smallest, n + Places<D, kTiles, kChunk>::kCost);
-    }
   }
   return s;
 }
@@ -481,13 +493,28 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
   const int run0 = min((wide ? tid : lane) * run, a.num_seqs), run1 = min(run0 + run, a.num_seqs);
   int mine = 0, incl = 0, largest = 0, smallest = 0x7fffffff;
   if (wide || warp == C::kTmaWarp) {
+    if constexpr (!kChunk) {
 #pragma unroll 4
-    for (int b = run0; b < run1; ++b) {
-      const auto q = seq_tiles<D, kTiles, kChunk>(a, b);
-      mine += q.all(a.head_groups);
-      if constexpr (kChunk) largest = max(largest, q.largest), smallest = min(smallest, q.smallest);
-    }
-    if constexpr (kChunk) {
+      for (int b = run0; b < run1; ++b) mine += seq_tiles<D, kTiles, kChunk>(a, b).all(a.head_groups);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < run; ++i) {
+        auto q = seq_tiles<D, kTiles, kChunk>(a, min(run0 + i, a.num_seqs - 1));
+        if (run0 + i >= run1) q.row_units = 0;
+        // sequences of many units by the whole warp, one after the other
+        const unsigned many = __ballot_sync(0xffffffffu, q.row_units > 8);
+        if (!(many >> lane & 1)) q.count(a.tile_nodes);
+        for (unsigned left = many; left; left &= left - 1) {
+          const int from = __ffs(left) - 1;
+          auto x = q;
+          x.nq = __shfl_sync(0xffffffffu, q.nq, from), x.nk = __shfl_sync(0xffffffffu, q.nk, from);
+          x.shift = __shfl_sync(0xffffffffu, q.shift, from), x.row_units = __shfl_sync(0xffffffffu, q.row_units, from);
+          x.count_warp(a.tile_nodes, lane);
+          if (lane == from) q.places = x.places, q.largest = x.largest, q.smallest = x.smallest;
+        }
+        mine += q.all(a.head_groups);
+        largest = max(largest, q.largest), smallest = min(smallest, q.smallest);
+      }
       largest = __reduce_max_sync(0xffffffffu, largest);
       smallest = __reduce_min_sync(0xffffffffu, smallest);
     }
@@ -530,7 +557,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     }
     if (my_begin < my_end && before <= my_begin && my_begin < before + mine) {
       int b = run0;
-      for (int n; my_begin >= before + (n = seq_tiles<D, kTiles, kChunk>(a, b).all(a.head_groups)); ++b) before += n;
+      if constexpr (!kChunk)  // (chunks: the producer goes on from the thread's first sequence)
+        for (int n; my_begin >= before + (n = seq_tiles<D, kTiles, kChunk>(a, b).all(a.head_groups)); ++b) before += n;
       bar->list[1] = b;
       bar->list[2] = before;
     }
@@ -679,7 +707,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     const int head0 = static_cast<int>(blockIdx.x) - group * a.head_group, end = my_end;
     int pos = my_begin, b = pos < end ? bar->list[1] : 0, seq_at = pos < end ? bar->list[2] : 0;
     int nload = 0, nq[2] = {0, 0};  // K tiles, and Q tiles into each buffer
-    // chunks: the sequence, and the unit of it (and of a group of heads) that holds place pos, from place unit_at on
+    // chunks: the sequence (b is the next one), and the unit of it (and of a group of heads) that holds place pos, from place unit_at on
     SeqTiles<D, kTiles, kChunk> seq{};
     int heads = 0, unit = 0, unit_at = 0;
     // Units of a sequence read the same keys, each CTA its run of them. A CTA begins a run with the tile whose number is
@@ -688,11 +716,6 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     // GB of HBM reads in the runs' own order).
     const int share_tiles = max((my_end - my_begin) / P::kTile, 1);
     int taken = 0;
-    if (kChunk && pos < end) {
-      seq = seq_tiles<D, kTiles, kChunk>(a, b);
-      heads = (pos - seq_at) / seq.places;
-      unit_at = seq_at + heads * seq.places;
-    }
     bool ok = true;
     for (int k = 0; ok; ++k) {
       Seg s{};
@@ -700,12 +723,32 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       int tile_places = 1;
       while (kChunk && pos < end && !s.valid) {
         for (;;) {
-          if (pos >= seq_at + seq.all(a.head_groups)) {
+          if (pos >= seq_at + seq.all(a.head_groups)) {  // (before the list's first sequence, seq has no places)
             seq_at += seq.all(a.head_groups);
-            seq = seq_tiles<D, kTiles, kChunk>(a, ++b);
-            heads = unit = 0;
-            unit_at = seq_at;
-            continue;
+            seq = seq_tiles<D, kTiles, kChunk>(a, b++);
+            seq.count_warp(tile_nodes, lane);
+            if (pos >= seq_at + seq.all(a.head_groups)) continue;
+            heads = (pos - seq_at) / seq.places;
+            unit_at = seq_at + heads * seq.places;
+            // its unit, 32 at a time
+#pragma unroll 1
+            for (unit = 0;; unit += 32) {
+              const int n = unit + lane < seq.row_units ? seq.unit_places(unit + lane, tile_nodes) : 0;
+              int upto = n;
+#pragma unroll
+              for (int off = 1; off < 32; off <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += x;
+              }
+              const unsigned over = __ballot_sync(0xffffffffu, unit_at + upto > pos);
+              if (over || unit + 32 >= seq.row_units) {
+                const int hit = over ? __ffs(over) - 1 : seq.row_units - 1 - unit;
+                unit_at += __shfl_sync(0xffffffffu, upto - n, hit);
+                unit += hit;
+                break;
+              }
+              unit_at += __shfl_sync(0xffffffffu, upto, 31);
+            }
           }
           tile_places = seq.weight(unit, tile_nodes);
           size = seq.template unit_tiles<kKeys>(unit, kTiles * tile_nodes) * tile_places + P::kCost;
@@ -725,7 +768,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         s.nt = (max(to - P::kCost, 0) + tile_places - 1) / tile_places - s.k0;
         if (s.nt <= 0) continue;  // it ends before the unit's first tile, or began inside its last
         s.valid = 1;
-        s.b = b;
+        s.b = b - 1;
         s.tok0 = seq.tok0;
         s.nq = seq.nq;
         s.nk = seq.unit_keys(unit, kTiles * tile_nodes);
