@@ -512,6 +512,18 @@ def test_chunk_long():
         c.check(*c.run(), what=(d, nk))
 
 
+@pytest.mark.parametrize("d, B", [(64, 3), (128, 70), (64, 170), (256, 40)])
+def test_chunk_many_units(d, B):
+    # sequences of many units among such of one or none, one and several a lane of the list
+    r = np.random.default_rng(B)
+    nq = [int(x) for x in r.choice([0, 1, 5, 40, 300, 700], B, p=[0.1, 0.3, 0.2, 0.2, 0.1, 0.1])]
+    nq[0], nq[-1] = 700, 450
+    nk = [n + int(x) for n, x in zip(nq, r.integers(0, 200, B))]
+    for causal in (True, False):
+        c = Chunk(16, 2, d, 32, nk, nq, causal=causal, seed=B)
+        c.check(*c.run())
+
+
 def test_chunk_infinities_in_later_values():
     # V rows of a token that hold infinities and NaN reach its own and later tokens only
     for d in (64, 128, 256):
