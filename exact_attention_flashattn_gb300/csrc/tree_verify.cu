@@ -19,8 +19,8 @@
 // takes a request, each a part of the row; all of them walk the tree alike and send one another their sums. 64 trees
 // over 131072 tokens: 11.0 us, 3.0 TB/s, of which the row takes 6 (with cluster barriers around the sums, a second
 // pass over a warp's run for the border and the walk in 64 bits: 25 us). A request whose drafts are refused one by
-// one takes a sum each, 5 us over 151007 tokens (2.1 of them the walk and the exchange; the rest the latency of the
-// values' arithmetic at two warps a scheduler), which 40 drawn trees' 26.8 us end with. Not faster: 512 threads a CTA,
+// one takes a sum each, 4.8 us over 151007 tokens (1.8 of them the walk and the exchange; the rest the latency of the
+// values' arithmetic at two warps a scheduler), which 40 drawn trees' 25.9 us end with. Not faster: 512 threads a CTA,
 // rows through a deeper ring in shared memory, a cluster spread over the SMs, rows read to and fro.
 #include <type_traits>
 
@@ -51,6 +51,7 @@ constexpr uint32_t kBigBits = 0x40400000u, kSmallBits = 0x35400000u;
 struct Fixed {
   uint32_t big, small;
 };
+constexpr int64_t kOne = 1ll << 44;
 __device__ __forceinline__ int64_t whole(int big, int small) { return (static_cast<int64_t>(big) << 22) + small; }
 __device__ __forceinline__ int64_t whole(Fixed f) {
   return whole(static_cast<int>(f.big - kBigBits), static_cast<int>(f.small - kSmallBits));
@@ -221,8 +222,11 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
 
   // the walk's state (warp 0, its lanes alike)
   int next = 1, last = 0, count = 1, refused = 0;
-  double A = 0.0, S = 1.0;
-  float Af = 0.f, Sf = 1.f;
+  // A = a_hi + a_lo; S as a double without draft probabilities, as a sum of integers with them (64-bit floats on the way from
+  // a sum to the next one take a third of a microsecond)
+  float a_hi = 0.f, a_lo = 0.f, Sf = 1.f;
+  double S = 1.0;
+  int64_t S_int = kOne;
   bool summed = false;  // the sums below are of r as it is now
   // r's sums: of the CTAs before this one, of all, of this CTA's warps before this one, of this warp
   int64_t before = 0, total = 0, warps_before = 0, mine = 0;
@@ -236,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
             state = kReady;
           } else if (summed) {
             whole_row = true;
-            A = 0.0;
+            a_hi = a_lo = 0.f;
             refused = 0;
           }
           break;
@@ -257,23 +261,28 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
           for (int x = lane; x < refused; x += 32) again |= sm.refused[x] == t;
           again = __any_sync(0xffffffffu, again);
         }
-        const float bar = u * Sf * q, r = again ? 0.f : kDrawn ? p - Af * q : p;
+        const float bar = u * Sf * q, r = again ? 0.f : kDrawn ? p - a_hi * q : p;
         bool keep = bar < r;
-        if (!(fabsf(bar - r) > 0x1p-20f * (fabsf(bar) + p + Af * q))) {
+        if (!(fabsf(bar - r) > 0x1p-20f * (fabsf(bar) + p + a_hi * q))) {
+          const double A = static_cast<double>(a_hi) + a_lo, sum = kDrawn ? static_cast<double>(S_int) * 0x1p-44 : S;
           const double rd = again ? 0.0 : kDrawn ? fmax(p - A * q, 0.0) : p;
-          keep = u * S * q < rd;
+          keep = u * sum * q < rd;
         }
         if (keep) {
           last = c;
           if (lane == 0) sm.path[count] = c;
           ++count;
           refused = 0;
-          A = 0.0, Af = 0.f;
-          S = 1.0, Sf = 1.f;
+          a_hi = a_lo = 0.f;
+          S = 1.0, Sf = 1.f, S_int = kOne;
           summed = false;
         } else if constexpr (kDrawn) {
-          A += S;
-          Af = static_cast<float>(A);
+          // A += S, whose first 24 bits are Sf
+          const float s_lo = static_cast<float>(S_int - static_cast<int64_t>(Sf * 0x1p44f)) * 0x1p-44f;
+          const float t = a_hi + Sf, b = t - a_hi;  // a_hi + Sf = t + what follows, exactly
+          const float lo = (a_hi - (t - b)) + (Sf - b) + (a_lo + s_lo);
+          a_hi = t + lo;
+          a_lo = lo - (a_hi - t);
           break;
         } else if (!again) {
           S = fmax(S - p, 0.0);
@@ -286,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
       if (lane == 0) {
         sm.count = count;
         sm.num_refused = refused;
-        sm.a_hi = static_cast<float>(A);
-        sm.a_lo = static_cast<float>(A - sm.a_hi);
+        sm.a_hi = a_hi;
+        sm.a_lo = a_lo;
         sm.state = state;
       }
     }
@@ -296,10 +305,10 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
 
     // ---- the sum of r: each warp of the cluster takes a run of pieces
     const Row row(a, t0 + sm.path[sm.count - 1]);
-    const float a_hi = sm.a_hi, a_lo = sm.a_lo;
+    const float A_hi = sm.a_hi, A_lo = sm.a_lo;
     const int run = run_of(row.pieces, cluster), v0 = min((rank * kWarps + warp) * run, row.pieces), v1 = min(v0 + run, row.pieces);
     mine = 0;
-    const bool with_q = a_hi != 0.f;  // A = 0: r is p
+    const bool with_q = A_hi != 0.f;  // A = 0: r is p
     auto sum_run = [&](auto whole_pieces) {
       constexpr bool kWhole = decltype(whole_pieces)::value;
       float p[kBatch][4], q[kBatch][4];
@@ -309,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           Fixed f[4];
-          four<kDrawn>(p[i], q[i], a_hi, a_lo, f);
+          four<kDrawn>(p[i], q[i], A_hi, A_lo, f);
           load_piece<kDrawn, kWhole>(row, with_q, v + 32 * (i + kBatch) + lane, v1, p[i], q[i]);
           // (128 values are below 2^30 in either part)
           const int big = __reduce_add_sync(0xffffffffu, static_cast<int>(f[0].big + f[1].big + f[2].big + f[3].big - 4 * kBigBits));
@@ -331,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
         float p[4], q[4];
         load_piece<kDrawn, false>(row, with_q, piece, v1, p, q);
         Fixed f[4];
-        four<kDrawn>(p, q, a_hi, a_lo, f);
+        four<kDrawn>(p, q, A_hi, A_lo, f);
         const int64_t x = whole(f[0]) + whole(f[1]) + whole(f[2]) + whole(f[3]);
         if (lane == 0) sm.group[warp][(piece - v0) / 32] += x;
         mine += x;
@@ -385,8 +394,13 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
     }
     summed = true;
     if (warp == 0) {
-      S = static_cast<double>(total) * 0x1p-44;
-      Sf = static_cast<float>(S);
+      if constexpr (kDrawn) {
+        S_int = total;
+        Sf = static_cast<float>(total) * 0x1p-44f;
+      } else {
+        S = static_cast<double>(total) * 0x1p-44;
+        Sf = static_cast<float>(S);
+      }
     }
   }
 
@@ -404,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
   int64_t sum = before + warps_before;
   if (!(sum <= bar && bar < sum + mine)) return;
   const Row row(a, t0 + sm.path[sm.count - 1]);
-  const float a_hi = sm.a_hi, a_lo = sm.a_lo;
+  const float A_hi = sm.a_hi, A_lo = sm.a_lo;
   const int run = run_of(row.pieces, cluster), v0 = min((rank * kWarps + warp) * run, row.pieces), v1 = min(v0 + run, row.pieces);
   auto scan = [&](int64_t x) {
 #pragma unroll
@@ -427,10 +441,10 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
     sum += __shfl_sync(0xffffffffu, x, 31);
   }
   float p[4], q[4];
-  load_piece<kDrawn, false>(row, a_hi != 0.f, v0 + 32 * g + lane, v1, p, q);
+  load_piece<kDrawn, false>(row, A_hi != 0.f, v0 + 32 * g + lane, v1, p, q);
   const int t = 4 * (v0 + 32 * g + lane) - row.skip;
   Fixed fixed4[4];
-  four<kDrawn>(p, q, a_hi, a_lo, fixed4);
+  four<kDrawn>(p, q, A_hi, A_lo, fixed4);
   int64_t f[4], all = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
