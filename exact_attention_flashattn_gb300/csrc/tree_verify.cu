@@ -38,7 +38,7 @@ constexpr int kMaxNodes = kTreeMaxNodes;
 // An SM: four CTAs of 64 registers, so that 64 requests are under way at once; with draft probabilities two of 114 (40
 // trees over 151007 tokens: three of 80 registers take 1.08 times as long, four, with spills, 1.33).
 constexpr int ctas(bool drawn) { return drawn ? 2 : 4; }
-constexpr int kBatch = 4;  // pieces of a row that a lane has under way (40 drawn trees: 26.8 us, with 6 29.2, 8 29.6)
+constexpr int kBatch = 4;  // pieces of a row that a lane has under way (40 drawn trees: with 6 1.09 times as long, 8 1.10)
 
 // Values in [0, 1] (NaN and negative ones: 0, larger ones: 1).
 __device__ __forceinline__ float unit(float x) { return __saturatef(x); }
@@ -64,7 +64,7 @@ __device__ __forceinline__ void four(const float (&p)[4], const float (&q)[4], f
   for (int i = 0; i < 2; ++i) {
     const pair_t x = pair(unit(p[2 * i]), unit(p[2 * i + 1]));
     pair_t s = x, lo = 0;
-    if constexpr (kDrawn) {  // (also where A = 0 and q does not count: without a branch 26.8 us, with one 28.3)
+    if constexpr (kDrawn) {  // (also where A = 0 and q does not count: with a branch 1.06 times as long)
       const pair_t y = pair(unit(q[2 * i]), unit(q[2 * i + 1])), hi2 = pair(a_hi, a_hi);
       const pair_t m = mul(pair(-a_hi, -a_hi), y);                         // A q = -m + m_lo
       const pair_t m_lo = fma(pair(a_lo, a_lo), y, fma(hi2, y, m));
@@ -137,7 +137,8 @@ struct Row {
 
 // Piece `piece`, or 0 where it is not in front of `end`. kWhole: only pieces that lie in the row from end to end, and
 // of a q whose pieces begin where p's do: one load under a condition, so that a batch's arithmetic is one block of code
-// (40 drawn trees 30.5 -> 26.8 us; without q, where there is little of it, 11.0 us against 11.3 the other way round).
+// (40 drawn trees: with branches 1.14 times as long; without q, where there is little of it, 64 trees 11.0 us with and 11.3
+// without).
 template <bool kDrawn, bool kWhole>
 __device__ __forceinline__ void load_piece(const Row& row, bool with_q, int piece, int end, float (&p)[4], float (&q)[4]) {
 #pragma unroll
