@@ -380,12 +380,13 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
     }
     const bool ok = mbar_wait(arrived, turn >> 1 & 1, a.timeout_ns, &sm.abort);
     if (!__syncthreads_and(ok)) {
-      // The others may still send to this CTA: it stays until each of them has ended or given up as well, and for a
-      // moment more, in which what they sent arrives.
+      // The others may still send to this CTA, sums of this turn or of the next one: it stays until each of them has
+      // ended or given up as well. That does not order what they sent before, so it stays for a millisecond more,
+      // whatever its barriers say; a sum is under way for a microsecond or two.
       if (tid == 0) raise_timeout(&sm.abort, a.status);
       asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-      const int never = 0;
-      mbar_wait(arrived, turn >> 1 & 1, 1000000, &never);
+      const uint64_t since = globaltimer_ns();
+      for (int i = 0; i < 1 << 20 && globaltimer_ns() - since < 1000000; ++i) __nanosleep(500);
       return;
     }
     before = total = 0;
