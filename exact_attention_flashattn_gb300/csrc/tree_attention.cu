@@ -631,7 +631,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
       for (int run = 0; run < (turn > 0 ? 3 : 1); ++run) {
         if (run == 1) kt = s.k0, run_end = s.k0 + turn;
         if (run == 2) kt = s.k0 + plain, run_end = s.k0 + nctx;
-        const int first = kt * kKeys + my_piece;
+        // (of a run without tiles, and for a lane without copies, nothing is looked up)
+        const int first = kt < s.ct && my_piece < kKeys ? kt * kKeys + my_piece : 0;
         page = first / a.page_size, at = first - page * a.page_size;
         int row_next = pool_row(kt);
 #pragma unroll 1
@@ -761,7 +762,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
           continue;
         }
         // the tiles whose first place is in the range
-        const int at = pos - unit_at, to = whole_units ? size : min(size, at + end - pos);
+        const int at = pos - unit_at, to = whole_units ? size : min(size, end - unit_at);
         u0 = unit_at;
         pos += to - at;
         s.k0 = (max(at - P::kCost, 0) + tile_places - 1) / tile_places;
@@ -794,8 +795,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         }
         size = q.per_unit + tree_unit_cost(D);
         const int local = pos - seq_at, unit = local / size;
-        const int at = local - unit * size, to = min(size, at + end - pos);  // places of the unit
+        const int at = local - unit * size;  // places of the unit
         u0 = pos - at;
+        const int to = min(size, end - u0);
         pos += to - at;
         s.k0 = max(at - tree_unit_cost(D), 0);
         s.nt = to - tree_unit_cost(D) - s.k0;
@@ -1313,7 +1315,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
               // the infinities and NaN among the drafts (chunks: among the keys of masked tiles) that this row sees
               if constexpr (kChunk) {
                 const int* table = a.block_table + static_cast<int64_t>(s.b) * a.max_pages;
-                const int d1 = min((s.k0 + s.nt) * kKeys, limit);
+                // (the end of the last tile may be 2^31: tables hold up to 2^31 - 1 keys)
+                const int d1 = static_cast<int>(min(static_cast<int64_t>(s.k0 + s.nt) * kKeys, static_cast<int64_t>(limit)));
                 for (int x = max(s.k0 * kKeys, all_see(s)); x < d1; ++x) {
                   const int page = min(max(table[x / a.page_size], 0), a.num_pages - 1);
                   const uint16_t* v = a.v + ((static_cast<int64_t>(page) * a.page_size + x % a.page_size) * a.Hkv + s.hkv) * D + c * 32;

@@ -578,6 +578,30 @@ def test_chunk_pool_past_32_bits():
     assert torch.equal(o[:210], ref[:210])
 
 
+@pytest.mark.parametrize("d, Hq, n", [(64, 1, 2), (128, 16, 15), (256, 1, 2)])
+def test_chunk_capacity_of_31_bits(d, Hq, n):
+    # 2^31 - 48 keys, one page again and again; the last tile's end is past 31 bits. All scores are 0 and all values 1, so
+    # that every sum is of whole numbers; the last token's own value holds an infinity, the third to last's a NaN
+    page, cols = 400, 5368709
+    nk = page * cols
+    assert nk == (1 << 31) - 48
+    q = randn((n, Hq, d), gen(1))
+    k, v = torch.zeros((2, page, 1, d), dtype=torch.bfloat16, device="cuda"), torch.ones((2, page, 1, d), dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros((1, cols), dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    v[1, page - 1, 0, 5] = INF
+    v[1, page - 3, 0, 6] = NAN
+    o, lse = bw.attn_chunk_paged(q, k, v, table, i32([nk]), i32([0, n]), n)
+    see_inf, see_nan = torch.isinf(o[:, :, 5]), torch.isnan(o[:, :, 6])
+    assert bool(see_inf[-1].all()) and not bool(see_inf[:-1].any())
+    assert bool(see_nan[max(n - 3, 0):].all()) and not bool(see_nan[:max(n - 3, 0)].any())
+    o[-1, :, 5] = 1
+    o[max(n - 3, 0):, :, 6] = 1
+    assert bool((o == 1).all())
+    # the logarithm and its products, as above; 304 parts at most, of whole sums, added one by one
+    assert float((lse.double() - math.log(nk)).abs().max()) <= 2.0 ** -21 * 23 + 400 * 2.0 ** -24
+
+
 def test_chunk_thousands_of_sequences():
     r = np.random.default_rng(1)
     nq = [1] * 3000
