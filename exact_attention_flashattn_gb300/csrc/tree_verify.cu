@@ -191,11 +191,11 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
     behind = min(max(a.cu_q[b + 1], t0), a.total_q);
   }
   const int n = min(behind - t0, a.max_nodes);
-  // rows behind the last request hold no node
+  // rows behind the last request hold no node (up to 2^31 - 1 of them: a step past the last would leave 32 bits)
   if (b + 1 >= a.num_seqs)
-    for (int i = behind + rank * kThreads + tid; i < a.total_q; i += cluster * kThreads) a.accepted[i] = -1;
+    for (int64_t i = static_cast<int64_t>(behind) + rank * kThreads + tid; i < a.total_q; i += cluster * kThreads) a.accepted[i] = -1;
   if (n == 0) {  // the whole cluster leaves
-    for (int i = t0 + rank * kThreads + tid; i < behind; i += cluster * kThreads) a.accepted[i] = -1;
+    for (int64_t i = static_cast<int64_t>(t0) + rank * kThreads + tid; i < behind; i += cluster * kThreads) a.accepted[i] = -1;
     if (b < a.num_seqs && rank == 0 && tid == 0) {
       a.counts[b] = 0;
       a.next[b] = -1;
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
 
   if (rank == 0) {
     const int kept = sm.count;
-    for (int i = tid; i < behind - t0; i += kThreads) a.accepted[t0 + i] = i < kept ? t0 + sm.path[i] : -1;
+    for (int64_t i = tid; i < behind - t0; i += kThreads) a.accepted[t0 + i] = i < kept ? t0 + sm.path[i] : -1;
     if (tid == 0) {
       a.counts[b] = kept;
       if (total == 0) a.next[b] = -1;  // p has no probabilities at all

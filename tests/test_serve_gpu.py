@@ -256,6 +256,20 @@ def test_verify_limits():
     assert counts.tolist() == [0, 0] and nxt.tolist() == [-1, -1]
 
 
+def test_verify_rows_to_31_bits():
+    # 2^31 - 1 rows: behind the last request, behind the last node that is tried, of a request that may try none
+    n = (1 << 31) - 1
+    links = torch.zeros(n, dtype=torch.int32, device="cuda")  # every node has token 0 and hangs under the first
+    p = torch.ones((n, 1), device="cuda")
+    u, w = links.view(torch.float32), torch.tensor([0.5], device="cuda")  # numbers of 0
+    acc = torch.empty_like(links)
+    for last, most, kept in ((3, 3, 2), (n, 5, 2), (n - 200, 0, 0)):
+        acc.fill_(7)
+        _, counts, nxt = bw.attn_tree_verify(links, links, i32([0, last]), p, u, w, most, accepted=acc)
+        assert counts.tolist() == [kept] and nxt.tolist() == [0 if kept else -1]
+        assert acc[:kept].tolist() == list(range(kept)) and int(acc[kept:].max()) == -1 and int(acc[kept:].min()) == -1
+
+
 @pytest.mark.parametrize("drawn", [False, True])
 @pytest.mark.parametrize("requests, V", [(130, 9001), (250, 9001), (450, 9001), (900, 9001), (150, 140001), (260, 300001)])
 def test_verify_many_requests(requests, V, drawn):
