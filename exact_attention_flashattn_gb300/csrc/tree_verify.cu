@@ -98,9 +98,9 @@ __device__ __forceinline__ void send(int64_t* p, uint64_t* bar, uint32_t rank, i
       "r"(smem_u32(bar)), "r"(rank), "l"(v)
       : "memory");
 }
-// floor(w x) of a number w in [0, 1)
+// floor(w x) of a number w in [0, 1), -0 among them
 __device__ __forceinline__ int64_t part_of(float w, int64_t x) {
-  const uint32_t bits = __float_as_uint(w), e = bits >> 23;
+  const uint32_t bits = __float_as_uint(w), e = bits >> 23 & 255;
   const uint64_t m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;  // w = m 2^-down, down at least 24
   const int down = 150 - static_cast<int>(e ? e : 1);
   const uint64_t lo = m * static_cast<uint64_t>(x), hi = __umul64hi(m, static_cast<uint64_t>(x));

@@ -218,6 +218,18 @@ def test_verify_odd_inputs(drawn):
         check_verify(tokens, i32(parents), lengths, p, q if drawn else None, u, w, pad=pad, what=seed)
 
 
+def test_verify_numbers_of_minus_zero():
+    # -0 is 0: every draft that is possible is kept, and the first possible token comes behind the path
+    p = torch.zeros((2, 40), device="cuda")
+    p[0, 3] = p[0, 7] = p[1, 9] = p[1, 11] = 0.5
+    zeros, w = torch.tensor([-0.0, -0.0], device="cuda"), torch.tensor([-0.0], device="cuda")
+    for drawn in (None, p.clone()):
+        for token, path, following in ((7, [0, 1], 9), (8, [0, -1], 3)):
+            acc, counts, nxt = bw.attn_tree_verify(i32([0, token]), i32([-1, 0]), i32([0, 2]), p, zeros, w, 2, draft_probs=drawn)
+            # (a token that the draft's distribution does not have is refused, and p less that distribution is nothing: p itself)
+            assert acc.tolist() == path and nxt.tolist() == [following]
+
+
 def test_verify_nothing_left():
     V = 40
     p = torch.zeros((4, V), device="cuda")
