@@ -11,6 +11,8 @@
 // 32 bits. The coming turns' values are copied to shared memory meanwhile. 16384 rows of 32 + 8 heads of 128: 53.8 us,
 // 6.2 TB/s (weights and rotation apart, in single values: 78 us and 2400 instructions a row; a row shared by a
 // block's warps, with a barrier a row: 59.6; five blocks an SM in 96 registers: 59.7).
+#include <type_traits>
+
 #include "kernels.h"
 #include "packed.cuh"
 #include "ptx.cuh"
@@ -53,11 +55,17 @@ __device__ __forceinline__ pair_t unpack(uint32_t w) { return pair(__uint_as_flo
 __device__ __forceinline__ uint32_t pack(pair_t x) { return pack_bf16x2(first(x), second(x)); }
 __device__ __forceinline__ float bf16(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
 
+// A head's 1 / sqrt is of its sum of squares, which may pass 2^128, or vanish where eps does not hide that (a mean square
+// loses 2^-126 at most, which counts below 2^-100). Such a head's squares are taken once more, of values 2^-96 or 2^96 times
+// as large, which lie between 2^-37 and 2^51 where they count. An eps below 2^-100 has its own instances (kTiny), as what
+// the small values need there costs the others 4 % (16384 rows of 32 + 8 heads of 128: 56.3 us; the check alone 0.3).
+constexpr float kTinyEps = 0x1p-100f;
+
 // A warp takes a row's heads (or one of `gridDim.y` parts of them), kHeads a turn, and then another row's.
 constexpr int kRing = 3;        // turns that a warp has under way (16384 rows of 32 + 8 heads of 128: 53.8 us, 4 55.1, 6 57.1)
 constexpr int kRopeBlocks = 4;  // an SM
 
-template <int D, int kMode>
+template <int D, int kMode, bool kTiny>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) qk_rope_kernel(const RopeArgs a, int per_part) {
   constexpr int kLanes = D / 16, kHeads = 32 / kLanes;  // lanes a head, heads a turn
   constexpr int kWarps = kRopeThreads / 32, kMine = D / 64;  // kMine: a lane's pairs
@@ -205,6 +213,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) qk_rope_kernel(cons
             if (kMode == kHalves ? !turned : 4 * (i < 4 ? pa : pb) + (i & 3) >= a.pairs) other[i] = 0;
         }
       }
+      const int head = (is_k ? turn - q_turns : turn) * kHeads + group;
+      const bool live = head < (is_k ? a.Hkv : a.Hq);
       if (is_k ? a.k_weight : a.q_weight) {
         pair_t sum = mul(x[0], x[0]);
 #pragma unroll
@@ -212,15 +222,39 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) qk_rope_kernel(cons
         float ss = first(sum) + second(sum);
 #pragma unroll
         for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        const float v = ss * (1.f / D) + a.eps;
+        float r = rsqrtf(v);
+        if (live && !(v < INFINITY && (!kTiny || v >= kTinyEps))) {
+          const bool large = !kTiny || !(v < 1.f);
+          const float up = large ? 0x1p-96f : 0x1p96f;
+          const uint32_t* raw = reinterpret_cast<const uint32_t*>(ring + (slot == 0 ? kRing - 1 : slot - 1) * 64);
+          float y = 0.f;
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const pair_t two = unpack(raw[i < 4 ? i : 4 * 32 + i - 4]);
+            y += first(two) * up * (first(two) * up) + second(two) * up * (second(two) * up);
+          }
+          const unsigned lanes = ((1u << (kLanes - 1) << 1) - 1u) << (group * kLanes);  // the head's
+#pragma unroll
+          for (int off = kLanes / 2; off > 0; off >>= 1) y += __shfl_xor_sync(lanes, y, off);
+          r = rsqrtf(y * (1.f / D) + a.eps * up * up);
+          if constexpr (kTiny) {
+            // r times `up` may pass the largest number: the values take a share
+            const float share = large ? 0x1p-32f : 0x1p96f;
+            r *= large ? 0x1p-64f : 1.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = mul(x[i], pair(share, share)), other[i] = mul(other[i], pair(share, share));
+          } else {
+            r *= up;
+          }
+        }
         const pair_t rr = pair(r, r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = mul(x[i], rr), other[i] = mul(other[i], rr);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = fma(other[i], S[i], mul(x[i], C[i]));
-      const int head = (is_k ? turn - q_turns : turn) * kHeads + group;
-      if (head < (is_k ? a.Hkv : a.Hq)) {
+      if (live) {
         uint4* dst = reinterpret_cast<uint4*>((is_k ? a.k_out + row * a.k_out_stride : a.q_out + row * a.q_out_stride) + head * D);
         dst[pa] = make_uint4(pack(x[0]), pack(x[1]), pack(x[2]), pack(x[3]));
         dst[pb] = make_uint4(pack(x[4]), pack(x[5]), pack(x[6]), pack(x[7]));
@@ -243,9 +277,13 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
   const int blocks = (a.num_rows + kWarps - 1) / kWarps, room = kSms * kRopeBlocks / parts;
   const dim3 grid(blocks < room || room < 1 ? blocks : room, parts);
   auto go = [&](auto kernel) { return launch_dependent(kernel, grid, kRopeThreads, kWarps * kRing * 1024, stream, a, per_part); };
-  if (a.interleaved) return go(qk_rope_kernel<D, kAdjacent>);
-  if (a.pairs % 8 == 0) return go(qk_rope_kernel<D, kHalves>);
-  return go(qk_rope_kernel<D, kHalvesAny>);
+  auto go_mode = [&](auto tiny) {
+    constexpr bool kTiny = decltype(tiny)::value;
+    if (a.interleaved) return go(qk_rope_kernel<D, kAdjacent, kTiny>);
+    if (a.pairs % 8 == 0) return go(qk_rope_kernel<D, kHalves, kTiny>);
+    return go(qk_rope_kernel<D, kHalvesAny, kTiny>);
+  };
+  return a.eps < kTinyEps && (a.q_weight || a.k_weight) ? go_mode(std::true_type()) : go_mode(std::false_type());
 }
 
 }  // namespace

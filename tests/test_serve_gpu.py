@@ -408,6 +408,39 @@ def test_rope_far_positions_and_in_place():
     assert bool(torch.isnan(y[1, 1]).all()) and not bool(torch.isnan(y[0]).any() | torch.isnan(y[1, 0]).any())
 
 
+@pytest.mark.parametrize("d, Hq, Hkv, pairs, inter", [(128, 4, 2, 64, False), (128, 5, 1, 17, False), (64, 7, 2, 32, True), (256, 3, 3, 128, False), (256, 4, 1, 9, False)])
+def test_rope_norm_of_any_magnitude(d, Hq, Hkv, pairs, inter):
+    # squares that pass 2^128 and such that vanish; heads of ordinary size beside them in a turn
+    sizes = [1e-40, 1e-38, 1e-30, 1e-25, 1e-19, 1e-15, 1.0, 1e15, 1e18, 1e20, 1e30, 2e37]
+    n, g = len(sizes), gen(d)
+    w = randn((d,), g)
+    f = (100.0 ** (-torch.arange(pairs, device="cuda") / pairs)).float()
+    pos = torch.randint(0, 50, (n,), generator=g, device="cuda").to(torch.int32)
+    for eps in (0.0, 1e-35, 1e-6, 1.0, 1e30):
+        q, k = (torch.randn((n, h, d), generator=g, device="cuda", dtype=torch.float64).clamp(-4, 4) for h in (Hq, Hkv))
+        for x in (q, k):
+            for h in range(x.shape[1]):
+                x[:, h] *= torch.tensor(sizes[h:] + sizes[:h], device="cuda", dtype=torch.float64)[:, None]
+        q, k = q.to(torch.bfloat16), k.to(torch.bfloat16)
+        q[n - 1, 0] = torch.where(q[n - 1, 0] > 0, 3e38, -3e38).to(torch.bfloat16)
+        for x, y in zip((q, k), bw.attn_qk_norm_rope(q, k, pos, f, w, w, eps, interleaved=inter)):
+            x = x.double()
+            x = x / torch.sqrt(x.square().mean(-1, keepdim=True) + eps) * w.double()
+            ref, size, extra = x.clone(), x.abs(), torch.zeros_like(x)
+            for i in range(pairs):
+                a, b = (2 * i, 2 * i + 1) if inter else (i, i + pairs)
+                t = pos.double() * f[i].double()
+                c, s = torch.cos(t)[:, None], torch.sin(t)[:, None]
+                ref[..., a], ref[..., b] = x[..., a] * c - x[..., b] * s, x[..., a] * s + x[..., b] * c
+                size[..., a] = size[..., b] = x[..., a].abs() + x[..., b].abs()
+                extra[..., a] = extra[..., b] = size[..., a] * (2.0 ** -21 + 2.0 ** -51 * t.abs()[:, None])
+            dv = size * (d / 2 + 6) * 2.0 ** -24 + extra
+            tol = dv + 2.0 ** -8 * (ref.abs() + dv) + 1e-38
+            err = (y.double() - ref).abs()
+            bad = ~(err <= tol)
+            assert not bool(bad.any()), (eps, bad.any(-1).nonzero().tolist(), y[bad][:5], ref[bad][:5])
+
+
 def test_rope_axes_out_of_range_and_no_rows():
     q, f = randn((5, 2, 64), gen(1)), torch.rand(32, device="cuda")
     pos = torch.randint(0, 1000, (2, 5), device="cuda").to(torch.int32)
