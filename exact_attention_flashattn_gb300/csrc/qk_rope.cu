@@ -28,7 +28,8 @@ enum RopeMode { kHalves, kAdjacent, kHalvesAny };  // kHalvesAny: pairs no multi
 
 // A rotation's angle in turns is position * frequency / 2 pi modulo 1: with frequency / 2 pi as a fraction of 2^64
 // the product of integers wraps to just that, however far the position. The frequency's 24 bits times 1 / 2 pi
-// in 2^-64ths, shifted by its exponent: off by 2^-39 of itself and 2^-64 of a turn at most.
+// in 2^-64ths (cut off: at most 2^-61 of itself), exactly, shifted by its exponent, which cuts off at most 2^-64 of a turn. A
+// frequency of 1 at position 2^31 is so off by 2^-32 of a turn, as much as cos_sin() cuts off.
 __device__ __forceinline__ uint64_t turn_of(float freq) {
   constexpr uint64_t kInvTwoPi = 0x28be60db9391054aull;  // 1 / 2 pi, in 2^-64ths
   const uint32_t bits = __float_as_uint(freq), e = bits >> 23 & 255;
