@@ -11,6 +11,8 @@
 // 32 bits. The coming turns' values are copied to shared memory meanwhile. 16384 rows of 32 + 8 heads of 128: 53.8 us,
 // 6.2 TB/s (weights and rotation apart, in single values: 78 us and 2400 instructions a row; a row shared by a
 // block's warps, with a barrier a row: 59.6; five blocks an SM in 96 registers: 59.7).
+#include <math.h>
+
 #include <type_traits>
 
 #include "kernels.h"
@@ -28,8 +30,11 @@ enum RopeMode { kHalves, kAdjacent, kHalvesAny };  // kHalvesAny: pairs no multi
 
 // A rotation's angle in turns is position * frequency / 2 pi modulo 1: with frequency / 2 pi as a fraction of 2^64
 // the product of integers wraps to just that, however far the position. The frequency's 24 bits times 1 / 2 pi
-// in 2^-64ths (cut off: at most 2^-61 of itself), exactly, shifted by its exponent, which cuts off at most 2^-64 of a turn. A
-// frequency of 1 at position 2^31 is so off by 2^-32 of a turn, as much as cos_sin() cuts off.
+// in 2^-64ths (cut off: at most 2^-61 of itself), exactly, shifted by its exponent, which cuts off at most 2^-64 of a turn
+// (2^-63 next to a whole one, see kNoTurn). A frequency of 1 at position 2^31 is so off by 2^-32 of a turn, as much as
+// cos_sin() cuts off.
+// Infinities and NaN have no angle: kNoTurn, for which the smallest turns of either sign, 2^-64, give way to twice that.
+constexpr uint64_t kNoTurn = 1;
 __device__ __forceinline__ uint64_t turn_of(float freq) {
   constexpr uint64_t kInvTwoPi = 0x28be60db9391054aull;  // 1 / 2 pi, in 2^-64ths
   const uint32_t bits = __float_as_uint(freq), e = bits >> 23 & 255;
@@ -43,13 +48,16 @@ __device__ __forceinline__ uint64_t turn_of(float freq) {
     t = lo >> down | hi << (64 - down);
   else
     t = down < 128 ? hi >> (down - 64) : 0;
+  if (e == 255) return kNoTurn;
+  if (t == kNoTurn) t = 2;
+  if (t == 0 - kNoTurn) t = 0 - 2ull;
   return bits >> 31 ? 0 - t : t;
 }
 __device__ __forceinline__ float2 cos_sin(int position, uint64_t turn) {
   const uint64_t x = static_cast<uint64_t>(static_cast<int64_t>(position)) * turn;
   float s, c;
   sincospif(static_cast<float>(static_cast<int32_t>(x >> 32)) * 0x1p-31f, &s, &c);
-  return make_float2(c, s);
+  return turn == kNoTurn ? make_float2(NAN, NAN) : make_float2(c, s);
 }
 
 __device__ __forceinline__ pair_t unpack(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }

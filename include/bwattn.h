@@ -456,7 +456,8 @@ int attn_chunk_paged(const void* q, const void* k_pages, const void* v_pages, co
  *   k_weight     : [d] bf16 DEVICE arrays, 16-byte aligned: x_c becomes x_c * weight_c / sqrt(mean(x^2) + eps), the
  *                  mean over the head's d channels, whatever the magnitude of x (with eps = 0 a head of zeros is
  *                  0 / 0: NaN). NULL: x is not normalised
- *   inv_freq     : [pairs] fp32 DEVICE array, radians per position of each pair of channels, 0 <= pairs <= d / 2
+ *   inv_freq     : [pairs] fp32 DEVICE array, radians per position of each pair of channels, 0 <= pairs <= d / 2. A pair
+ *                  whose frequency is infinite or NaN comes out as NaN
  *   positions    : [num_axes, num_rows] int32 DEVICE array (any value, negative ones too)
  *   axes         : [pairs] int32 DEVICE array, which row of positions turns the pair (values are clamped to
  *                  [0, num_axes)), or NULL: the first

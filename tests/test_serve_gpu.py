@@ -441,6 +441,22 @@ def test_rope_norm_of_any_magnitude(d, Hq, Hkv, pairs, inter):
             assert not bool(bad.any()), (eps, bad.any(-1).nonzero().tolist(), y[bad][:5], ref[bad][:5])
 
 
+@pytest.mark.parametrize("inter, pairs", [(False, 32), (True, 20), (False, 13)])
+def test_rope_frequencies_that_are_none(inter, pairs):
+    # infinities and NaN turn their own pairs into NaN, at position 0 too, and no others
+    g = gen(pairs)
+    q, k, w = randn((6, 3, 64), g), randn((6, 1, 64), g), randn((64,), g)
+    pos, f = i32([0, 1, 5, -7, 1 << 30, 3]), torch.rand(pairs, device="cuda")
+    f[1], f[2] = 3.5e-19, -3.5e-19  # one 2^-64th of a turn a position, and a part
+    bad = f.clone()
+    bad[0], bad[4], bad[pairs - 1] = INF, NAN, -INF
+    for weight in (None, w):
+        for x, y in zip(bw.attn_qk_norm_rope(q, k, pos, f, weight, weight, interleaved=inter), bw.attn_qk_norm_rope(q, k, pos, bad, weight, weight, interleaved=inter)):
+            channels = [c for i in (0, 4, pairs - 1) for c in ((2 * i, 2 * i + 1) if inter else (i, i + pairs))]
+            others = [c for c in range(64) if c not in channels]
+            assert bool(torch.isnan(y[..., channels]).all()) and torch.equal(y[..., others], x[..., others]) and bool(torch.isfinite(x).all())
+
+
 def test_rope_axes_out_of_range_and_no_rows():
     q, f = randn((5, 2, 64), gen(1)), torch.rand(32, device="cuda")
     pos = torch.randint(0, 1000, (2, 5), device="cuda").to(torch.int32)
