@@ -23,7 +23,6 @@ namespace bw {
 
 namespace {
 
-constexpr int kSms = 152;
 constexpr int kRopeThreads = 128;
 
 enum RopeMode { kHalves, kAdjacent, kHalvesAny };  // kHalvesAny: pairs no multiple of 8
@@ -278,12 +277,16 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
   constexpr int kHeads = 512 / D, kWarps = kRopeThreads / 32;
   const int turns = (a.Hq + kHeads - 1) / kHeads + (a.Hkv + kHeads - 1) / kHeads;
   // a row's heads go to several warps where there are too few rows to fill the SMs
-  const int64_t most = kSms * kRopeBlocks * kWarps;
+  int dev = 0, sms = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  const int64_t most = sms * kRopeBlocks * kWarps;
   int parts = static_cast<int>(most / a.num_rows);
   parts = parts < 1 ? 1 : parts > turns ? turns : parts;
   const int per_part = (turns + parts - 1) / parts;
   parts = (turns + per_part - 1) / per_part;
-  const int blocks = (a.num_rows + kWarps - 1) / kWarps, room = kSms * kRopeBlocks / parts;
+  const int blocks = (a.num_rows - 1) / kWarps + 1, room = sms * kRopeBlocks / parts;
   const dim3 grid(blocks < room || room < 1 ? blocks : room, parts);
   auto go = [&](auto kernel) { return launch_dependent(kernel, grid, kRopeThreads, kWarps * kRing * 1024, stream, a, per_part); };
   auto go_mode = [&](auto tiny) {
