@@ -473,16 +473,20 @@ __global__ void __launch_bounds__(kThreads, ctas(kDrawn)) tree_verify_kernel(con
 }  // namespace
 
 cudaError_t launch_tree_verify(VerifyArgs& a, cudaStream_t stream) {
-  const cudaError_t e = status_word(&a.status);
+  cudaError_t e = status_word(&a.status);
   if (e != cudaSuccess) return e;
   a.timeout_ns = wait_timeout_ns();
+  int dev = 0, sms = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   // CTAs a request: as many as keep a warp busy with some pieces of its row, fewer where there are many requests (what
   // a CTA does beside its part of the row is the same for all: 300 trees over 65536 tokens, 8 CTAs each 27.5 us, 4 19.6, 2
-  // 16.1, 1 18.1; 100 drawn ones over 131072 36.6, 39.6, 54.1), and enough to have places for the sums of a row's groups
-  constexpr int kMostCtas = 800, kPlaces = 32 * kWarps * kMaxGroups;
-  const int pieces = a.vocab / 4 + 2;  // at most
+  // 16.1, 1 18.1; 100 drawn ones over 131072 36.6, 39.6, 54.1; 800 CTAs on 152 SMs), and enough to have places for the
+  // sums of a row's groups
+  constexpr int kPlaces = 32 * kWarps * kMaxGroups;
+  const int most_ctas = 800 * sms / 152, pieces = a.vocab / 4 + 2;  // at most
   int cluster = kMaxCluster;
-  while (cluster > 1 && (a.vocab < cluster * kWarps * 128 || a.num_seqs * cluster > kMostCtas)) cluster /= 2;
+  while (cluster > 1 && (a.vocab < cluster * kWarps * 128 || a.num_seqs * cluster > most_ctas)) cluster /= 2;
   while (pieces > cluster * kPlaces) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((a.num_seqs > 0 ? a.num_seqs : 1) * cluster));
