@@ -622,6 +622,42 @@ def test_chunk_infinities_in_later_values():
         assert bool(torch.isnan(got[140:250, 2:, 5]).all())
 
 
+SHARED = [
+    # d, Hq, Hkv, page, keys, new tokens, bound
+    (128, 8, 2, 16, [20000, 300], [200, 150], None),
+    (128, 16, 2, 16, [30000], [3], None),
+    (128, 16, 2, 64, [30000, 40], [30, 40], None),
+    (128, 16, 2, 16, [30000, 9000], [3, 1], 2000),
+    (64, 12, 4, 48, [25000, 7000], [250, 9], None),
+    (64, 2, 2, 16, [40000], [5], 900),
+    (64, 8, 2, 32, [9000], [7], None),
+    (256, 4, 2, 16, [6000, 2000], [70, 300], None),
+    (256, 8, 1, 64, [20000], [4], None),
+]
+
+
+@pytest.mark.parametrize("i", range(len(SHARED)))
+def test_chunk_infinities_in_shared_units(i):
+    d, Hq, Hkv, page, nk, nq, bound = SHARED[i]
+    c = Chunk(Hq, Hkv, d, page, nk, nq, seed=i, bound=bound)
+    ref, z = (x.clone() for x in c.run())
+    c.check(ref, z)
+    g, at = Hq // Hkv, 0
+    # the last KV head's values of some of the new tokens, in two channels
+    seen = torch.zeros_like(ref, dtype=torch.int32)  # 1: an infinity, 2: a NaN
+    for b, n in enumerate(nq):
+        for t, ch, value, mark in ((n // 3, 5, INF, 1), (n - 1, 5, NAN, 2), (n // 2, d - 3, -INF, 1)):
+            j = nk[b] - n + t
+            c.v[c.where[b][0][j], c.where[b][1][j], Hkv - 1, ch] = value
+            seen[at + t:at + n, Hq - g:, ch] |= mark
+        at += n
+    got, z2 = c.run()
+    m = sum(nq)
+    assert torch.equal(z2[:m], z[:m])
+    assert torch.equal(got[:m][seen[:m] == 0], ref[:m][seen[:m] == 0])
+    assert bool(torch.isinf(got[:m][seen[:m] == 1]).all()) and bool(torch.isnan(got[:m][seen[:m] >= 2]).all())
+
+
 def test_chunk_scale_and_caller_buffers():
     c = Chunk(8, 2, 128, 16, [300, 77], [40, 77], seed=3, pad=0)
     ref, z = c.run(scale=0.5 / math.sqrt(128))
