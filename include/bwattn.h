@@ -492,14 +492,16 @@ int attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, co
  *                  (with kv_plan_paged's slots: the `rows` of kv_append_paged)
  *   counts       : [num_seqs] int32, written: nodes of the path (0 for a request without nodes)
  *   next_tokens  : [num_seqs] int32, written: the token behind the path (-1 for a request without nodes, and
- *                  where the target's row has no probabilities at all)
+ *                  where the target's row has no probabilities above 2^-45)
  * From the root on, with p (q) the last kept node's row and r = p, S = 1, A = 0: its children are tried in the order of
  * their rows. With draft_probs, child i of token t is kept iff u_i S q(t) < r(t), else A grows by S, r becomes
  * max(p - A q, 0) and S its sum. Without, it is kept iff u_i S < r(t), else S falls by r(t) (not below 0) and r(t)
  * becomes 0. Behind the last kept node comes the first token whose running sum of r exceeds w times r's sum (of
  * p's, where r is all 0), w < 1 the request's sample_uniform. Sums are taken of values rounded to
- * 2^-44, in integers: the same whatever the launch. Supported: vocab <= 500000, max_nodes <= 1024 (further nodes
- * of a request are not tried). Strides at least vocab; outputs in an input's place or in one another's: INVALID_ARG.
+ * 2^-44, in integers: the same whatever the launch. A value up to 2^-45 so has no weight in them, and an r of such values
+ * alone counts as all 0 (the token then comes from p, refused ones among it; all of what is lost is below vocab * 2^-45,
+ * 1.5e-8 at most). Supported: vocab <= 500000, max_nodes <= 1024 (further nodes of a request are not tried). Strides at
+ * least vocab; outputs in an input's place or in one another's: INVALID_ARG.
  */
 int attn_tree_verify(const int32_t* tokens, const int32_t* parents, const int32_t* cu_seqlens_q, const float* target_probs,
                      const float* draft_probs, const float* uniforms, const float* sample_uniforms, int32_t* accepted,

@@ -230,6 +230,20 @@ def test_verify_numbers_of_minus_zero():
             assert acc.tolist() == path and nxt.tolist() == [following]
 
 
+@pytest.mark.parametrize("drawn", [False, True])
+def test_verify_values_below_the_sums_step(drawn):
+    # values are summed as multiples of 2^-44: up to half of one they have no weight, and where a refusal leaves only such
+    # ones the token comes from p itself; from 2^-45 on they are a whole one, and what is left is theirs
+    q = torch.zeros((2, 40), device="cuda")
+    q[0, 3] = 1.0
+    for small, following in ((2.0 ** -60, 3), (2.0 ** -46, 3), (2.0 ** -45, 3), (1.5 * 2.0 ** -45, 7), (2.0 ** -44, 7), (2.0 ** -30, 7)):
+        p = torch.zeros((2, 40), device="cuda")
+        p[0, 3], p[0, 7] = 0.5, small
+        acc, counts, nxt = bw.attn_tree_verify(i32([0, 3]), i32([-1, 0]), i32([0, 2]), p, torch.tensor([0.0, 0.75], device="cuda"),
+                                               torch.tensor([0.3], device="cuda"), 2, draft_probs=q if drawn else None)
+        assert counts.tolist() == [1] and acc.tolist() == [0, -1] and nxt.tolist() == [following], small
+
+
 def test_verify_nothing_left():
     V = 40
     p = torch.zeros((4, V), device="cuda")
