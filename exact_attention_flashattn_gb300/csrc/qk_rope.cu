@@ -8,9 +8,10 @@
 // A warp takes whole rows, some heads a turn: d / 16 lanes a head, each with two pieces of 8 channels that hold both
 // halves of its pairs, so rotating needs no exchange. Weights, cosines and sines are multiplied once a row: an
 // output is r (x C + other S), with r the head's 1 / sqrt and `other` the pair's other channel, in packed pairs of
-// 32 bits. The coming turns' values are copied to shared memory meanwhile. 16384 rows of 32 + 8 heads of 128: 53.8 us,
-// 6.2 TB/s (weights and rotation apart, in single values: 78 us and 2400 instructions a row; a row shared by a
-// block's warps, with a barrier a row: 59.6; five blocks an SM in 96 registers: 59.7).
+// 32 bits. The coming turns' values are copied to shared memory meanwhile. 16384 rows of 32 + 8 heads of 128: 54.4 us,
+// 6.2 TB/s, with neighbours as pairs 54.3, without norms 54.2, in place 55.5 (weights and rotation apart, in single
+// values: 78 us and 2400 instructions a row; a row shared by a block's warps, with a barrier a row: 59.6; five blocks an
+// SM in 96 registers: 61.4). Of 64 channels 28.8 us for half the bytes, 16 + 4 heads of 256 59.5; 32 pairs of 128 channels 65.3.
 #include <math.h>
 
 #include <type_traits>
@@ -66,11 +67,12 @@ __device__ __forceinline__ float bf16(uint16_t x) { return __uint_as_float(stati
 // A head's 1 / sqrt is of its sum of squares, which may pass 2^128, or vanish where eps does not hide that (a mean square
 // loses 2^-126 at most, which counts below 2^-100). Such a head's squares are taken once more, of values 2^-96 or 2^96 times
 // as large, which lie between 2^-37 and 2^51 where they count. An eps below 2^-100 has its own instances (kTiny), as what
-// the small values need there costs the others 4 % (16384 rows of 32 + 8 heads of 128: 56.3 us; the check alone 0.3).
+// the small values need there costs the others up to 5 % (16384 rows of 32 + 8 heads of 128: 57.2 us; the check for the
+// large ones 0.3, where every head of q is one 77 in all; 16 + 4 heads of 256 58.3 without it).
 constexpr float kTinyEps = 0x1p-100f;
 
 // A warp takes a row's heads (or one of `gridDim.y` parts of them), kHeads a turn, and then another row's.
-constexpr int kRing = 3;        // turns that a warp has under way (16384 rows of 32 + 8 heads of 128: 53.8 us, 4 55.1, 6 57.1)
+constexpr int kRing = 3;        // turns that a warp has under way (16384 rows of 32 + 8 heads of 128: 54.3 us, 4 54.9, 6 57.1)
 constexpr int kRopeBlocks = 4;  // an SM
 
 template <int D, int kMode, bool kTiny>
@@ -80,7 +82,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) qk_rope_kernel(cons
   __shared__ __align__(16) float sm_coef[kWarps][2][2][D];  // C and S of q's channels and of k's
   // kHalvesAny: a turn's values; a word between pieces and some between heads, so that a warp's lanes, each at the same
   // place of its piece, are in 32 banks (16384 rows of 40 heads of 128, 17 pairs: without them 101 us, with them, and
-  // second pieces left alone where they hold no pair, 78)
+  // second pieces left alone where they hold no pair, 79)
   constexpr int kHeadWords = D + D / 8 + (D == 64 ? 28 : D == 128 ? 24 : 16);
   static_assert(kHeadWords % 32 == 9 * kLanes % 32, "banks");
   __shared__ float sm_x[kMode == kHalvesAny ? kWarps : 1][kMode == kHalvesAny ? kHeads : 1][kMode == kHalvesAny ? kHeadWords : 1];

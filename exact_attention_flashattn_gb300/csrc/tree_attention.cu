@@ -43,8 +43,8 @@
 // Chunks (kChunk): the new tokens' own K and V are in the cache too, and the mask is the causal one at the sequence's
 // end, token i of nq seeing keys up to i + nk - nq. A chunk of thousands of tokens has many units, which end at their
 // own last key; the tiles that all of a unit's rows see come first, through the loops without masks, then those on the
-// diagonal. The operations bound it: 2 x 8192 tokens of 32/8 heads of 128 take 715 us, 1540 TFLOP/s (as packed K and V
-// 639), 512 tokens behind 65024 330 us, 1660 TFLOP/s. A batch mixes them with decode steps, of which a unit is one row
+// diagonal. The operations bound it: 2 x 8192 tokens of 32/8 heads of 128 take 704 us, 1560 TFLOP/s, called on end
+// 728 (as packed K and V 639), 512 tokens behind 65024 330 us, 1660 TFLOP/s, on end at the power cap 370. A batch mixes them with decode steps, of which a unit is one row
 // tile: there both streams take it (even and odd key tiles, joined through tensor memory at its end), as one stream
 // alone reads K and V at half the rate that HBM gives (40 requests, 60 % of them decode steps, 24/8 heads of 64: 238
 // -> 222 us, now 213).
@@ -141,9 +141,11 @@ __device__ __forceinline__ bool vote(bool x) { return __all_sync(0xffffffffu, x)
 
 // Places of the list that a tile takes. A batch of chunks mixes units of two row tiles with units of one (decode steps
 // among them, whose tiles are a matter of their bytes): there a tile of two row tiles takes 4 places, of one 3, or at d =
-// 64 with copies of more than 16 rows 2 (40 requests of up to 9000 keys, 60 % of them decode steps, 24/8 heads of 64:
-// 64-token pages 206 us with 2 and 217 with 3, 48-token ones, which take copies of 16 rows, 223 and 213; 32/8 heads of
-// 128, 16-token pages, up to 30000 keys: 723 with 3, 876 with 2 before both streams took such tiles).
+// 64 with copies of more than 16 rows 2. 40 requests of up to 9000 keys, 60 % of them decode steps, 24/8 heads of 64, with
+// 2 and with 3, in us: pages of 16 tokens 247 and 219, 48 (copies of 16 rows) 225 and 220, 80 (16) 223 and 219, 32 (32) 212
+// and 219, 96 (32) 208 and 218, 64 208 and 219, 128 207 and 219; 24 requests of up to 20000 keys, 32/8 heads: 16 344 and
+// 278, 48 311 and 279, 32 290 and 279, 96 277 and 278, 64 274 and 279, 128 266 and 279. 32/8 heads of 128, 16-token pages,
+// up to 30000 keys: 723 with 3, 876 with 2 before both streams took such tiles.
 template <int D, int kTiles, bool kChunk>
 struct Places {
   static constexpr int kTile = kChunk && kTiles == 2 ? 4 : 1;
@@ -340,7 +342,8 @@ struct Regs {
 struct MaskedTile {
   float m, l, alpha;
 };
-// Chunks: no mask, the row's own first `mine` keys.
+// Chunks: no mask, the row's own first `mine` keys. (Weights are rounded to bf16 as in the loop's own tiles, and for the same
+// reason; l sums them before.)
 template <bool kChunk>
 __device__ __noinline__ MaskedTile masked_tile(uint32_t tS, uint32_t tP, int left, int mine, const uint64_t* bits, int bit0, float sl2,
                                                float m_ref) {

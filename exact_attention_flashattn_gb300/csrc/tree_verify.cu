@@ -17,11 +17,12 @@
 // What bounds it: one row of p (and of q) a request, V values, and for few requests the latency of what follows one
 // another: lengths, links and tokens, their probabilities, the walk, the row, its sums, the border. A cluster of CTAs
 // takes a request, each a part of the row; all of them walk the tree alike and send one another their sums. 64 trees
-// over 131072 tokens: 11.0 us, 3.0 TB/s, of which the row takes 6 (with cluster barriers around the sums, a second
-// pass over a warp's run for the border and the walk in 64 bits: 25 us). A request whose drafts are refused one by
-// one takes a sum each, 4.8 us over 151007 tokens (1.8 of them the walk and the exchange; the rest the latency of the
-// values' arithmetic at two warps a scheduler), which 40 drawn trees' 25.9 us end with. Not faster: 512 threads a CTA,
-// rows through a deeper ring in shared memory, a cluster spread over the SMs, rows read to and fro.
+// over 131072 tokens: 13.1 us with other rows each time, from memory (2.6 TB/s), 11.0 with rows in L2, of which the row
+// takes 6 (with cluster barriers around the sums, a second pass over a warp's run for the border and the walk in 64 bits:
+// 25 us). A request whose drafts are refused one by one takes a sum each, 4.8 us over 151007 tokens (1.8 of them the walk
+// and the exchange; the rest the latency of the values' arithmetic at two warps a scheduler), which 40 drawn trees' 25.5 us
+// with rows in L2, 32.8 from memory, end with. Not faster: 512 threads a CTA, rows through a deeper ring in shared memory, a
+// cluster spread over the SMs, rows read to and fro. (Times in this file are with rows in L2 where nothing else is said.)
 #include <type_traits>
 
 #include "kernels.h"
@@ -35,7 +36,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxNodes = kTreeMaxNodes;
-// An SM: four CTAs of 64 registers, so that 64 requests are under way at once; with draft probabilities two of 114 (40
+// An SM: four CTAs of 64 registers, so that 64 requests are under way at once; with draft probabilities two of 110 (40
 // trees over 151007 tokens: three of 80 registers take 1.08 times as long, four, with spills, 1.33).
 constexpr int ctas(bool drawn) { return drawn ? 2 : 4; }
 constexpr int kBatch = 4;  // pieces of a row that a lane has under way (40 drawn trees: with 6 1.09 times as long, 8 1.10)
